@@ -12,6 +12,11 @@ Programs (flashinfer PR #8258, opening summary paragraph), shapes row-major:
     grouped_gemm_wgrad(X [M,K], G [M,N], offsets)         -> dW [E,N,K]  = G_e^T X_e
     router_gemm_fp32_bf16x3(X [M,K] fp32, Wr [N,K] fp32)  -> out [M,N] fp32
 
+Around them, for a whole expert layer: the router's selection (moe_route,
+moe_route_grad), the movement of rows (moe_dispatch, moe_combine,
+moe_combine_grad), and products in 8-bit integers (quantize_int8,
+grouped_gemm_int8, gemm_int8); `moe` puts them together.
+
 ``offsets`` is an int32 CUDA tensor: offsets[0] = 0, non-decreasing,
 offsets[E] = M; expert e owns tokens offsets[e] .. offsets[e+1]-1.
 """
@@ -19,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdrgg.so")
@@ -39,6 +45,8 @@ EXPORTS = (
     "grouped_gemm_workspace_size", "drgg_workspace_init", "drgg_plan", "drgg_wgrad_chunking",
     "drgg_tailsplit_units", "drgg_wgrad_tail_plan", "drgg_wgrad_split_plan", "grouped_gemm_wgrad_noalloc",
     "drgg_set_knob", "drgg_timing_count", "drgg_timing_read", "drgg_status_string", "drgg_abi_version",
+    "moe_route", "moe_route_workspace_size", "moe_route_grad", "moe_dispatch", "moe_combine", "moe_combine_grad",
+    "quantize_int8", "grouped_gemm_int8", "gemm_int8",
 )
 
 
@@ -138,6 +146,18 @@ def _load(path=LIB_PATH):
     lib.drgg_timing_count.restype = c_int
     lib.drgg_timing_read.argtypes = [c_int, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float)]
     lib.drgg_timing_read.restype = c_int
+    lib.moe_route.argtypes = [vp, i64, i32, i32, c_int, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_route_workspace_size.argtypes = [i64, i32, i32, ctypes.POINTER(sz)]
+    lib.moe_route_grad.argtypes = [vp, vp, vp, vp, i64, i32, i32, c_int, vp, vp]
+    lib.moe_dispatch.argtypes = [vp, vp, i64, i32, i64, c_int, vp, vp]
+    lib.moe_combine.argtypes = [vp, vp, vp, i64, i32, i64, c_int, vp, vp]
+    lib.moe_combine_grad.argtypes = [vp, vp, vp, vp, i64, i32, i64, c_int, vp, vp, vp]
+    lib.quantize_int8.argtypes = [vp, c_int, i64, i64, vp, i32, vp, vp, vp]
+    lib.grouped_gemm_int8.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, c_int, c_int, vp, vp]
+    lib.gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp]
+    for name in ("moe_route", "moe_route_workspace_size", "moe_route_grad", "moe_dispatch", "moe_combine",
+                 "moe_combine_grad", "quantize_int8", "grouped_gemm_int8", "gemm_int8"):
+        getattr(lib, name).restype = c_int
     lib.drgg_status_string.argtypes = [c_int]
     lib.drgg_status_string.restype = ctypes.c_char_p
     lib.drgg_abi_version.argtypes = []
@@ -405,9 +425,9 @@ def _workspace(device, nbytes, workspace, deterministic, kind="wgrad", stream=No
         # keyed by the program that runs (`deterministic` here: whether the
         # deterministic program runs): a non-deterministic call routed to it
         # shares its buffer of partials, the split program has its own,
-        # zeroed one; the data gradient's W^T and the router's reduction
-        # slices have their own
-        prog = kind if kind in ("dgrad", "router") else bool(deterministic)
+        # zeroed one; the data gradient's W^T, the router's reduction slices
+        # and the selection's counts have their own
+        prog = kind if kind in ("dgrad", "router", "route") else bool(deterministic)
         key = (str(device), s.cuda_stream, prog)
         if key not in _default_ws:
             _default_ws[key] = Workspace(device)
@@ -687,6 +707,211 @@ def workspace_init(buf, stream=None):
     """Zero a workspace tensor with the library's fill kernel."""
     _check(lib.drgg_workspace_init(buf.data_ptr(), buf.numel() * buf.element_size(),
                                    _stream(buf.device, stream)), "drgg_workspace_init")
+
+
+# ---- the operators around the grouped products ---------------------------------
+
+class Routing(NamedTuple):
+    """What moe_route returns."""
+    experts: "torch.Tensor"         # [T, k] int32, largest logit first
+    weights: "torch.Tensor"         # [T, k] float32
+    group_offsets: "torch.Tensor"   # [E+1] int32, as the grouped products take them
+    positions: "torch.Tensor"       # [T, k] int32, each pair's row in the grouped order
+
+
+def route_workspace_size(T: int, E: int, k: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.moe_route_workspace_size(T, E, k, ctypes.byref(n)), "moe_route_workspace_size")
+    return n.value
+
+
+def moe_route(logits, k, renormalize=True, workspace=None, stream=None):
+    """The k largest of each token's router logits [T, E] (FP32; ties to the
+    lowest index), their softmax weights (over the chosen, or over all experts
+    with renormalize=False), and the stable grouping of the T*k pairs by
+    expert, as a Routing.  A masked (-inf) logit gets weight 0, also when all
+    of a token's are."""
+    torch = _torch()
+    _need(logits, torch.float32, "logits", 2)
+    T, E = logits.shape
+    k, dev = int(k), logits.device
+    nbytes = route_workspace_size(T, E, k)
+    experts = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    positions = torch.empty((T, k), dtype=torch.int32, device=dev)
+    with _on_one_device(stream, logits):
+        ws_ptr, ws_bytes = _workspace(dev, nbytes, workspace, True, kind="route", stream=stream) if nbytes else (None, 0)
+        st = lib.moe_route(logits.data_ptr(), T, E, k, int(bool(renormalize)), experts.data_ptr(), weights.data_ptr(),
+                           offsets.data_ptr(), positions.data_ptr(), ws_ptr, ws_bytes, _stream(dev, stream))
+    _check(st, "moe_route")
+    return Routing(experts, weights, offsets, positions)
+
+
+def moe_route_grad(dweights, logits, experts, weights, renormalize=True, out=None, stream=None):
+    """dlogits [T, E] from the gradient of moe_route's weights."""
+    torch = _torch()
+    _need(logits, torch.float32, "logits", 2)
+    T, E = logits.shape
+    _need(experts, torch.int32, "experts", 2)
+    k = experts.shape[1]
+    _need_pairs(experts, T, k, torch.int32, "experts")
+    _need_pairs(weights, T, k, torch.float32, "weights")
+    _need_pairs(dweights, T, k, torch.float32, "dweights")
+    out = _out_rows2(out, (T, E), torch.float32, logits.device)
+    with _on_one_device(stream, logits, dweights, experts, weights, out):
+        st = lib.moe_route_grad(dweights.data_ptr(), logits.data_ptr(), experts.data_ptr(), weights.data_ptr(), T, E, k,
+                                int(bool(renormalize)), out.data_ptr(), _stream(logits.device, stream))
+    _check(st, "moe_route_grad")
+    return out
+
+
+def _need_pairs(t, T, k, dtype, name):
+    _need(t, dtype, name, 2)
+    if tuple(t.shape) != (T, k):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, k)}")
+
+
+def _out_rows2(out, shape, dtype, device, name="out"):
+    if out is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    _need(out, dtype, name, len(shape))
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} has the wrong shape")
+    return out
+
+
+def _row_code(t, name):
+    """The dtype code of a contiguous 2-d row tensor, BF16 or FP32."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
+    _need(t, t.dtype, name, 2)
+    return BF16 if t.dtype == torch.bfloat16 else FP32
+
+
+def moe_dispatch(X, positions, out=None, stream=None):
+    """Rows in the grouped order: out[positions[t, j]] = X[t] for X [T, H]
+    (BF16 or FP32, H a multiple of 8); out [T*k, H]."""
+    torch = _torch()
+    code = _row_code(X, "X")
+    T, H = X.shape
+    _need(positions, torch.int32, "positions", 2)
+    k = positions.shape[1]
+    _need_pairs(positions, T, k, torch.int32, "positions")
+    out = _out_rows2(out, (T * k, H), X.dtype, X.device)
+    with _on_one_device(stream, X, positions, out):
+        st = lib.moe_dispatch(X.data_ptr(), positions.data_ptr(), T, k, H, code, out.data_ptr(),
+                              _stream(X.device, stream))
+    _check(st, "moe_dispatch")
+    return out
+
+
+def moe_combine(rows, positions, weights=None, out=None, stream=None):
+    """Rows back in token order: out[t] = sum_j weights[t, j] *
+    rows[positions[t, j]] (FP32 sum, one rounding to the rows' dtype).  Without
+    weights this is the gradient of moe_dispatch."""
+    torch = _torch()
+    code = _row_code(rows, "rows")
+    R, H = rows.shape
+    _need(positions, torch.int32, "positions", 2)
+    T, k = positions.shape
+    if R != T * k:
+        raise ValueError(f"rows has {R} rows, positions {T} x {k}")
+    if weights is not None:
+        _need_pairs(weights, T, k, torch.float32, "weights")
+    out = _out_rows2(out, (T, H), rows.dtype, rows.device)
+    with _on_one_device(stream, rows, positions, weights, out):
+        st = lib.moe_combine(rows.data_ptr(), positions.data_ptr(), weights.data_ptr() if weights is not None else None,
+                             T, k, H, code, out.data_ptr(), _stream(rows.device, stream))
+    _check(st, "moe_combine")
+    return out
+
+
+def moe_combine_grad(dout, rows, positions, weights, stream=None):
+    """Gradients of the weighted moe_combine: (drows [T*k, H] in the rows'
+    dtype, dweights [T, k] FP32)."""
+    torch = _torch()
+    code = _row_code(rows, "rows")
+    R, H = rows.shape
+    _need(positions, torch.int32, "positions", 2)
+    T, k = positions.shape
+    if R != T * k:
+        raise ValueError(f"rows has {R} rows, positions {T} x {k}")
+    _need_pairs(weights, T, k, torch.float32, "weights")
+    _need(dout, rows.dtype, "dout", 2)
+    if tuple(dout.shape) != (T, H):
+        raise ValueError(f"dout has shape {tuple(dout.shape)}, expected {(T, H)}")
+    drows, dweights = torch.empty_like(rows), torch.empty_like(weights)
+    with _on_one_device(stream, dout, rows, positions, weights):
+        st = lib.moe_combine_grad(dout.data_ptr(), rows.data_ptr(), positions.data_ptr(), weights.data_ptr(), T, k, H,
+                                  code, drows.data_ptr(), dweights.data_ptr(), _stream(rows.device, stream))
+    _check(st, "moe_combine_grad")
+    return drows, dweights
+
+
+def quantize_int8(X, positions=None, stream=None):
+    """Codes and scales of the rows of X [T, K] (BF16 or FP32, K a multiple of
+    16): (q int8 [T, K], scale FP32 [T]).  With positions [T, k] each token's
+    codes go to its k rows of the grouped order: q [T*k, K], scale [T*k]."""
+    torch = _torch()
+    code = _row_code(X, "X")
+    T, K = X.shape
+    k = 1
+    if positions is not None:
+        _need(positions, torch.int32, "positions", 2)
+        k = positions.shape[1]
+        _need_pairs(positions, T, k, torch.int32, "positions")
+    q = torch.empty((T * k, K), dtype=torch.int8, device=X.device)
+    scale = torch.empty((T * k,), dtype=torch.float32, device=X.device)
+    with _on_one_device(stream, X, positions):
+        st = lib.quantize_int8(X.data_ptr(), code, T, K, positions.data_ptr() if positions is not None else None, k,
+                               q.data_ptr(), scale.data_ptr(), _stream(X.device, stream))
+    _check(st, "quantize_int8")
+    return q, scale
+
+
+def _int8_operands(Xq, x_scale, Wq, w_scale, wdim, gated, out_dtype, out):
+    torch = _torch()
+    _need(Xq, torch.int8, "Xq", 2)
+    _need(Wq, torch.int8, "Wq", wdim)
+    _need(x_scale, torch.float32, "x_scale", 1)
+    _need(w_scale, torch.float32, "w_scale", wdim - 1)
+    M, K = Xq.shape
+    N = Wq.shape[-2]
+    if Wq.shape[-1] != K or x_scale.shape[0] != M or w_scale.shape != Wq.shape[:-1]:
+        raise ValueError(f"shape mismatch: Xq {tuple(Xq.shape)}, x_scale {tuple(x_scale.shape)}, "
+                         f"Wq {tuple(Wq.shape)}, w_scale {tuple(w_scale.shape)}")
+    code = _dtype_code(out_dtype if out_dtype is not None else torch.bfloat16)
+    out = _out_rows2(out, (M, N // 2 if gated else N), _torch_dtype(code), Xq.device)
+    return M, N, K, code, out
+
+
+def grouped_gemm_int8(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, out_dtype=None, out=None, stream=None):
+    """Y[t] = x_scale[t] * w_scale[e(t)] * (Xq[t] Wq[e(t)]^T) for int8 codes Xq
+    [M, K], Wq [E, N, K] and FP32 scales [M], [E, N]: an exact integer sum,
+    scaled in FP32 and rounded once to out_dtype (bf16 by default).  gated:
+    the N = 2I columns are gate and up halves, and Y [M, I] = silu(gate) * up."""
+    E = _offsets(group_offsets)
+    M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 3, gated, out_dtype, out)
+    if Wq.shape[0] != E:
+        raise ValueError(f"shape mismatch: Wq {tuple(Wq.shape)}, E={E}")
+    with _on_one_device(stream, Xq, x_scale, Wq, w_scale, group_offsets, out):
+        st = lib.grouped_gemm_int8(Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(),
+                                   group_offsets.data_ptr(), E, M, N, K, int(bool(gated)), code, out.data_ptr(),
+                                   _stream(Xq.device, stream))
+    _check(st, "grouped_gemm_int8")
+    return out
+
+
+def gemm_int8(Xq, x_scale, Wq, w_scale, gated=False, out_dtype=None, out=None, stream=None):
+    """The one-group case of grouped_gemm_int8: Wq [N, K], w_scale [N]."""
+    M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 2, gated, out_dtype, out)
+    with _on_one_device(stream, Xq, x_scale, Wq, w_scale, out):
+        st = lib.gemm_int8(Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(), M, N, K,
+                           int(bool(gated)), code, out.data_ptr(), _stream(Xq.device, stream))
+    _check(st, "gemm_int8")
+    return out
 
 
 if os.environ.get("DRGG_NO_ROUTES", "0") in ("", "0"):

@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdrgg.so")
-SOURCES = ["api.cpp", "kernels.hip"]
+SOURCES = ["api.cpp", "api_moe.cpp", "kernels.hip", "moe.hip", "int8.hip"]
 ARCH = os.environ.get("DRGG_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

@@ -37,30 +37,24 @@ bool env_flag(const char* name) {
     const char* v = std::getenv(name);
     return v && *v && std::strcmp(v, "0") != 0;
 }
-bool checks_offsets() { return g_knob_check_offsets.load() != 0 || env_flag("DRGG_CHECK_OFFSETS"); }
 bool checks_workspace() { return g_knob_check_ws.load() != 0 || env_flag("DRGG_CHECK_WORKSPACE"); }
 
-constexpr int64_t kMaxBytes = (int64_t)1 << 62;
 constexpr int kMaxDevices = 64;
-
-// checked a * b for non-negative operands
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > kMaxBytes / a) return false;
-    *out = a * b;
-    return true;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The HIP error behind this thread's most recent DRGG_EDEVICE (its text is
 // appended to drgg_status_string(DRGG_EDEVICE)).
 thread_local hipError_t g_last_hip_error = hipSuccess;
 
+}  // namespace
+
 drgg_status device_error(hipError_t e) {
     g_last_hip_error = e;
     return DRGG_EDEVICE;
 }
+
+bool checks_offsets() { return g_knob_check_offsets.load() != 0 || env_flag("DRGG_CHECK_OFFSETS"); }
+
+namespace {
 
 // CU count of the current device, cached per device.
 drgg_status current_cu_count(int* cus) {
@@ -233,7 +227,7 @@ drgg_status make_plan(drgg_op op, int32_t E, int64_t M, int64_t N, int64_t K, in
     return DRGG_OK;
 }
 
-drgg_status launch_status(hipError_t e) { return e == hipSuccess ? DRGG_OK : device_error(e); }
+}  // namespace
 
 // Debug check of the group offsets (DRGG_CHECK_OFFSETS): a synchronous copy
 // to the host, then o[0] = 0, non-decreasing, o[E] = M, else DRGG_ESHAPE.
@@ -248,6 +242,8 @@ drgg_status check_offsets_sync(const int32_t* offs, int32_t E, int64_t M, hipStr
         if (h[(size_t)i + 1] < h[(size_t)i]) return DRGG_ESHAPE;
     return DRGG_OK;
 }
+
+namespace {
 
 // Debug check of the split program's workspace (DRGG_CHECK_WORKSPACE): its
 // tile sums and tickets must be zero before a call (a buffer that served a

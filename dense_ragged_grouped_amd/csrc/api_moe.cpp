@@ -1,0 +1,169 @@
+// api_moe.cpp -- the C ABI of the operators around the grouped products
+// (declared in include/drgg.h): the router's selection, the movement of rows,
+// and the 8-bit integer products.  Argument checks in checked 64-bit
+// arithmetic, then launches (moe.hip, int8.hip) on the caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/drgg.h"
+#include "internal.hpp"
+#include "plan.hpp"
+
+namespace drgg {
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+drgg_status check_pairs(int64_t T, int32_t k) {
+    int64_t r;
+    if (k < 1 || k > 64) return DRGG_EINVAL;
+    if (T < 0 || !mul_ok(T, k, &r) || r > INT32_MAX) return DRGG_ESHAPE;
+    return DRGG_OK;
+}
+
+drgg_status check_route(int64_t T, int32_t E, int32_t k) {
+    if (E < 1 || E > kMaxExperts || k > E) return DRGG_EINVAL;
+    return check_pairs(T, k);
+}
+
+size_t route_table_bytes(int64_t T, int32_t E) {
+    const int64_t blocks = route_blocks(T);
+    return blocks > 1 ? (size_t)((blocks + 1) * E * 4) : 0;   // at most 2^25 blocks of 1024 experts
+}
+
+drgg_status check_rows(int64_t T, int32_t k, int64_t H, drgg_dtype dt) {
+    if (dt != DRGG_BF16 && dt != DRGG_FP32) return DRGG_EINVAL;
+    drgg_status st = check_pairs(T, k);
+    if (st != DRGG_OK) return st;
+    if (H < 8 || H > (1 << 22)) return DRGG_ESHAPE;
+    return H % 8 ? DRGG_EALIGN : DRGG_OK;
+}
+
+drgg_status run_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, const float* w_scale,
+                     const int32_t* offs, int32_t E, int64_t M, int64_t N, int64_t K, int gated, drgg_dtype dt, void* Y,
+                     hipStream_t s) {
+    if (E < 1 || E > kMaxExperts) return DRGG_EINVAL;
+    if (dt != DRGG_BF16 && dt != DRGG_FP32) return DRGG_EINVAL;
+    const int64_t na = gated ? 16 : 8;
+    if (M < 0 || M > INT32_MAX || N < na || N > (1 << 22) || K < 16 || K > kInt8MaxK) return DRGG_ESHAPE;
+    if (N % na || K % 16) return DRGG_EALIGN;
+    if (!Wq || !w_scale || (M > 0 && (!Xq || !x_scale || !Y))) return DRGG_EINVAL;
+    if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || !aligned16(w_scale) || !aligned4(x_scale) ||
+        !aligned4(offs))
+        return DRGG_EALIGN;
+    if (offs && checks_offsets()) {
+        drgg_status st = check_offsets_sync(offs, E, M, s);
+        if (st != DRGG_OK) return st;
+    }
+    if (M == 0) return DRGG_OK;
+    Int8Args a{Xq, Wq, x_scale, w_scale, offs, Y, M, N, K, E};
+    return launch_status(launch_int8(a, gated != 0, dt == DRGG_BF16, s));
+}
+
+}  // namespace
+}  // namespace drgg
+
+using namespace drgg;
+
+extern "C" {
+
+drgg_status moe_route_workspace_size(int64_t T, int32_t E, int32_t k, size_t* bytes) {
+    if (!bytes) return DRGG_EINVAL;
+    drgg_status st = check_route(T, E, k);
+    if (st != DRGG_OK) return st;
+    *bytes = route_table_bytes(T, E);
+    return DRGG_OK;
+}
+
+drgg_status moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
+                      float* weights, int32_t* group_offsets, int32_t* positions, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+    drgg_status st = check_route(T, E, k);
+    if (st != DRGG_OK) return st;
+    if (!group_offsets || (T > 0 && (!logits || !experts || !weights || !positions))) return DRGG_EINVAL;
+    if (!aligned16(logits) || !aligned4(experts) || !aligned4(weights) || !aligned4(group_offsets) ||
+        !aligned4(positions))
+        return DRGG_EALIGN;
+    const size_t need = route_table_bytes(T, E);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return DRGG_EWORKSPACE;
+        if (!aligned16(workspace)) return DRGG_EALIGN;
+    }
+    return launch_status(launch_moe_route(logits, T, E, k, renormalize != 0, experts, weights, group_offsets, positions,
+                                          static_cast<int32_t*>(workspace), stream));
+}
+
+drgg_status moe_route_grad(const float* dweights, const float* logits, const int32_t* experts, const float* weights,
+                           int64_t T, int32_t E, int32_t k, int renormalize, float* dlogits, hipStream_t stream) {
+    drgg_status st = check_route(T, E, k);
+    if (st != DRGG_OK) return st;
+    if (T > 0 && (!dweights || !logits || !experts || !weights || !dlogits)) return DRGG_EINVAL;
+    if (!aligned16(logits) || !aligned16(dlogits) || !aligned4(dweights) || !aligned4(experts) || !aligned4(weights))
+        return DRGG_EALIGN;
+    if (T == 0) return DRGG_OK;
+    return launch_status(
+        launch_moe_route_grad(dweights, logits, experts, weights, T, E, k, renormalize != 0, dlogits, stream));
+}
+
+drgg_status moe_dispatch(const void* X, const int32_t* positions, int64_t T, int32_t k, int64_t H, drgg_dtype dtype,
+                         void* rows, hipStream_t stream) {
+    drgg_status st = check_rows(T, k, H, dtype);
+    if (st != DRGG_OK) return st;
+    if (T > 0 && (!X || !positions || !rows)) return DRGG_EINVAL;
+    if (!aligned16(X) || !aligned16(rows) || !aligned4(positions)) return DRGG_EALIGN;
+    if (T == 0) return DRGG_OK;
+    return launch_status(launch_moe_dispatch(X, positions, T, k, H, dtype == DRGG_BF16, rows, stream));
+}
+
+drgg_status moe_combine(const void* rows, const int32_t* positions, const float* weights, int64_t T, int32_t k,
+                        int64_t H, drgg_dtype dtype, void* out, hipStream_t stream) {
+    drgg_status st = check_rows(T, k, H, dtype);
+    if (st != DRGG_OK) return st;
+    if (T > 0 && (!rows || !positions || !out)) return DRGG_EINVAL;
+    if (!aligned16(rows) || !aligned16(out) || !aligned4(positions) || !aligned4(weights)) return DRGG_EALIGN;
+    if (T == 0) return DRGG_OK;
+    return launch_status(launch_moe_combine(rows, positions, weights, T, k, H, dtype == DRGG_BF16, out, stream));
+}
+
+drgg_status moe_combine_grad(const void* dout, const void* rows, const int32_t* positions, const float* weights,
+                             int64_t T, int32_t k, int64_t H, drgg_dtype dtype, void* drows, float* dweights,
+                             hipStream_t stream) {
+    drgg_status st = check_rows(T, k, H, dtype);
+    if (st != DRGG_OK) return st;
+    if (T > 0 && (!dout || !rows || !positions || !weights || !drows || !dweights)) return DRGG_EINVAL;
+    if (!aligned16(dout) || !aligned16(rows) || !aligned16(drows) || !aligned4(positions) || !aligned4(weights) ||
+        !aligned4(dweights))
+        return DRGG_EALIGN;
+    if (T == 0) return DRGG_OK;
+    return launch_status(launch_moe_combine_grad(dout, rows, positions, weights, T, k, H, dtype == DRGG_BF16, drows,
+                                                 dweights, stream));
+}
+
+drgg_status quantize_int8(const void* X, drgg_dtype dtype, int64_t T, int64_t K, const int32_t* positions, int32_t k,
+                          int8_t* q, float* scale, hipStream_t stream) {
+    if (dtype != DRGG_BF16 && dtype != DRGG_FP32) return DRGG_EINVAL;
+    if (!positions && k != 1) return DRGG_EINVAL;
+    drgg_status st = check_pairs(T, k);
+    if (st != DRGG_OK) return st;
+    if (K < 16 || K > (1 << 22)) return DRGG_ESHAPE;
+    if (K % 16) return DRGG_EALIGN;
+    if (T > 0 && (!X || !q || !scale)) return DRGG_EINVAL;
+    if (!aligned16(X) || !aligned16(q) || !aligned4(scale) || !aligned4(positions)) return DRGG_EALIGN;
+    if (T == 0) return DRGG_OK;
+    return launch_status(launch_quantize_int8(X, dtype == DRGG_BF16, T, K, positions, k, q, scale, stream));
+}
+
+drgg_status grouped_gemm_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, const float* w_scale,
+                              const int32_t* group_offsets, int32_t E, int64_t M, int64_t N, int64_t K, int gated,
+                              drgg_dtype out_dtype, void* Y, hipStream_t stream) {
+    if (!group_offsets) return DRGG_EINVAL;
+    return run_int8(Xq, x_scale, Wq, w_scale, group_offsets, E, M, N, K, gated, out_dtype, Y, stream);
+}
+
+drgg_status gemm_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, const float* w_scale, int64_t M,
+                      int64_t N, int64_t K, int gated, drgg_dtype out_dtype, void* Y, hipStream_t stream) {
+    return run_int8(Xq, x_scale, Wq, w_scale, nullptr, 1, M, N, K, gated, out_dtype, Y, stream);
+}
+
+}  // extern "C"

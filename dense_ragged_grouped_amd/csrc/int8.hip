@@ -1,0 +1,236 @@
+// int8.hip -- gfx950 (CDNA4) kernels of the 8-bit integer products:
+//
+//   quantisation   s = max|x| / 127,  q = round(127 x / max|x|)   per row
+//   product        Y[t,n] = xs[t] ws[e,n] sum_k Xq[t,k] Wq[e,n,k]
+//   gated product  Y[t,i] = silu(g) u,  g, u = columns i and N/2 + i of the product
+//
+// The sum is an exact 32-bit integer (K <= kInt8MaxK), so no order or split
+// of it changes a result; it is scaled in FP32 and rounded once.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "internal.hpp"
+#include "plan.hpp"
+
+namespace drgg {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
+// ---------------------------------------------------------------------------
+// quantisation
+//
+// 16 values of a row per thread and step (16-byte code stores).  127 x is
+// exact for BF16 x, so that x = max|x| / 2 is a true tie (63.5, to 64); the
+// division is the correctly rounded one.  Rows whose largest value is beyond
+// 2^120 are scaled by 2^-8 first (exact), so that 127 x stays finite.  A row
+// that holds an infinity or NaN gets scale NaN and codes 0: every product
+// with it is NaN, and no other row's is.
+
+struct QuantArgs {
+    const void* X;
+    const int32_t* positions;   // null: row t stays row t
+    int8_t* q;
+    float* scale;
+    int64_t T, C;               // C: groups of 16 values per row
+    int32_t k;
+};
+
+template <bool BF16>
+__device__ __forceinline__ void load16(float (&f)[16], const void* X, int64_t i) {
+    if constexpr (BF16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const u32x4 v = reinterpret_cast<const u32x4*>(X)[2 * i + h];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                f[8 * h + 2 * r] = __uint_as_float(v[r] << 16);
+                f[8 * h + 2 * r + 1] = __uint_as_float(v[r] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const f32x4 v = reinterpret_cast<const f32x4*>(X)[4 * i + h];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[4 * h + r] = v[r];
+        }
+    }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
+    __shared__ uint32_t part[4];
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool live = t < a.T;
+    // the largest magnitude as bits: their unsigned order is the order of the
+    // magnitudes, with infinity and NaN above every finite value
+    uint32_t m = 0;
+    if (live)
+        for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
+            float f[16];
+            load16<BF16>(f, a.X, t * a.C + c);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+        }
+    const int width = blockDim.x < 64 ? blockDim.x : 64;
+    for (int d = 1; d < width; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+    if (blockDim.x > 64) {
+        const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+        if ((tid & 63) == 0) part[tid >> 6] = m;
+        __syncthreads();
+        const int w0 = threadIdx.y * (blockDim.x / 64);
+        for (unsigned w = 0; w < blockDim.x / 64; ++w) m = max(m, part[w0 + w]);
+    }
+    if (!live) return;
+    const bool bad = m >= 0x7F800000u;
+    const float most = __uint_as_float(m);
+    const float scale = bad ? __uint_as_float(0x7FC00000u) : most / 127.f;
+    const float down = most > 0x1p120f ? 0x1p-8f : 1.f;
+    const float by = bad || m == 0 ? 1.f : most * down;
+    const int64_t R = a.T * a.k;
+    for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
+        float f[16];
+        load16<BF16>(f, a.X, t * a.C + c);
+        u32x4 out;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int q = bad ? 0 : (int)rintf(f[4 * h + r] * down * 127.f / by);
+                v |= (uint32_t)(q & 0xFF) << (8 * r);
+            }
+            out[h] = v;
+        }
+        for (int j = 0; j < a.k; ++j) {
+            const int64_t p = a.positions ? a.positions[t * a.k + j] : t;
+            if (p < 0 || p >= R) continue;
+            reinterpret_cast<u32x4*>(a.q)[p * a.C + c] = out;
+            if (c == 0) a.scale[p] = scale;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// product, few rows per group
+//
+// A workgroup takes 32 weight rows of one group (gated: 16 gate rows and
+// their 16 up rows) and the group's token rows in blocks of 16; its four
+// waves split K in steps of 64 values and add their integer sums through
+// LDS.  Fragments go from memory to registers directly: lane l of a
+// v_mfma_i32_16x16x64_i8 holds values 16*(l/16) .. +15 of row l%16, one
+// 16-byte load, for the weights (first operand) as for the tokens; the result
+// has token l%16 and weight rows 4*(l/16) .. +3 in lane l.
+
+template <bool OUT_BF16, bool GATED>
+__global__ __launch_bounds__(256) void int8_rows_kernel(Int8Args a) {
+    __shared__ i32x4 sums[4][2][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    const int e = blockIdx.y;
+    int64_t lo = 0, hi = a.M;
+    if (a.offs) {
+        lo = min<int64_t>(max<int64_t>(a.offs[e], 0), a.M);
+        hi = min<int64_t>(max<int64_t>(a.offs[e + 1], lo), a.M);
+    }
+    if (lo >= hi) return;
+    const int64_t NO = GATED ? a.N / 2 : a.N;   // output columns
+    constexpr int kCols = GATED ? 16 : 32;      // of them per workgroup
+    const int64_t n0 = (int64_t)blockIdx.x * kCols;
+    // weight rows of the two blocks of 16; rows past the end repeat the last
+    // one, and their results are not stored
+    const int64_t nb0 = min(n0 + r, NO - 1);
+    const int64_t nb1 = GATED ? NO + nb0 : min(n0 + 16 + r, NO - 1);
+    const int8_t* w0 = a.W + ((int64_t)e * a.N + nb0) * a.K;
+    const int8_t* w1 = a.W + ((int64_t)e * a.N + nb1) * a.K;
+    for (int64_t m0 = lo; m0 < hi; m0 += 16) {
+        const int8_t* x = a.X + min(m0 + r, hi - 1) * a.K;
+        i32x4 acc0 = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
+        for (int64_t k0 = wave * 64; k0 < a.K; k0 += 256) {
+            const int64_t k = k0 + 16 * g;
+            i32x4 b = {0, 0, 0, 0}, v0 = b, v1 = b;
+            if (k < a.K) {
+                b = *reinterpret_cast<const i32x4*>(x + k);
+                v0 = *reinterpret_cast<const i32x4*>(w0 + k);
+                v1 = *reinterpret_cast<const i32x4*>(w1 + k);
+            }
+            acc0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(v0, b, acc0, 0, 0, 0);
+            acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(v1, b, acc1, 0, 0, 0);
+        }
+        sums[wave][0][lane] = acc0;
+        sums[wave][1][lane] = acc1;
+        __syncthreads();
+        const int64_t t = m0 + r;
+        if (wave < (GATED ? 1 : 2) && t < hi) {
+            const float xs = a.xs[t];
+            const int64_t n = n0 + 16 * wave + 4 * g;
+            float y[4];
+            i32x4 c0 = sums[0][wave][lane], c1 = sums[0][1][lane];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+                c0 += sums[w][wave][lane];
+                c1 += sums[w][1][lane];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t ni = min(n + i, NO - 1);
+                y[i] = (float)c0[i] * a.ws[(int64_t)e * a.N + ni] * xs;
+                if constexpr (GATED) {
+                    const float u = (float)c1[i] * a.ws[(int64_t)e * a.N + NO + ni] * xs;
+                    y[i] = y[i] / (1.f + expf(-y[i])) * u;
+                }
+            }
+            if (n < NO) {   // NO is a multiple of 4
+                if constexpr (OUT_BF16)
+                    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + t * NO + n) =
+                        u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+                else
+                    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + t * NO + n) =
+                        f32x4{y[0], y[1], y[2], y[3]};
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, const int32_t* positions, int32_t k,
+                                int8_t* q, float* scale, hipStream_t s) {
+    QuantArgs a{X, positions, q, scale, T, K / 16, k};
+    unsigned x = 1;
+    while (x < 256 && x < a.C) x *= 2;
+    const dim3 block(x, 256 / x), grid((unsigned)ceil_div(T, block.y));
+    timing_mark("quantize_int8_kernel", s);
+    if (bf16) hipLaunchKernelGGL(quantize_int8_kernel<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(quantize_int8_kernel<false>, grid, block, 0, s, a);
+    timing_end(s);
+    return hipGetLastError();
+}
+
+hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, hipStream_t s) {
+    const dim3 grid((unsigned)ceil_div(gated ? a.N / 2 : a.N, gated ? 16 : 32), (unsigned)a.E), block(256);
+    timing_mark("int8_rows_kernel", s);
+    if (gated) {
+        if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((int8_rows_kernel<false, true>), grid, block, 0, s, a);
+    } else {
+        if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, false>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((int8_rows_kernel<false, false>), grid, block, 0, s, a);
+    }
+    timing_end(s);
+    return hipGetLastError();
+}
+
+}  // namespace drgg

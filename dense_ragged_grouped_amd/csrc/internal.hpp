@@ -1,5 +1,6 @@
-// internal.hpp -- declarations shared by the C ABI (api.cpp) and the kernel
-// launchers (kernels.hip).  Not part of the public interface.
+// internal.hpp -- declarations shared by the C ABI (api.cpp, api_moe.cpp) and
+// the kernel launchers (kernels.hip, moe.hip, int8.hip).  Not part of the
+// public interface.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -7,7 +8,31 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "../../include/drgg.h"
+
 namespace drgg {
+
+// ---- argument checks shared by the C ABI's files ---------------------------
+
+constexpr int64_t kMaxBytes = (int64_t)1 << 62;
+
+// checked a * b for non-negative operands
+inline bool mul_ok(int64_t a, int64_t b, int64_t* out) {
+    if (a < 0 || b < 0) return false;
+    if (a != 0 && b > kMaxBytes / a) return false;
+    *out = a * b;
+    return true;
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// DRGG_EDEVICE, with the HIP error kept for drgg_status_string (api.cpp)
+drgg_status device_error(hipError_t e);
+inline drgg_status launch_status(hipError_t e) { return e == hipSuccess ? DRGG_OK : device_error(e); }
+
+// Debug check of the group offsets (api.cpp): whether it is on, and the check.
+bool checks_offsets();
+drgg_status check_offsets_sync(const int32_t* offs, int32_t E, int64_t M, hipStream_t s);
 
 // Arguments of the grouped-GEMM kernels, passed by value.
 struct GemmArgs {
@@ -54,6 +79,40 @@ hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);
 constexpr size_t kScratchBytes = size_t(64) << 20;
 hipError_t scratch_buffer(void** ptr);
 hipError_t launch_hold_cus(int n, uint64_t ticks, hipStream_t s);
+
+// ---- the expert layer's operators (moe.hip, int8.hip) -----------------------
+
+int64_t route_blocks(int64_t T);   // workgroups of the selection; its table has (blocks + 1) * E words
+hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
+                            float* weights, int32_t* offsets, int32_t* positions, int32_t* table, hipStream_t s);
+hipError_t launch_moe_route_grad(const float* dweights, const float* logits, const int32_t* experts,
+                                 const float* weights, int64_t T, int32_t E, int32_t k, int renormalize,
+                                 float* dlogits, hipStream_t s);
+hipError_t launch_moe_dispatch(const void* X, const int32_t* positions, int64_t T, int32_t k, int64_t H, bool bf16,
+                               void* rows, hipStream_t s);
+hipError_t launch_moe_combine(const void* rows, const int32_t* positions, const float* weights, int64_t T, int32_t k,
+                              int64_t H, bool bf16, void* out, hipStream_t s);
+hipError_t launch_moe_combine_grad(const void* dout, const void* rows, const int32_t* positions, const float* weights,
+                                   int64_t T, int32_t k, int64_t H, bool bf16, void* drows, float* dweights,
+                                   hipStream_t s);
+hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, const int32_t* positions, int32_t k,
+                                int8_t* q, float* scale, hipStream_t s);
+
+// Arguments of the 8-bit products: X [M,K], W [E,N,K] codes, xs [M], ws [E,N]
+// scales, offs [E+1] on the device (null: one group of all M rows).
+struct Int8Args {
+    const int8_t* X;
+    const int8_t* W;
+    const float* xs;
+    const float* ws;
+    const int32_t* offs;
+    void* out;
+    int64_t M, N, K;
+    int32_t E;
+};
+// the longest reduction whose sum fits 32 bits for any codes: 131056 * 128^2 < 2^31
+constexpr int64_t kInt8MaxK = 131056;
+hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, hipStream_t s);
 
 // Per-launch timing marks (a measurement knob, off by default): when on, an
 // event is recorded on the stream before every kernel launch of a call and

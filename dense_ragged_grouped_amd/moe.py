@@ -1,0 +1,101 @@
+"""A gated feed-forward block of E experts, put together from the package's
+operators: router logits [T, E] send each of T tokens to k experts, expert e
+maps a row x to W2_e (silu(g) * u) with (g, u) the halves of W1_e x, and the k
+results are added with the router's weights.
+
+    ffn_int8   serving: the two products in 8-bit integers
+    ffn        training: BF16 products, differentiable in the rows, the logits
+               and both weights
+
+Weights are stacked per expert, W1 [E, 2I, H] (gate rows, then up rows) and
+W2 [E, H, I].
+"""
+import torch
+
+from . import (grouped_gemm_int8, moe_combine, moe_combine_grad, moe_dispatch, moe_route, moe_route_grad,
+               quantize_int8)
+from .autograd import grouped_linear
+
+
+def quantize_weights(W):
+    """Codes and scales of stacked weights [E, N, K] (BF16 or FP32), one scale
+    per expert and output channel: (int8 [E, N, K], FP32 [E, N])."""
+    E, N, K = W.shape
+    q, scale = quantize_int8(W.reshape(E * N, K))
+    return q.view(E, N, K), scale.view(E, N)
+
+
+def ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True):
+    """The block on 8-bit weights (codes and scales as quantize_weights gives
+    them): X [T, H] BF16 to [T, H] BF16.  Rows are quantised per token, into
+    the grouped order, before each product; the activation between the
+    products stays in FP32 until then."""
+    r = moe_route(logits, k, renormalize=renormalize)
+    q, s = quantize_int8(X, r.positions)
+    h = grouped_gemm_int8(q, s, W1q, w1_scale, r.group_offsets, gated=True, out_dtype=torch.float32)
+    q, s = quantize_int8(h)
+    y = grouped_gemm_int8(q, s, W2q, w2_scale, r.group_offsets)
+    return moe_combine(y, r.positions, r.weights)
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, renormalize):
+        r = moe_route(logits, k, renormalize=renormalize)
+        ctx.save_for_backward(logits, r.experts, r.weights)
+        ctx.renormalize = renormalize
+        ctx.mark_non_differentiable(r.experts, r.group_offsets, r.positions)
+        return tuple(r)
+
+    @staticmethod
+    def backward(ctx, _experts, dweights, _offsets, _positions):
+        logits, experts, weights = ctx.saved_tensors
+        return moe_route_grad(dweights.contiguous(), logits, experts, weights, renormalize=ctx.renormalize), None, None
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, positions):
+        ctx.save_for_backward(positions)
+        return moe_dispatch(X, positions)
+
+    @staticmethod
+    def backward(ctx, dout):
+        return moe_combine(dout.contiguous(), *ctx.saved_tensors), None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, positions, weights):
+        ctx.save_for_backward(rows, positions, weights)
+        return moe_combine(rows, positions, weights)
+
+    @staticmethod
+    def backward(ctx, dout):
+        drows, dweights = moe_combine_grad(dout.contiguous(), *ctx.saved_tensors)
+        return drows, None, dweights
+
+
+def route(logits, k, renormalize=True):
+    """moe_route, differentiable: (experts, weights, group_offsets, positions)
+    with the weights differentiable in the logits."""
+    return _Route.apply(logits, k, renormalize)
+
+
+def dispatch(X, positions):
+    """moe_dispatch, differentiable in X."""
+    return _Dispatch.apply(X, positions)
+
+
+def combine(rows, positions, weights):
+    """The weighted moe_combine, differentiable in rows and weights."""
+    return _Combine.apply(rows, positions, weights)
+
+
+def ffn(X, logits, W1, W2, k, renormalize=True, deterministic=True):
+    """The block in BF16, differentiable in X [T, H], logits [T, E] (FP32), W1
+    and W2; the weight gradients as autograd.grouped_linear computes them."""
+    _, weights, offsets, positions = route(logits, k, renormalize)
+    gate, up = grouped_linear(dispatch(X, positions), W1, offsets, deterministic).chunk(2, dim=1)
+    h = torch.nn.functional.silu(gate) * up
+    return combine(grouped_linear(h, W2, offsets, deterministic), positions, weights)

@@ -467,6 +467,110 @@ drgg_status drgg_wgrad_split_plan(const int32_t *group_offsets, int32_t E, int64
  */
 drgg_status drgg_tailsplit_units(int64_t tiles, int64_t workers, int64_t *out);
 
+/*
+ * ---- The operators around the grouped products of an expert layer ----------
+ *
+ * Router logits become group offsets and a place for every (token, expert)
+ * pair; rows move into the grouped order and back; and for serving the
+ * products run in 8-bit integers.  The conventions at the top of this file
+ * hold here too (caller-owned buffers, asynchronous on `stream`, nothing
+ * enqueued on an error, capturable).  Alignment: logits, dlogits, rows, codes,
+ * w_scale and the workspace 16 bytes, other arrays 4.
+ *
+ * T tokens with k experts each make R = T*k pairs, pair t*k + j being token t
+ * and its j-th expert.  Limits: 1 <= E <= 1024, 1 <= k <= min(E, 64),
+ * T*k < 2^31.
+ */
+
+/*
+ * Selection.  logits [T, E] FP32.  experts [T, k] int32: the k largest logits
+ * of each token, in decreasing order, the lowest index first among equals
+ * (-0 equals +0; NaN counts as larger than +infinity).  weights [T, k] FP32:
+ * the softmax over the k chosen logits (renormalize != 0) or over all E of
+ * them, taken at the chosen.  An expert whose logit is -infinity (masked)
+ * has weight 0, and a token with all of them masked has k zero weights (its
+ * experts are 0 .. k-1); a token with +infinity or NaN among the logits its
+ * softmax runs over gets NaN weights.
+ * The pairs are put in the order of their expert, pairs of one expert in
+ * order of t: group_offsets [E+1] int32 as the grouped products take them
+ * (o[E] = T*k), positions [T, k] int32 the row of each pair in that order.
+ * Workspace: moe_route_workspace_size bytes (0 for one workgroup's worth of
+ * tokens), no initialisation; calls in flight at once must not share it.
+ */
+drgg_status moe_route(const float *logits, int64_t T, int32_t E, int32_t k, int renormalize,
+                      int32_t *experts, float *weights, int32_t *group_offsets,
+                      int32_t *positions, void *workspace, size_t workspace_bytes,
+                      hipStream_t stream);
+drgg_status moe_route_workspace_size(int64_t T, int32_t E, int32_t k, size_t *bytes);
+
+/*
+ * Gradient of the weights in the logits: dlogits [T, E] FP32 from dweights
+ * [T, k] and moe_route's experts and weights; with s = sum_j w_j dw_j,
+ *   renormalize != 0: w_j (dw_j - s) at the chosen experts, 0 elsewhere;
+ *   else:             p_e (dw_e - s), p the softmax over all experts and dw_e
+ *                     the chosen experts' dweights, 0 for the others.
+ * A token with every expert masked gets zeros.
+ */
+drgg_status moe_route_grad(const float *dweights, const float *logits, const int32_t *experts,
+                           const float *weights, int64_t T, int32_t E, int32_t k, int renormalize,
+                           float *dlogits, hipStream_t stream);
+
+/*
+ * Rows between the token order and the grouped order.  Rows have H values
+ * (BF16 or FP32; H a multiple of 8, at most 2^22); positions [T, k] as
+ * moe_route gives them, a permutation of 0 .. T*k-1.  An entry outside that
+ * range is skipped, so that no access leaves the buffers; a grouped row that
+ * no entry names is not written.
+ *   dispatch      rows[positions[t,j]] = X[t]
+ *   combine       out[t] = sum_j weights[t,j] * rows[positions[t,j]], an FP32
+ *                 sum in order of j, one rounding; weights NULL: all 1, which
+ *                 is dispatch's gradient
+ *   combine_grad  drows[positions[t,j]] = weights[t,j] * dout[t] and
+ *                 dweights[t,j] = <dout[t], rows[positions[t,j]]> (FP32)
+ */
+drgg_status moe_dispatch(const void *X, const int32_t *positions, int64_t T, int32_t k, int64_t H,
+                         drgg_dtype dtype, void *rows, hipStream_t stream);
+drgg_status moe_combine(const void *rows, const int32_t *positions, const float *weights, int64_t T,
+                        int32_t k, int64_t H, drgg_dtype dtype, void *out, hipStream_t stream);
+drgg_status moe_combine_grad(const void *dout, const void *rows, const int32_t *positions,
+                             const float *weights, int64_t T, int32_t k, int64_t H,
+                             drgg_dtype dtype, void *drows, float *dweights, hipStream_t stream);
+
+/*
+ * Row quantisation to 8-bit integers.  X [T, K] BF16 or FP32, K a multiple of
+ * 16: scale = max|x| / 127 and q = round(127 x / max|x|) (ties to even), so
+ * that x ~ scale * q with |q| <= 127.  A row of zeros has scale 0; a row that
+ * holds an infinity or NaN has scale NaN and codes 0.  positions NULL (k = 1):
+ * q [T, K], scale [T].  With positions [T, k]: q [T*k, K], scale [T*k], token
+ * t's codes at its k rows (the dispatch and the quantisation in one pass).
+ * Weights [E, N, K] are quantised per output channel as T = E*N rows.
+ */
+drgg_status quantize_int8(const void *X, drgg_dtype dtype, int64_t T, int64_t K,
+                          const int32_t *positions, int32_t k, int8_t *q, float *scale,
+                          hipStream_t stream);
+
+/*
+ * Products in 8-bit integers, one scale per token and one per (expert, output
+ * channel):
+ *   Y[t,n] = x_scale[t] * w_scale[e(t),n] * sum_k Xq[t,k] * Wq[e(t),n,k]
+ * Xq [M,K] and Wq [E,N,K] int8 (any codes, -128 included), x_scale [M] and
+ * w_scale [E,N] FP32.  The sum is exact; it is scaled in FP32 and rounded
+ * once to out_dtype.  Y [M,N]; rows outside every group (offsets that end
+ * before M) are not written.
+ * gated != 0: N = 2I, Y [M,I] = silu(g) * u with g and u columns i and I + i of
+ * the product (in FP32), silu(g) = g / (1 + exp(-g)).
+ * N a multiple of 8 (gated: 16), K of 16, 16 <= K <= 131056 (so that the sum
+ * fits 32 bits), M < 2^31, N <= 2^22.  gemm_int8 is the one-group case
+ * without offsets.  No workspace.
+ */
+drgg_status grouped_gemm_int8(const int8_t *Xq, const float *x_scale, const int8_t *Wq,
+                              const float *w_scale, const int32_t *group_offsets, int32_t E,
+                              int64_t M, int64_t N, int64_t K, int gated, drgg_dtype out_dtype,
+                              void *Y, hipStream_t stream);
+drgg_status gemm_int8(const int8_t *Xq, const float *x_scale, const int8_t *Wq,
+                      const float *w_scale, int64_t M, int64_t N, int64_t K, int gated,
+                      drgg_dtype out_dtype, void *Y, hipStream_t stream);
+
 /* Text of a status code, with the HIP error name and text appended for
  * DRGG_EDEVICE (the fail-closed precedent of PR #7516, #7632 commit body:
  * an error names what failed and why). */
