@@ -54,8 +54,6 @@ drgg_status device_error(hipError_t e) {
 
 bool checks_offsets() { return g_knob_check_offsets.load() != 0 || env_flag("DRGG_CHECK_OFFSETS"); }
 
-namespace {
-
 // CU count of the current device, cached per device.
 drgg_status current_cu_count(int* cus) {
     static std::mutex mu;
@@ -75,6 +73,8 @@ drgg_status current_cu_count(int* cus) {
     *cus = cache[dev];
     return DRGG_OK;
 }
+
+namespace {
 
 // Shape checks shared by the three programs.
 drgg_status check_problem(int32_t E, int64_t M, int64_t N, int64_t K, drgg_dtype dt) {

@@ -57,8 +57,11 @@ drgg_status run_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, c
         if (st != DRGG_OK) return st;
     }
     if (M == 0) return DRGG_OK;
+    int cus = 0;
+    drgg_status st = current_cu_count(&cus);
+    if (st != DRGG_OK) return st;
     Int8Args a{Xq, Wq, x_scale, w_scale, offs, Y, M, N, K, E};
-    return launch_status(launch_int8(a, gated != 0, dt == DRGG_BF16, s));
+    return launch_status(launch_int8(a, gated != 0, dt == DRGG_BF16, cus, s));
 }
 
 }  // namespace

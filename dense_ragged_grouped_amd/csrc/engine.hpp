@@ -19,6 +19,29 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+
+// The element type of a product: fragment, accumulator and MFMA.  The engine
+// moves 16-byte pieces and counts the reduction in 2-byte units: one BF16
+// value, or a pair of 8-bit ones.  A fragment is 16 bytes of a tile row per
+// lane either way (8 BF16 values, 16 8-bit ones), and the MFMA shapes agree:
+// 32x32 outputs, the lower half of the lanes on the first 16 bytes of a
+// sub-step's 32 and the upper half on the last.
+struct Bf16 {
+    typedef bf16x8 Frag;
+    typedef f32x16 Acc;
+    static __device__ __forceinline__ Acc mfma(Frag b, Frag a, Acc c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, c, 0, 0, 0);
+    }
+};
+struct Int8 {
+    typedef i32x4 Frag;
+    typedef i32x16 Acc;
+    static __device__ __forceinline__ Acc mfma(Frag b, Frag a, Acc c) {
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, c, 0, 0, 0);
+    }
+};
 
 constexpr int kThreads = 256;       // fold / zero / router kernels
 // Grouped-GEMM kernels run 4 waves (one per SIMD) or, for the 256x256
@@ -408,11 +431,16 @@ __device__ __forceinline__ int64_t xcd_remap(int64_t b, int64_t G) {
 //   K-major:  base[i * ld + kk]   (reduction index contiguous)
 //   MN-major: base[kk * ld + i]   (output index contiguous; nvalid % 8 == 0)
 // Everything outside reads as zero.
+// A paired operand (K-major; gate and up rows of one weight matrix) is two
+// runs of nvalid rows, the second `pair` bytes after the first, and its tile
+// rows alternate between them in blocks of 32: tile rows 64p .. 64p+31 are
+// rows 32p .. 32p+31 of the first run, 64p+32 .. 64p+63 those of the second.
 struct Operand {
     const uint16_t* base;
     int64_t ld;
     int32_t nvalid;
     int32_t klen;
+    int64_t pair = 0;
 };
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -540,7 +568,7 @@ __device__ __forceinline__ int swzMN(int row) {
 // of the 4 waves issues a quarter.  Lane l of instruction g writes LDS bytes
 // [g*1024 + 16*l, +16); the swizzle is applied by choosing which global
 // chunk the lane fetches.
-template <int ROWS, bool KMAJ, int WAVES>
+template <int ROWS, bool KMAJ, int WAVES, bool PAIRED = false>
 struct StageLoader {
     static constexpr int kSpan = KMAJ ? 2 : 1;   // stages per load
     static constexpr int kPerWave = ROWS * kStageK * 2 * kSpan / 1024 / WAVES;
@@ -552,6 +580,7 @@ struct StageLoader {
     int32_t kp[kPerWave];     // reduction position of those 16 bytes from the first stage loaded
     int64_t step_bytes;       // byte distance between consecutive stages
     const char* base;
+    int64_t pair;             // paired operands: bytes to the second run
     int32_t klen;
 
     __device__ __forceinline__ void init(const Operand& op) {
@@ -561,6 +590,7 @@ struct StageLoader {
         asm volatile("" : "+v"(lane));
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         base = reinterpret_cast<const char*>(op.base);
+        if constexpr (PAIRED) pair = op.pair;
         klen = op.klen;
         step_bytes = KMAJ ? kStageK * 2 : (int64_t)kStageK * op.ld * 2;
 #pragma unroll
@@ -569,7 +599,8 @@ struct StageLoader {
             const int row = b / kRowBytes, phys = (b % kRowBytes) / 16;
             if constexpr (KMAJ) {
                 const int logical = phys ^ swzK(row);
-                off[i] = row < op.nvalid ? (uint32_t)(row * op.ld * 2 + logical * 16) : kOOB;
+                const int from = PAIRED ? (row & 31) + 32 * (row >> 6) : row;
+                off[i] = from < op.nvalid ? (uint32_t)(from * op.ld * 2 + logical * 16) : kOOB;
                 kp[i] = logical * 8;
             } else {
                 const int col = (phys ^ swzMN<kCPR>(row)) * 8;
@@ -595,8 +626,12 @@ struct StageLoader {
 #pragma unroll
         for (int i = J0; i < J1; ++i) {
             const uint32_t o = kp[i] < rem ? off[i] : kOOB;
+            // a wave instruction covers 8 rows of 128 bytes, so rows of one
+            // block of 32 and of one run of a paired operand
+            static_assert(!PAIRED || (KMAJ && kRowBytes == 128), "8 rows per wave instruction");
+            const bool second = PAIRED && (((wave * kPerWave + i) >> 2) & 1);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                r, (lds_void_t*)(buf + (wave * kPerWave + i) * 1024), 16, o, 0, 0, 0);
+                second ? make_rsrc(base + L * step_bytes + pair) : r, (lds_void_t*)(buf + (wave * kPerWave + i) * 1024), 16, o, 0, 0, 0);
         }
     }
 };
@@ -669,7 +704,7 @@ struct Stages {
 // so that the accumulator of lane l holds tile row l%32 and, in registers
 // 4q..4q+3, four consecutive tile columns 8q + 4*(l/32) .. +3: a lane's
 // outputs leave as 8- or 16-byte stores.
-template <int BM, int BN, bool AK, bool BK, int WAVES = kGemmWaves>
+template <int BM, int BN, bool AK, bool BK, int WAVES = kGemmWaves, class El = Bf16>
 struct TileMma {
     // wave grid: kWGM waves along the tile rows, kWGN along its columns
     static constexpr int kWGM = (WAVES == 8 && BM >= 256) ? 4 : 2;
@@ -682,8 +717,8 @@ struct TileMma {
     // LDS reads per sub-step: one per 32-row block (K-major), two (MN-major)
     static constexpr int kReads = kBI * (AK ? 1 : 2) + kBJ * (BK ? 1 : 2);
     static constexpr int kMfmas = kBI * kBJ;
-    f32x16 acc[kBI][kBJ];
-    bf16x8 fa[2][kBI], fb[2][kBJ];   // fragments of sub-step 0 and 1
+    typename El::Acc acc[kBI][kBJ];
+    typename El::Frag fa[2][kBI], fb[2][kBJ];   // fragments of sub-step 0 and 1
 
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -691,7 +726,7 @@ struct TileMma {
 #pragma unroll
             for (int j = 0; j < kBJ; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
     }
 
     // fragments of sub-step s of stage ST (its buffers in st) into set F
@@ -701,11 +736,14 @@ struct TileMma {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int ra = wave_row(wave), rb = wave_col(wave);
         // in the order the MFMAs consume them
-        fa[F][0] = read_frag<BM, AK>(st.a[ST], ST & 1, ra, s, l);
+        typedef typename El::Frag Frag;
+        fa[F][0] = __builtin_bit_cast(Frag, read_frag<BM, AK>(st.a[ST], ST & 1, ra, s, l));
 #pragma unroll
-        for (int j = 0; j < kBJ; ++j) fb[F][j] = read_frag<BN, BK>(st.b[ST], ST & 1, rb + 32 * j, s, l);
+        for (int j = 0; j < kBJ; ++j)
+            fb[F][j] = __builtin_bit_cast(Frag, read_frag<BN, BK>(st.b[ST], ST & 1, rb + 32 * j, s, l));
 #pragma unroll
-        for (int i = 1; i < kBI; ++i) fa[F][i] = read_frag<BM, AK>(st.a[ST], ST & 1, ra + 32 * i, s, l);
+        for (int i = 1; i < kBI; ++i)
+            fa[F][i] = __builtin_bit_cast(Frag, read_frag<BM, AK>(st.a[ST], ST & 1, ra + 32 * i, s, l));
     }
 
     // FIRST: the tile's first products, accumulated onto zero (this is what
@@ -716,8 +754,7 @@ struct TileMma {
         for (int i = 0; i < kBI; ++i)
 #pragma unroll
             for (int j = 0; j < kBJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[F][j], fa[F][i], FIRST ? f32x16{} : acc[i][j],
-                                                                    0, 0, 0);
+                acc[i][j] = El::mfma(fb[F][j], fa[F][i], FIRST ? typename El::Acc{} : acc[i][j]);
     }
 };
 
@@ -787,9 +824,13 @@ __device__ __forceinline__ void store_tile(const Mma& mma, void* out, int64_t ld
 // all it needs.  CPOL is the stores' cache policy: non-temporal for outputs;
 // 0 for data read back soon (the weight gradient's chunk partials, which the
 // fold then finds in the last-level cache).
-template <bool OUT_BF16, int R, int CPOL = kCpolNT, class Mma>
-__device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, void* out, int64_t ld, int rows,
-                                                 int cols) {
+//
+// store_tile_values is the same for values that are made on the way: value(i,
+// j, q) gives the four of row block i at columns 32j + 8q + 4*(lane/32) .. +3
+// of the wave's part, which starts at column rb and has NJ blocks of 32.
+template <bool OUT_BF16, int R, int CPOL, class Mma, int NJ, class Value>
+__device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* scr, void* out, int64_t ld, int rows,
+                                                  int cols) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -798,11 +839,11 @@ __device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, voi
     constexpr int BPS = SEG / 32;   // 32-column blocks per segment
     constexpr int CPL = R / 8;      // read-back chunks per lane and round
     static_assert(R == 8 || R == 16, "rounds of 8 or 16 rows");
-    static_assert(Mma::kBJ % BPS == 0, "whole segments per wave");
+    static_assert(NJ % BPS == 0, "whole segments per wave");
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ra = Mma::wave_row(wave), rb = Mma::wave_col(wave);
+    const int ra = Mma::wave_row(wave);
     lds_t* sw = scr + wave * (R * 128);
     const int r = lane & 31, h = lane >> 5;
     const int rr = r % R;   // this lane's scratch row in the round that owns it
@@ -812,20 +853,20 @@ __device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, voi
         const int r0 = ra + 32 * i;
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<char*>(out) + (int64_t)r0 * ld * ES);
 #pragma unroll
-        for (int g = 0; g < Mma::kBJ / BPS; ++g) {
+        for (int g = 0; g < NJ / BPS; ++g) {
             const int c0 = rb + g * SEG;
 #pragma unroll
             for (int s = 0; s < 32 / R; ++s) {
                 if (r / R == s) {
 #pragma unroll
                     for (int b = 0; b < BPS; ++b) {
-                        const f32x16& a = mma.acc[i][g * BPS + b];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
+                            const f32x4 a = value(i, g * BPS + b, q);
                             if constexpr (OUT_BF16) {
                                 // columns 32b + 8q + 4h .. +3: chunk 4b + q, its half h
-                                const bf16x2 lo = __builtin_convertvector((f32x2{a[4 * q], a[4 * q + 1]}), bf16x2);
-                                const bf16x2 hi = __builtin_convertvector((f32x2{a[4 * q + 2], a[4 * q + 3]}), bf16x2);
+                                const bf16x2 lo = __builtin_convertvector((f32x2{a[0], a[1]}), bf16x2);
+                                const bf16x2 hi = __builtin_convertvector((f32x2{a[2], a[3]}), bf16x2);
                                 *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(
                                     sw + rr * 128 + (((4 * b + q) ^ sx) << 4) + 8 * h) =
                                     u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
@@ -833,8 +874,8 @@ __device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, voi
                                 // columns 8q + 4h .. +3: chunk 2q + h
                                 *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(
                                     sw + rr * 128 + (((2 * q + h) ^ sx) << 4)) =
-                                    u32x4{__float_as_uint(a[4 * q]), __float_as_uint(a[4 * q + 1]),
-                                          __float_as_uint(a[4 * q + 2]), __float_as_uint(a[4 * q + 3])};
+                                    u32x4{__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                                          __float_as_uint(a[3])};
                             }
                         }
                     }
@@ -854,6 +895,17 @@ __device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, voi
             }
         }
     }
+}
+template <bool OUT_BF16, int R, int CPOL = kCpolNT, class Mma>
+__device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, void* out, int64_t ld, int rows,
+                                                 int cols) {
+    const int rb = Mma::wave_col(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    store_tile_values<OUT_BF16, R, CPOL, Mma, Mma::kBJ>(
+        [&](int i, int j, int q) {
+            const f32x16& a = mma.acc[i][j];
+            return f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+        },
+        rb, scr, out, ld, rows, cols);
 }
 
 // Issue schedule of the stage loads of a 4-wave runner (steps t of the
@@ -897,11 +949,11 @@ struct IssuePlan {
 // taken around the accumulators.  The next tile is decoded at the start of
 // step nk4-4, whose loads fetch its first stage.  Must be called by all
 // threads.
-template <int BM, int BN, bool AK, bool BK, int WAVES = kGemmWaves>
+template <int BM, int BN, bool AK, bool BK, int WAVES = kGemmWaves, class El = Bf16, bool PAIRED_B = false>
 struct TileRunner {
-    using Mma = TileMma<BM, BN, AK, BK, WAVES>;
+    using Mma = TileMma<BM, BN, AK, BK, WAVES, El>;
     using LA = StageLoader<BM, AK, WAVES>;
-    using LB = StageLoader<BN, BK, WAVES>;
+    using LB = StageLoader<BN, BK, WAVES, PAIRED_B>;
     using Plan = IssuePlan<AK, BK, LA::kPerWave, LB::kPerWave>;
     Mma mma;
     LA la;

@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "engine.hpp"
 #include "internal.hpp"
 #include "plan.hpp"
 
@@ -16,10 +17,7 @@ namespace drgg {
 
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -204,6 +202,105 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(Int8Args a) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// product, many rows per group
+//
+// The BF16 forward's persistent tile walk and main loop (engine.hpp) on 8-bit
+// elements: the same bytes per step, twice the products.  A gated tile's
+// columns are BN/2 gate rows of W and their BN/2 up rows in alternating
+// blocks of 32 (a paired operand), so that a lane holds a gate and its up in
+// the accumulators of neighbouring blocks.  The epilogue scales (and gates)
+// the sums as they pass to the staged whole-line stores.
+template <int BM, int BN, bool OUT_BF16, bool GATED, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
+    DRGG_STAGES(BM, BN, true, true, stg);
+    __shared__ Sched sch;
+    __shared__ __attribute__((aligned(16))) char ep[WAVES * ep_rows(BM, BN) * 128];
+    using Mma = TileMma<BM, BN, true, true, WAVES, Int8>;
+    constexpr int BC = GATED ? BN / 2 : BN;             // output columns per tile
+    constexpr int NJ = GATED ? Mma::kBJ / 2 : Mma::kBJ; // blocks of 32 of them per wave
+    const int64_t NO = GATED ? a.N / 2 : a.N, K2 = a.K / 2;
+    const int32_t ntn = (int32_t)((NO + BC - 1) / BC);
+    build_schedule(sch, a.offs, a.E, a.M, a.M, [=](int, int32_t T) { return ((T + BM - 1) / BM) * ntn; });
+    const int64_t total = uni(sch.prefix[a.E]);
+    const int64_t G = gridDim.x;
+    int64_t w = xcd_remap(blockIdx.x, G);
+    auto more = [&]() { return w < total; };
+    auto next = [&](TileInfo& t) {
+        const int e = uni(find_expert(sch, a.E, (int32_t)w));
+        const int32_t oe = uni(sch.offs[e]), oe1 = uni(sch.offs[e + 1]);
+        const int32_t local = (int32_t)w - uni(sch.prefix[e]);
+        const int32_t mt = local / ntn, nt = local % ntn;
+        t.o0 = oe + (int64_t)mt * BM;
+        t.o1 = (int64_t)nt * BC;
+        t.rows = (int32_t)min<int64_t>(BM, oe1 - t.o0);
+        t.cols = (int32_t)min<int64_t>(BC, NO - t.o1);
+        t.e = e;
+        t.A = Operand{reinterpret_cast<const uint16_t*>(a.X + t.o0 * a.K), K2, t.rows, (int32_t)K2};
+        t.B = Operand{reinterpret_cast<const uint16_t*>(a.W + ((int64_t)e * a.N + t.o1) * a.K), K2, t.cols,
+                      (int32_t)K2, NO * a.K};
+        w += G;
+    };
+    auto finish = [&](const TileInfo& t, const Mma& mma) {
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int rb = GATED ? Mma::wave_col(wave) / 2 : Mma::wave_col(wave);
+        const float* xs = a.xs + t.o0;
+        const float* ws = a.ws + (int64_t)t.e * a.N + t.o1;
+        float sx[Mma::kBI];
+        f32x4 sw[GATED ? 2 : 1][NJ][4];
+#pragma unroll
+        for (int i = 0; i < Mma::kBI; ++i)
+            sx[i] = xs[min(Mma::wave_row(wave) + 32 * i + (lane & 31), t.rows - 1)];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                // cols is a multiple of 8: the last four stand in for those past the end
+                const int c = min(rb + 32 * j + 8 * q + 4 * (lane >> 5), t.cols - 4);
+                sw[0][j][q] = *reinterpret_cast<const f32x4*>(ws + c);
+                if constexpr (GATED) sw[1][j][q] = *reinterpret_cast<const f32x4*>(ws + NO + c);
+            }
+        auto value = [&](int i, int j, int q) {
+            f32x4 y;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int c = 4 * q + r;
+                if constexpr (GATED) {
+                    const float g = (float)mma.acc[i][2 * j][c] * sw[0][j][q][r] * sx[i];
+                    const float u = (float)mma.acc[i][2 * j + 1][c] * sw[1][j][q][r] * sx[i];
+                    y[r] = g / (1.f + expf(-g)) * u;
+                } else {
+                    y[r] = (float)mma.acc[i][j][c] * sw[0][j][q][r] * sx[i];
+                }
+            }
+            return y;
+        };
+        const int64_t o = t.o0 * NO + t.o1;
+        void* base = OUT_BF16 ? (void*)(static_cast<uint16_t*>(a.out) + o) : (void*)(static_cast<float*>(a.out) + o);
+        store_tile_values<OUT_BF16, ep_rows(BM, BN), kCpolNT, Mma, NJ>(value, rb, (lds_t*)ep, base, NO, t.rows, t.cols);
+    };
+    TileRunner<BM, BN, true, true, WAVES, Int8, GATED> runner;
+    runner.st = stg;
+    runner.run(more, next, finish);
+}
+
+template <int BM, int BN, int WAVES>
+hipError_t launch_int8_tile(const Int8Args& a, bool gated, bool bf16, int64_t grid_n, hipStream_t s) {
+    const dim3 grid((unsigned)grid_n), block(64 * WAVES);
+    timing_mark("int8_tile_kernel", s);
+    if (gated) {
+        if (bf16) hipLaunchKernelGGL((int8_tile_kernel<BM, BN, true, true, WAVES>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((int8_tile_kernel<BM, BN, false, true, WAVES>), grid, block, 0, s, a);
+    } else {
+        if (bf16) hipLaunchKernelGGL((int8_tile_kernel<BM, BN, true, false, WAVES>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((int8_tile_kernel<BM, BN, false, false, WAVES>), grid, block, 0, s, a);
+    }
+    timing_end(s);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, const int32_t* positions, int32_t k,
@@ -219,7 +316,16 @@ hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, 
     return hipGetLastError();
 }
 
-hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, hipStream_t s) {
+hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, hipStream_t s) {
+    if (a.M > 32 * (int64_t)a.E) {
+        // tiles of 128x256 where those of 256x256 leave CUs without one
+        const int64_t nc = ceil_div(gated ? a.N / 2 : a.N, gated ? 128 : 256);
+        const bool large = (a.M / 256) * nc >= kRuleCUs;
+        const int64_t most = (a.M / (large ? 256 : 128) + a.E) * nc;
+        const int64_t grid_n = most < cus ? most : cus;
+        if (large) return launch_int8_tile<256, 256, 8>(a, gated, bf16, grid_n, s);
+        return launch_int8_tile<128, 256, 4>(a, gated, bf16, grid_n, s);
+    }
     const dim3 grid((unsigned)ceil_div(gated ? a.N / 2 : a.N, gated ? 16 : 32), (unsigned)a.E), block(256);
     timing_mark("int8_rows_kernel", s);
     if (gated) {

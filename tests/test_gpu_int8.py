@@ -171,6 +171,23 @@ def test_dense(drgg, M, N, K, gated):
     assert torch.equal(got, one)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,K", [(1040, 208), (2064, 16), (1040, 528)])
+def test_many_rows(drgg, N, K, dtype, gated):
+    """Enough output tiles that every compute unit has one of the largest."""
+    counts = [5000, 0, 1, 7777, 256, 511, 3000]
+    M, E = sum(counts), len(counts)
+    X, xs, W, ws = operands(M, N, K, E, N + K)
+    if gated:
+        xs = xs / np.float32(16 * np.sqrt(K))
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    out = torch.full((M + 3, N // 2 if gated else N), 7.0, dtype=dtype, device="cuda")
+    got = drgg.grouped_gemm_int8(dev(X), dev(xs), dev(W), dev(ws), dev(offsets), gated=gated, out_dtype=dtype, out=out[:M])
+    check(host(got), grouped64(X, xs, W, ws, offsets), dtype, gated)
+    assert bool((out[M:] == 7.0).all())
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_longest_sum_of_the_largest_codes(drgg, M):
     """K = 131056 products of 2^14 stay below 2^31."""
