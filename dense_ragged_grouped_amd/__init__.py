@@ -15,7 +15,8 @@ Programs (flashinfer PR #8258, opening summary paragraph), shapes row-major:
 Around them, for a whole expert layer: the router's selection (moe_route,
 moe_route_grad), the movement of rows (moe_dispatch, moe_combine,
 moe_combine_grad), and products in 8-bit integers (quantize_int8,
-grouped_gemm_int8, gemm_int8); `moe` puts them together.
+grouped_gemm_int8, gemm_int8); moe_ffn_int8 runs them as one serving block, and
+`moe` holds the differentiable ones.
 
 ``offsets`` is an int32 CUDA tensor: offsets[0] = 0, non-decreasing,
 offsets[E] = M; expert e owns tokens offsets[e] .. offsets[e+1]-1.
@@ -46,7 +47,7 @@ EXPORTS = (
     "drgg_tailsplit_units", "drgg_wgrad_tail_plan", "drgg_wgrad_split_plan", "grouped_gemm_wgrad_noalloc",
     "drgg_set_knob", "drgg_timing_count", "drgg_timing_read", "drgg_status_string", "drgg_abi_version",
     "moe_route", "moe_route_workspace_size", "moe_route_grad", "moe_dispatch", "moe_combine", "moe_combine_grad",
-    "quantize_int8", "grouped_gemm_int8", "gemm_int8",
+    "quantize_int8", "grouped_gemm_int8", "gemm_int8", "moe_ffn_int8", "moe_ffn_int8_workspace_size",
 )
 
 
@@ -155,7 +156,9 @@ def _load(path=LIB_PATH):
     lib.quantize_int8.argtypes = [vp, c_int, i64, i64, vp, i32, vp, vp, vp]
     lib.grouped_gemm_int8.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, c_int, c_int, vp, vp]
     lib.gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp]
-    for name in ("moe_route", "moe_route_workspace_size", "moe_route_grad", "moe_dispatch", "moe_combine",
+    lib.moe_ffn_int8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, i64, c_int, vp, vp, sz, vp]
+    lib.moe_ffn_int8_workspace_size.argtypes = [i64, i32, i32, i64, i64, ctypes.POINTER(sz)]
+    for name in ("moe_ffn_int8", "moe_ffn_int8_workspace_size", "moe_route", "moe_route_workspace_size", "moe_route_grad", "moe_dispatch", "moe_combine",
                  "moe_combine_grad", "quantize_int8", "grouped_gemm_int8", "gemm_int8"):
         getattr(lib, name).restype = c_int
     lib.drgg_status_string.argtypes = [c_int]
@@ -343,7 +346,7 @@ def _torch_dtype(code: int):
 
 def _need(t, dtype, name, ndim):
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -719,6 +722,46 @@ class Routing(NamedTuple):
     positions: "torch.Tensor"       # [T, k] int32, each pair's row in the grouped order
 
 
+def _call(name, stream, tensors, *args):
+    """lib.<name>(*args, stream) on the device of `tensors` (None entries
+    skipped).  These calls are short, so the usual case -- the tensors on the
+    current device, its current stream -- reads the stream's handle directly
+    (torch's accessor for it, 0.1 us; the Stream object and the device guard
+    cost 3 us)."""
+    torch = _torch()
+    first = tensors[0]
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if stream is None and raw is not None:
+        index = torch.cuda.current_device()
+        if all(t is None or t.get_device() == index for t in tensors):
+            _check(getattr(lib, name)(*args, raw(index)), name)
+            return
+    with _on_one_device(stream, *tensors):
+        _check(getattr(lib, name)(*args, _stream(first.device, stream)), name)
+
+
+def _need_shape(t, dtype, shape, name):
+    _need(t, dtype, name, len(shape))
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _out(out, dtype, shape, like):
+    if out is None:
+        return like.new_empty(shape, dtype=dtype)
+    _need_shape(out, dtype, shape, "out")
+    return out
+
+
+def _row_code(t, name):
+    """The dtype code of a contiguous 2-d row tensor, BF16 or FP32."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
+    _need(t, t.dtype, name, 2)
+    return BF16 if t.dtype == torch.bfloat16 else FP32
+
+
 def route_workspace_size(T: int, E: int, k: int) -> int:
     n = ctypes.c_size_t()
     _check(lib.moe_route_workspace_size(T, E, k, ctypes.byref(n)), "moe_route_workspace_size")
@@ -734,17 +777,16 @@ def moe_route(logits, k, renormalize=True, workspace=None, stream=None):
     torch = _torch()
     _need(logits, torch.float32, "logits", 2)
     T, E = logits.shape
-    k, dev = int(k), logits.device
+    k = int(k)
     nbytes = route_workspace_size(T, E, k)
-    experts = torch.empty((T, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
-    positions = torch.empty((T, k), dtype=torch.int32, device=dev)
-    with _on_one_device(stream, logits):
-        ws_ptr, ws_bytes = _workspace(dev, nbytes, workspace, True, kind="route", stream=stream) if nbytes else (None, 0)
-        st = lib.moe_route(logits.data_ptr(), T, E, k, int(bool(renormalize)), experts.data_ptr(), weights.data_ptr(),
-                           offsets.data_ptr(), positions.data_ptr(), ws_ptr, ws_bytes, _stream(dev, stream))
-    _check(st, "moe_route")
+    weights = logits.new_empty((T, k))
+    experts = logits.new_empty((T, k), dtype=torch.int32)
+    positions = logits.new_empty((T, k), dtype=torch.int32)
+    offsets = logits.new_empty((E + 1,), dtype=torch.int32)
+    ws_ptr, ws_bytes = (_workspace(logits.device, nbytes, workspace, True, kind="route", stream=stream) if nbytes
+                        else (None, 0))
+    _call("moe_route", stream, (logits,), logits.data_ptr(), T, E, k, 1 if renormalize else 0, experts.data_ptr(),
+          weights.data_ptr(), offsets.data_ptr(), positions.data_ptr(), ws_ptr, ws_bytes)
     return Routing(experts, weights, offsets, positions)
 
 
@@ -755,39 +797,13 @@ def moe_route_grad(dweights, logits, experts, weights, renormalize=True, out=Non
     T, E = logits.shape
     _need(experts, torch.int32, "experts", 2)
     k = experts.shape[1]
-    _need_pairs(experts, T, k, torch.int32, "experts")
-    _need_pairs(weights, T, k, torch.float32, "weights")
-    _need_pairs(dweights, T, k, torch.float32, "dweights")
-    out = _out_rows2(out, (T, E), torch.float32, logits.device)
-    with _on_one_device(stream, logits, dweights, experts, weights, out):
-        st = lib.moe_route_grad(dweights.data_ptr(), logits.data_ptr(), experts.data_ptr(), weights.data_ptr(), T, E, k,
-                                int(bool(renormalize)), out.data_ptr(), _stream(logits.device, stream))
-    _check(st, "moe_route_grad")
+    _need_shape(experts, torch.int32, (T, k), "experts")
+    _need_shape(weights, torch.float32, (T, k), "weights")
+    _need_shape(dweights, torch.float32, (T, k), "dweights")
+    out = _out(out, torch.float32, (T, E), logits)
+    _call("moe_route_grad", stream, (logits, dweights, experts, weights, out), dweights.data_ptr(), logits.data_ptr(),
+          experts.data_ptr(), weights.data_ptr(), T, E, k, 1 if renormalize else 0, out.data_ptr())
     return out
-
-
-def _need_pairs(t, T, k, dtype, name):
-    _need(t, dtype, name, 2)
-    if tuple(t.shape) != (T, k):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, k)}")
-
-
-def _out_rows2(out, shape, dtype, device, name="out"):
-    if out is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    _need(out, dtype, name, len(shape))
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} has the wrong shape")
-    return out
-
-
-def _row_code(t, name):
-    """The dtype code of a contiguous 2-d row tensor, BF16 or FP32."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
-    _need(t, t.dtype, name, 2)
-    return BF16 if t.dtype == torch.bfloat16 else FP32
 
 
 def moe_dispatch(X, positions, out=None, stream=None):
@@ -798,19 +814,15 @@ def moe_dispatch(X, positions, out=None, stream=None):
     T, H = X.shape
     _need(positions, torch.int32, "positions", 2)
     k = positions.shape[1]
-    _need_pairs(positions, T, k, torch.int32, "positions")
-    out = _out_rows2(out, (T * k, H), X.dtype, X.device)
-    with _on_one_device(stream, X, positions, out):
-        st = lib.moe_dispatch(X.data_ptr(), positions.data_ptr(), T, k, H, code, out.data_ptr(),
-                              _stream(X.device, stream))
-    _check(st, "moe_dispatch")
+    _need_shape(positions, torch.int32, (T, k), "positions")
+    out = _out(out, X.dtype, (T * k, H), X)
+    _call("moe_dispatch", stream, (X, positions, out), X.data_ptr(), positions.data_ptr(), T, k, H, code,
+          out.data_ptr())
     return out
 
 
-def moe_combine(rows, positions, weights=None, out=None, stream=None):
-    """Rows back in token order: out[t] = sum_j weights[t, j] *
-    rows[positions[t, j]] (FP32 sum, one rounding to the rows' dtype).  Without
-    weights this is the gradient of moe_dispatch."""
+def _grouped_rows(rows, positions, weights):
+    """(dtype code, T, k, H) of rows [T*k, H], positions and weights [T, k]."""
     torch = _torch()
     code = _row_code(rows, "rows")
     R, H = rows.shape
@@ -819,34 +831,29 @@ def moe_combine(rows, positions, weights=None, out=None, stream=None):
     if R != T * k:
         raise ValueError(f"rows has {R} rows, positions {T} x {k}")
     if weights is not None:
-        _need_pairs(weights, T, k, torch.float32, "weights")
-    out = _out_rows2(out, (T, H), rows.dtype, rows.device)
-    with _on_one_device(stream, rows, positions, weights, out):
-        st = lib.moe_combine(rows.data_ptr(), positions.data_ptr(), weights.data_ptr() if weights is not None else None,
-                             T, k, H, code, out.data_ptr(), _stream(rows.device, stream))
-    _check(st, "moe_combine")
+        _need_shape(weights, torch.float32, (T, k), "weights")
+    return code, T, k, H
+
+
+def moe_combine(rows, positions, weights=None, out=None, stream=None):
+    """Rows back in token order: out[t] = sum_j weights[t, j] *
+    rows[positions[t, j]] (FP32 sum, one rounding to the rows' dtype).  Without
+    weights this is the gradient of moe_dispatch."""
+    code, T, k, H = _grouped_rows(rows, positions, weights)
+    out = _out(out, rows.dtype, (T, H), rows)
+    _call("moe_combine", stream, (rows, positions, weights, out), rows.data_ptr(), positions.data_ptr(),
+          weights.data_ptr() if weights is not None else None, T, k, H, code, out.data_ptr())
     return out
 
 
 def moe_combine_grad(dout, rows, positions, weights, stream=None):
     """Gradients of the weighted moe_combine: (drows [T*k, H] in the rows'
     dtype, dweights [T, k] FP32)."""
-    torch = _torch()
-    code = _row_code(rows, "rows")
-    R, H = rows.shape
-    _need(positions, torch.int32, "positions", 2)
-    T, k = positions.shape
-    if R != T * k:
-        raise ValueError(f"rows has {R} rows, positions {T} x {k}")
-    _need_pairs(weights, T, k, torch.float32, "weights")
-    _need(dout, rows.dtype, "dout", 2)
-    if tuple(dout.shape) != (T, H):
-        raise ValueError(f"dout has shape {tuple(dout.shape)}, expected {(T, H)}")
-    drows, dweights = torch.empty_like(rows), torch.empty_like(weights)
-    with _on_one_device(stream, dout, rows, positions, weights):
-        st = lib.moe_combine_grad(dout.data_ptr(), rows.data_ptr(), positions.data_ptr(), weights.data_ptr(), T, k, H,
-                                  code, drows.data_ptr(), dweights.data_ptr(), _stream(rows.device, stream))
-    _check(st, "moe_combine_grad")
+    code, T, k, H = _grouped_rows(rows, positions, weights)
+    _need_shape(dout, rows.dtype, (T, H), "dout")
+    drows, dweights = rows.new_empty(rows.shape), weights.new_empty((T, k))
+    _call("moe_combine_grad", stream, (dout, rows, positions, weights), dout.data_ptr(), rows.data_ptr(),
+          positions.data_ptr(), weights.data_ptr(), T, k, H, code, drows.data_ptr(), dweights.data_ptr())
     return drows, dweights
 
 
@@ -857,17 +864,14 @@ def quantize_int8(X, positions=None, stream=None):
     torch = _torch()
     code = _row_code(X, "X")
     T, K = X.shape
-    k = 1
+    k, at = 1, None
     if positions is not None:
         _need(positions, torch.int32, "positions", 2)
-        k = positions.shape[1]
-        _need_pairs(positions, T, k, torch.int32, "positions")
-    q = torch.empty((T * k, K), dtype=torch.int8, device=X.device)
-    scale = torch.empty((T * k,), dtype=torch.float32, device=X.device)
-    with _on_one_device(stream, X, positions):
-        st = lib.quantize_int8(X.data_ptr(), code, T, K, positions.data_ptr() if positions is not None else None, k,
-                               q.data_ptr(), scale.data_ptr(), _stream(X.device, stream))
-    _check(st, "quantize_int8")
+        k, at = positions.shape[1], positions.data_ptr()
+        _need_shape(positions, torch.int32, (T, k), "positions")
+    q = X.new_empty((T * k, K), dtype=torch.int8)
+    scale = X.new_empty((T * k,), dtype=torch.float32)
+    _call("quantize_int8", stream, (X, positions), X.data_ptr(), code, T, K, at, k, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -882,9 +886,8 @@ def _int8_operands(Xq, x_scale, Wq, w_scale, wdim, gated, out_dtype, out):
     if Wq.shape[-1] != K or x_scale.shape[0] != M or w_scale.shape != Wq.shape[:-1]:
         raise ValueError(f"shape mismatch: Xq {tuple(Xq.shape)}, x_scale {tuple(x_scale.shape)}, "
                          f"Wq {tuple(Wq.shape)}, w_scale {tuple(w_scale.shape)}")
-    code = _dtype_code(out_dtype if out_dtype is not None else torch.bfloat16)
-    out = _out_rows2(out, (M, N // 2 if gated else N), _torch_dtype(code), Xq.device)
-    return M, N, K, code, out
+    code = BF16 if out_dtype is None else _dtype_code(out_dtype)
+    return M, N, K, code, _out(out, _torch_dtype(code), (M, N // 2 if gated else N), Xq)
 
 
 def grouped_gemm_int8(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, out_dtype=None, out=None, stream=None):
@@ -896,22 +899,56 @@ def grouped_gemm_int8(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, out_
     M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 3, gated, out_dtype, out)
     if Wq.shape[0] != E:
         raise ValueError(f"shape mismatch: Wq {tuple(Wq.shape)}, E={E}")
-    with _on_one_device(stream, Xq, x_scale, Wq, w_scale, group_offsets, out):
-        st = lib.grouped_gemm_int8(Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(),
-                                   group_offsets.data_ptr(), E, M, N, K, int(bool(gated)), code, out.data_ptr(),
-                                   _stream(Xq.device, stream))
-    _check(st, "grouped_gemm_int8")
+    _call("grouped_gemm_int8", stream, (Xq, x_scale, Wq, w_scale, group_offsets, out), Xq.data_ptr(),
+          x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(), group_offsets.data_ptr(), E, M, N, K,
+          1 if gated else 0, code, out.data_ptr())
     return out
 
 
 def gemm_int8(Xq, x_scale, Wq, w_scale, gated=False, out_dtype=None, out=None, stream=None):
     """The one-group case of grouped_gemm_int8: Wq [N, K], w_scale [N]."""
     M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 2, gated, out_dtype, out)
-    with _on_one_device(stream, Xq, x_scale, Wq, w_scale, out):
-        st = lib.gemm_int8(Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(), M, N, K,
-                           int(bool(gated)), code, out.data_ptr(), _stream(Xq.device, stream))
-    _check(st, "gemm_int8")
+    _call("gemm_int8", stream, (Xq, x_scale, Wq, w_scale, out), Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(),
+          w_scale.data_ptr(), M, N, K, 1 if gated else 0, code, out.data_ptr())
     return out
+
+
+def moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True, out=None, workspace=None, stream=None):
+    """A gated feed-forward block of E experts in one call: moe_route on logits
+    [T, E], quantize_int8 of X [T, H] (BF16) into the grouped order, the gated
+    product with W1q [E, 2I, H] (FP32 result), quantize_int8 of it, the product
+    with W2q [E, H, I] (BF16) and moe_combine: [T, H] BF16.  `workspace`: a
+    device tensor of at least ffn_workspace_size bytes, or None for one
+    allocated for this call."""
+    torch = _torch()
+    _need(X, torch.bfloat16, "X", 2)
+    T, H = X.shape
+    _need(logits, torch.float32, "logits", 2)
+    E = logits.shape[1]
+    _need_shape(logits, torch.float32, (T, E), "logits")
+    _need(W1q, torch.int8, "W1q", 3)
+    N = W1q.shape[1]
+    I = N // 2
+    _need_shape(W1q, torch.int8, (E, 2 * I, H), "W1q")
+    _need_shape(w1_scale, torch.float32, (E, N), "w1_scale")
+    _need_shape(W2q, torch.int8, (E, H, I), "W2q")
+    _need_shape(w2_scale, torch.float32, (E, H), "w2_scale")
+    out = _out(out, torch.bfloat16, (T, H), X)
+    if workspace is None:
+        nbytes = ffn_workspace_size(T, E, k, H, I)
+        with torch.cuda.stream(stream):   # freed memory stays ordered on the stream that uses it
+            workspace = X.new_empty((nbytes,), dtype=torch.uint8)
+    _call("moe_ffn_int8", stream, (X, logits, W1q, w1_scale, W2q, w2_scale, out, workspace), X.data_ptr(),
+          logits.data_ptr(), W1q.data_ptr(), w1_scale.data_ptr(), W2q.data_ptr(), w2_scale.data_ptr(), T, E, int(k), H,
+          I, 1 if renormalize else 0, out.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return out
+
+
+def ffn_workspace_size(T: int, E: int, k: int, H: int, I: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.moe_ffn_int8_workspace_size(T, E, k, H, I, ctypes.byref(n)), "moe_ffn_int8_workspace_size")
+    return n.value
 
 
 if os.environ.get("DRGG_NO_ROUTES", "0") in ("", "0"):

@@ -64,6 +64,39 @@ drgg_status run_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, c
     return launch_status(launch_int8(a, gated != 0, dt == DRGG_BF16, cus, s));
 }
 
+// The parts of moe_ffn_int8's workspace (byte offsets, multiples of 256).  The
+// experts' outputs y take the place of the grouped codes and the activation,
+// which are no longer needed by then.
+struct FfnLayout {
+    int64_t experts, weights, offsets, positions, table, xs, hs, hq, x, h, y, bytes;
+};
+drgg_status ffn_layout(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I, FfnLayout* L) {
+    drgg_status st = check_route(T, E, k);
+    if (st != DRGG_OK) return st;
+    if (H < 16 || H > kInt8MaxK || I < 16 || I > kInt8MaxK) return DRGG_ESHAPE;
+    if (H % 16 || I % 16) return DRGG_EALIGN;
+    const int64_t R = T * k;   // below 2^31; a row of any part is below 2^20 bytes
+    int64_t at = 0;
+    auto part = [&](int64_t n) {
+        const int64_t o = at;
+        at += round_up(n, 256);
+        return o;
+    };
+    L->experts = part(R * 4);
+    L->weights = part(R * 4);
+    L->offsets = part(((int64_t)E + 1) * 4);
+    L->positions = part(R * 4);
+    L->table = part((int64_t)route_table_bytes(T, E));
+    L->xs = part(R * 4);
+    L->hs = part(R * 4);
+    L->hq = part(R * I);
+    L->x = L->y = at;
+    L->h = at + round_up(R * H, 256);
+    const int64_t both = round_up(R * H, 256) + round_up(R * I * 4, 256), y = round_up(R * H * 2, 256);
+    L->bytes = at + (both > y ? both : y);
+    return DRGG_OK;
+}
+
 }  // namespace
 }  // namespace drgg
 
@@ -146,7 +179,7 @@ drgg_status moe_combine_grad(const void* dout, const void* rows, const int32_t* 
 drgg_status quantize_int8(const void* X, drgg_dtype dtype, int64_t T, int64_t K, const int32_t* positions, int32_t k,
                           int8_t* q, float* scale, hipStream_t stream) {
     if (dtype != DRGG_BF16 && dtype != DRGG_FP32) return DRGG_EINVAL;
-    if (!positions && k != 1) return DRGG_EINVAL;
+    if (T > 0 && !positions && k != 1) return DRGG_EINVAL;
     drgg_status st = check_pairs(T, k);
     if (st != DRGG_OK) return st;
     if (K < 16 || K > (1 << 22)) return DRGG_ESHAPE;
@@ -167,6 +200,54 @@ drgg_status grouped_gemm_int8(const int8_t* Xq, const float* x_scale, const int8
 drgg_status gemm_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, const float* w_scale, int64_t M,
                       int64_t N, int64_t K, int gated, drgg_dtype out_dtype, void* Y, hipStream_t stream) {
     return run_int8(Xq, x_scale, Wq, w_scale, nullptr, 1, M, N, K, gated, out_dtype, Y, stream);
+}
+
+drgg_status moe_ffn_int8_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I, size_t* bytes) {
+    if (!bytes) return DRGG_EINVAL;
+    FfnLayout L;
+    drgg_status st = ffn_layout(T, E, k, H, I, &L);
+    if (st != DRGG_OK) return st;
+    *bytes = (size_t)L.bytes;
+    return DRGG_OK;
+}
+
+drgg_status moe_ffn_int8(const void* X, const float* logits, const int8_t* W1q, const float* w1_scale,
+                         const int8_t* W2q, const float* w2_scale, int64_t T, int32_t E, int32_t k, int64_t H,
+                         int64_t I, int renormalize, void* out, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream) {
+    FfnLayout L;
+    drgg_status st = ffn_layout(T, E, k, H, I, &L);
+    if (st != DRGG_OK) return st;
+    if (!W1q || !w1_scale || !W2q || !w2_scale || (T > 0 && (!X || !logits || !out))) return DRGG_EINVAL;
+    if (!aligned16(X) || !aligned16(logits) || !aligned16(W1q) || !aligned16(w1_scale) || !aligned16(W2q) ||
+        !aligned16(w2_scale) || !aligned16(out))
+        return DRGG_EALIGN;
+    if (T == 0) return DRGG_OK;
+    if (!workspace || workspace_bytes < (size_t)L.bytes) return DRGG_EWORKSPACE;
+    if (!aligned16(workspace)) return DRGG_EALIGN;
+    char* ws = static_cast<char*>(workspace);
+    auto* experts = reinterpret_cast<int32_t*>(ws + L.experts);
+    auto* weights = reinterpret_cast<float*>(ws + L.weights);
+    auto* offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
+    auto* positions = reinterpret_cast<int32_t*>(ws + L.positions);
+    auto* xs = reinterpret_cast<float*>(ws + L.xs);
+    auto* hs = reinterpret_cast<float*>(ws + L.hs);
+    auto* hq = reinterpret_cast<int8_t*>(ws + L.hq);
+    auto* x = reinterpret_cast<int8_t*>(ws + L.x);
+    int cus = 0;
+    st = current_cu_count(&cus);
+    if (st != DRGG_OK) return st;
+    const int64_t R = T * k;
+    hipError_t e = launch_moe_route(logits, T, E, k, renormalize != 0, experts, weights, offsets, positions,
+                                    reinterpret_cast<int32_t*>(ws + L.table), stream);
+    if (e == hipSuccess) e = launch_quantize_int8(X, true, T, H, positions, k, x, xs, stream);
+    if (e == hipSuccess)
+        e = launch_int8(Int8Args{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E}, true, false, cus, stream);
+    if (e == hipSuccess) e = launch_quantize_int8(ws + L.h, false, R, I, nullptr, 1, hq, hs, stream);
+    if (e == hipSuccess)
+        e = launch_int8(Int8Args{hq, W2q, hs, w2_scale, offsets, ws + L.y, R, H, I, E}, false, true, cus, stream);
+    if (e == hipSuccess) e = launch_moe_combine(ws + L.y, positions, weights, T, k, H, true, out, stream);
+    return launch_status(e);
 }
 
 }  // extern "C"

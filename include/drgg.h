@@ -571,6 +571,23 @@ drgg_status gemm_int8(const int8_t *Xq, const float *x_scale, const int8_t *Wq,
                       const float *w_scale, int64_t M, int64_t N, int64_t K, int gated,
                       drgg_dtype out_dtype, void *Y, hipStream_t stream);
 
+/*
+ * A gated feed-forward block of E experts on 8-bit weights, the operators
+ * above in one call: moe_route(logits), quantize_int8 of X [T,H] BF16 into the
+ * grouped order, the gated product with W1q [E,2I,H] (gate rows, then up
+ * rows; FP32 result [T*k,I]), quantize_int8 of that, the product with W2q
+ * [E,H,I] (BF16), and moe_combine into out [T,H] BF16.  The same results as
+ * the single calls.  H and I multiples of 16.  Workspace:
+ * moe_ffn_int8_workspace_size bytes, 16-byte aligned, no initialisation;
+ * calls in flight at once must not share it.
+ */
+drgg_status moe_ffn_int8(const void *X, const float *logits, const int8_t *W1q,
+                         const float *w1_scale, const int8_t *W2q, const float *w2_scale,
+                         int64_t T, int32_t E, int32_t k, int64_t H, int64_t I, int renormalize,
+                         void *out, void *workspace, size_t workspace_bytes, hipStream_t stream);
+drgg_status moe_ffn_int8_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
+                                        size_t *bytes);
+
 /* Text of a status code, with the HIP error name and text appended for
  * DRGG_EDEVICE (the fail-closed precedent of PR #7516, #7632 commit body:
  * an error names what failed and why). */

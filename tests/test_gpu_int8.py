@@ -268,6 +268,47 @@ def test_ffn_int8(drgg, T, E, k, H, I):
     assert err < 2.0 ** -8, err
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(0, 4, 2, 64, 32), (5, 8, 3, 96, 16), (700, 5, 2, 144, 272)])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_ffn_is_its_operators(drgg, T, E, k, H, I, renormalize):
+    """The one call gives the same bits as the operators called one by one, also on a side stream, into a given
+    workspace full of garbage, and under graph replay."""
+    rng = np.random.default_rng(T)
+    X = dev(rng.standard_normal((T, H)).astype(np.float32), torch.bfloat16)
+    logits = dev(rng.standard_normal((T, E)).astype(np.float32))
+    w1, s1 = dev(rng.integers(-127, 128, (E, 2 * I, H)).astype(np.int8)), dev(rng.uniform(1, 2, (E, 2 * I)).astype(np.float32) / 999)
+    w2, s2 = dev(rng.integers(-127, 128, (E, H, I)).astype(np.int8)), dev(rng.uniform(1, 2, (E, H)).astype(np.float32) / 999)
+    r = drgg.moe_route(logits, k, renormalize=renormalize)
+    q, s = drgg.quantize_int8(X, r.positions)
+    h = drgg.grouped_gemm_int8(q, s, w1, s1, r.group_offsets, gated=True, out_dtype=torch.float32)
+    q, s = drgg.quantize_int8(h)
+    want = drgg.moe_combine(drgg.grouped_gemm_int8(q, s, w2, s2, r.group_offsets), r.positions, r.weights)
+    args = (X, logits, w1, s1, w2, s2, k, renormalize)
+    assert torch.equal(drgg.moe_ffn_int8(*args), want)
+    ws = torch.full((drgg.ffn_workspace_size(T, E, k, H, I) + 16,), 255, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = [drgg.moe_ffn_int8(*args, workspace=ws, stream=side), drgg.moe_ffn_int8(*args, stream=side)]
+    torch.cuda.synchronize()
+    assert torch.equal(other[0], want) and torch.equal(other[1], want)
+    g, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
+    with torch.cuda.graph(g):
+        drgg.moe_ffn_int8(*args, workspace=ws, out=out)
+    for _ in range(3):
+        out.zero_()
+        drgg.moe_ffn_int8(*args)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    if T:
+        with pytest.raises(drgg.DrggError):
+            drgg.moe_ffn_int8(*args, workspace=ws[:64])
+        with pytest.raises(ValueError):
+            drgg.moe_ffn_int8(X, logits, w1, s1, w2.transpose(1, 2).contiguous(), s2, k)
+        with pytest.raises(TypeError):
+            drgg.moe_ffn_int8(X.float(), logits, w1, s1, w2, s2, k)
+
+
 # ---- refusals --------------------------------------------------------------------------
 
 def test_refusals(drgg):
