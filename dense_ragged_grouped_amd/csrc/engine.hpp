@@ -938,6 +938,11 @@ struct IssuePlan {
     static constexpr int prologue = after(0, -1);                              // wait for stage 0
 };
 
+// A kernel's own loads for a tile (to LDS, in flight beside the stages'): none.
+struct NoLoads {
+    __device__ __forceinline__ void operator()(const TileInfo&) const {}
+};
+
 // Persistent tile loop over the stage pipeline.  `more()` tells whether this
 // workgroup has another tile and `next(t)` decodes it; `finish(t, mma)`
 // writes a finished tile from the accumulators.  Every step has the same
@@ -947,8 +952,12 @@ struct IssuePlan {
 // "loaded" with every lane masked, which writes zeros to LDS without
 // touching memory, so the MFMAs of a padding step add zeros and no branch is
 // taken around the accumulators.  The next tile is decoded at the start of
-// step nk4-4, whose loads fetch its first stage.  Must be called by all
-// threads.
+// step nk4-4, whose loads fetch its first stage.  `loads(t)` may issue LDS
+// loads that belong to a tile: it is called once per tile, before the first
+// tile's stages or else right after the barrier of the step that decodes the
+// tile (so after every wave has left the epilogue before the current tile),
+// and what it loads has landed for every wave by the tile's epilogue.  Must be
+// called by all threads.
 template <int BM, int BN, bool AK, bool BK, int WAVES = kGemmWaves, class El = Bf16, bool PAIRED_B = false>
 struct TileRunner {
     using Mma = TileMma<BM, BN, AK, BK, WAVES, El>;
@@ -1068,8 +1077,8 @@ struct TileRunner {
     }
 
     // Step kt of the current tile; ST = kt % 4; FIRST for step 0.
-    template <int ST, bool FIRST = false, class Next>
-    __device__ __forceinline__ void step(int kt, Next& next) {
+    template <int ST, bool FIRST = false, class Next, class Loads>
+    __device__ __forceinline__ void step(int kt, Next& next, Loads& loads) {
         constexpr int NX = (ST + 1) % kStages;
         constexpr int STO = (ST + kStages - 1) % kStages;
         // with kBar2 an even step issues the deferred loads of step kt-1 (for
@@ -1099,6 +1108,10 @@ struct TileRunner {
             wait_vm_lgkm<kBar2 ? 0 : Plan::at_barrier(4 + ST)>();
             barrier_nofence();
         }
+        if constexpr (ST == kReinitST && !std::is_same<Loads, NoLoads>::value) {
+            static_assert(!kBar2 || (ST & 1), "the decoding step passes a barrier");
+            if (kt - ST + kStages == nk4 && has_next) loads(nxt);
+        }
         // sub-step 1: its MFMAs; the loads into the buffers just freed; the
         // sub-step 0 fragments of stage kt+1
         if constexpr (kBar2 && (ST & 1)) {
@@ -1118,13 +1131,14 @@ struct TileRunner {
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    template <class More, class Next, class Finish>
-    __device__ __forceinline__ void run(More more, Next next, Finish finish) {
+    template <class More, class Next, class Finish, class Loads = NoLoads>
+    __device__ __forceinline__ void run(More more, Next next, Finish finish, Loads loads = Loads{}) {
         if (!more()) return;
         next(cur);
         nk = stages_of(cur);
         nk4 = round4(nk);
         has_next = false;
+        loads(cur);
         la.init(cur.A);
         lb.init(cur.B);
         if constexpr (kBar2) {
@@ -1157,19 +1171,19 @@ struct TileRunner {
             nk_nxt = 0;
             int kt0 = 0;
             if constexpr (kPeel) {
-                step<0, true>(0, next);
-                step<1>(1, next);
-                step<2>(2, next);
-                step<3>(3, next);
+                step<0, true>(0, next, loads);
+                step<1>(1, next, loads);
+                step<2>(2, next, loads);
+                step<3>(3, next, loads);
                 kt0 = kStages;
             } else {
                 mma.zero();
             }
             for (int kt = kt0; kt < nk4; kt += kStages) {
-                step<0>(kt, next);
-                step<1>(kt + 1, next);
-                step<2>(kt + 2, next);
-                step<3>(kt + 3, next);
+                step<0>(kt, next, loads);
+                step<1>(kt + 1, next, loads);
+                step<2>(kt + 2, next, loads);
+                step<3>(kt + 3, next, loads);
             }
             finish(cur, mma);
             if (!has_next) break;

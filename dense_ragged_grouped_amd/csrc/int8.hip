@@ -25,6 +25,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
+// silu(g) u = g u / (1 + exp(-g)).  The exponential and the reciprocal are the
+// hardware's (within 1 ulp each): with the library's expf and a correctly
+// rounded division the gate was the larger part of the gated product's
+// epilogue.  exp(-g) overflows to infinity below g = -88 and the result is 0.
+__device__ __forceinline__ float gate(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
+}
+
 // ---------------------------------------------------------------------------
 // quantisation
 //
@@ -185,8 +193,7 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(Int8Args a) {
                 const int64_t ni = min(n + i, NO - 1);
                 y[i] = (float)c0[i] * a.ws[(int64_t)e * a.N + ni] * xs;
                 if constexpr (GATED) {
-                    const float u = (float)c1[i] * a.ws[(int64_t)e * a.N + NO + ni] * xs;
-                    y[i] = y[i] / (1.f + expf(-y[i])) * u;
+                    y[i] = gate(y[i], (float)c1[i] * a.ws[(int64_t)e * a.N + NO + ni] * xs);
                 }
             }
             if (n < NO) {   // NO is a multiple of 4
@@ -241,39 +248,54 @@ __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
                       (int32_t)K2, NO * a.K};
         w += G;
     };
+    // A tile's scales: BM of its tokens, then BN of its weight rows (gated:
+    // BN/2 gate, then BN/2 up), 64 per wave load.  Two buffers: the next
+    // tile's land while the current one is computed.  Positions past the
+    // tile's rows and columns hold zeros.
+    __shared__ __attribute__((aligned(256))) float scales[2][BM + BN];
+    int put = 0, got = 0;
+    auto loads = [&](const TileInfo& t) {
+        const int lane = threadIdx.x & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const float* ws = a.ws + (int64_t)t.e * a.N + t.o1;
+#pragma unroll
+        for (int c0 = 0; c0 < BM + BN; c0 += 64 * WAVES) {
+            const int c = c0 + wave * 64;   // of the tile's BM + BN scales
+            if (c >= BM + BN) break;
+            const bool up = GATED && c >= BM + BC;
+            const float* from = c < BM ? a.xs + t.o0 + c : ws + (up ? NO - BC : 0) + (c - BM);
+            const int left = c < BM ? t.rows - c : t.cols - (c - BM - (up ? BC : 0));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                make_rsrc(from), (lds_void_t*)((lds_t*)scales[put] + c * 4), 4, lane < left ? lane * 4 : kOOB, 0, 0, 0);
+        }
+        put ^= 1;
+    };
     auto finish = [&](const TileInfo& t, const Mma& mma) {
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int rb = GATED ? Mma::wave_col(wave) / 2 : Mma::wave_col(wave);
-        const float* xs = a.xs + t.o0;
-        const float* ws = a.ws + (int64_t)t.e * a.N + t.o1;
+        typedef const __attribute__((address_space(3))) float lds_f32;
+        typedef const __attribute__((address_space(3))) f32x4 lds_f32x4;
+        const lds_t* sc = (const lds_t*)scales[got];
+        got ^= 1;
         float sx[Mma::kBI];
-        f32x4 sw[GATED ? 2 : 1][NJ][4];
 #pragma unroll
         for (int i = 0; i < Mma::kBI; ++i)
-            sx[i] = xs[min(Mma::wave_row(wave) + 32 * i + (lane & 31), t.rows - 1)];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                // cols is a multiple of 8: the last four stand in for those past the end
-                const int c = min(rb + 32 * j + 8 * q + 4 * (lane >> 5), t.cols - 4);
-                sw[0][j][q] = *reinterpret_cast<const f32x4*>(ws + c);
-                if constexpr (GATED) sw[1][j][q] = *reinterpret_cast<const f32x4*>(ws + NO + c);
-            }
+            sx[i] = *reinterpret_cast<lds_f32*>(sc + 4 * (Mma::wave_row(wave) + 32 * i + (lane & 31)));
+        const lds_t* sw = sc + 4 * (BM + rb + 4 * (lane >> 5));
         auto value = [&](int i, int j, int q) {
+            const f32x4 w = *reinterpret_cast<lds_f32x4*>(sw + 4 * (32 * j + 8 * q));
             f32x4 y;
+            if constexpr (GATED) {
+                const f32x4 v = *reinterpret_cast<lds_f32x4*>(sw + 4 * (BC + 32 * j + 8 * q));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int c = 4 * q + r;
-                if constexpr (GATED) {
-                    const float g = (float)mma.acc[i][2 * j][c] * sw[0][j][q][r] * sx[i];
-                    const float u = (float)mma.acc[i][2 * j + 1][c] * sw[1][j][q][r] * sx[i];
-                    y[r] = g / (1.f + expf(-g)) * u;
-                } else {
-                    y[r] = (float)mma.acc[i][j][c] * sw[0][j][q][r] * sx[i];
-                }
+                for (int r = 0; r < 4; ++r)
+                    y[r] = gate((float)mma.acc[i][2 * j][4 * q + r] * w[r] * sx[i],
+                                (float)mma.acc[i][2 * j + 1][4 * q + r] * v[r] * sx[i]);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[r] = (float)mma.acc[i][j][4 * q + r] * w[r] * sx[i];
             }
             return y;
         };
@@ -283,7 +305,7 @@ __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
     };
     TileRunner<BM, BN, true, true, WAVES, Int8, GATED> runner;
     runner.st = stg;
-    runner.run(more, next, finish);
+    runner.run(more, next, finish, loads);
 }
 
 template <int BM, int BN, int WAVES>
