@@ -27,11 +27,6 @@ drgg_status check_route(int64_t T, int32_t E, int32_t k) {
     return check_pairs(T, k);
 }
 
-size_t route_table_bytes(int64_t T, int32_t E) {
-    const int64_t blocks = route_blocks(T);
-    return blocks > 1 ? (size_t)((blocks + 1) * E * 4) : 0;   // at most 2^25 blocks of 1024 experts
-}
-
 drgg_status check_rows(int64_t T, int32_t k, int64_t H, drgg_dtype dt) {
     if (dt != DRGG_BF16 && dt != DRGG_FP32) return DRGG_EINVAL;
     drgg_status st = check_pairs(T, k);
@@ -127,7 +122,7 @@ drgg_status moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int 
         if (!aligned16(workspace)) return DRGG_EALIGN;
     }
     return launch_status(launch_moe_route(logits, T, E, k, renormalize != 0, experts, weights, group_offsets, positions,
-                                          static_cast<int32_t*>(workspace), stream));
+                                          workspace, stream));
 }
 
 drgg_status moe_route_grad(const float* dweights, const float* logits, const int32_t* experts, const float* weights,
@@ -239,7 +234,7 @@ drgg_status moe_ffn_int8(const void* X, const float* logits, const int8_t* W1q, 
     if (st != DRGG_OK) return st;
     const int64_t R = T * k;
     hipError_t e = launch_moe_route(logits, T, E, k, renormalize != 0, experts, weights, offsets, positions,
-                                    reinterpret_cast<int32_t*>(ws + L.table), stream);
+                                    ws + L.table, stream);
     if (e == hipSuccess) e = launch_quantize_int8(X, true, T, H, positions, k, x, xs, stream);
     if (e == hipSuccess)
         e = launch_int8(Int8Args{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E}, true, false, cus, stream);

@@ -85,9 +85,9 @@ hipError_t launch_hold_cus(int n, uint64_t ticks, hipStream_t s);
 
 // ---- the expert layer's operators (moe.hip, int8.hip) -----------------------
 
-int64_t route_blocks(int64_t T);   // workgroups of the selection; its table has (blocks + 1) * E words
+size_t route_table_bytes(int64_t T, int32_t E);   // the selection's workspace; 0 for one workgroup
 hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
-                            float* weights, int32_t* offsets, int32_t* positions, int32_t* table, hipStream_t s);
+                            float* weights, int32_t* offsets, int32_t* positions, void* table, hipStream_t s);
 hipError_t launch_moe_route_grad(const float* dweights, const float* logits, const int32_t* experts,
                                  const float* weights, int64_t T, int32_t E, int32_t k, int renormalize,
                                  float* dlogits, hipStream_t s);

@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "internal.hpp"
 #include "plan.hpp"
 
@@ -20,12 +22,14 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 // ---------------------------------------------------------------------------
 // selection
 //
-// One wave per token.  Lane l holds the logits of experts 4l .. 4l+3 of every
-// 256 (V groups of 256 cover E).  A logit is compared through a 32-bit key
-// whose unsigned order is the order of the values (NaN above +inf, -0 equal
-// to +0); key 0 marks an expert already taken or past E.  Each of the k
-// rounds takes the largest key of the wave, at the lowest expert index among
-// equals; lane j keeps round j's choice.
+// Sixteen lanes per token, one DPP row, so that a wave works on four tokens
+// and a maximum over a token's lanes is four rotations in the vector unit.
+// Lane l of the row holds the logits of experts 64c + 4l + i in key[4c + i].
+// A logit is compared through a 32-bit key whose unsigned order is the order
+// of the values (NaN above +inf, -0 equal to +0); key 0 marks an expert
+// already taken or past E.  Each of the k rounds takes the largest key of the
+// row, at the lowest expert index among equals; lane j % 16 keeps round j's
+// choice in its slot j / 16.
 
 __device__ __forceinline__ uint32_t order_key(float v) {
     if (v != v) return 0xFFFFFFFFu;
@@ -36,40 +40,48 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);   // NaN: 0x7FFFFFFF, a NaN
 }
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint32_t o = __shfl_xor(v, m, 64);
-        v = o > v ? o : v;
-    }
-    return v;
+// v of the lane N places on in the row of 16 (cyclic)
+template <int N>
+__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
-    return v;
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    v = max(v, row_rotate<8>(v));
+    v = max(v, row_rotate<4>(v));
+    v = max(v, row_rotate<2>(v));
+    return max(v, row_rotate<1>(v));
+}
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+    v = min(v, row_rotate<8>(v));
+    v = min(v, row_rotate<4>(v));
+    v = min(v, row_rotate<2>(v));
+    return min(v, row_rotate<1>(v));
+}
+// the same bits in all lanes: every lane adds the same pairs of pairs
+__device__ __forceinline__ float row_sum(float v) {
+    v += __uint_as_float(row_rotate<8>(__float_as_uint(v)));
+    v += __uint_as_float(row_rotate<4>(__float_as_uint(v)));
+    v += __uint_as_float(row_rotate<2>(__float_as_uint(v)));
+    return v + __uint_as_float(row_rotate<1>(__float_as_uint(v)));
 }
 
-// The logits of one token as keys (expert 256*c + 4*lane + i in key[c][i]).
+// The logits of one token as keys; none when !live.
 template <int V>
-__device__ __forceinline__ void load_keys(uint32_t (&key)[V][4], const float* row, int E, int lane) {
+__device__ __forceinline__ void load_keys(uint32_t (&key)[V], const float* row, int E, int l, bool live) {
     const bool vec = (E & 3) == 0;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-        const int e = 256 * c + 4 * lane;
+    for (int c = 0; c < V / 4; ++c) {
+        const int e = 64 * c + 4 * l;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
         if (vec) {
-            if (e < E) {
-                const f32x4 v = *reinterpret_cast<const f32x4*>(row + e);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) key[c][i] = order_key(v[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) key[c][i] = 0;
-            }
+            if (live && e < E) v = *reinterpret_cast<const f32x4*>(row + e);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) key[c][i] = e + i < E ? order_key(row[e + i]) : 0;
+            for (int i = 0; i < 4; ++i)
+                if (live && e + i < E) v[i] = row[e + i];
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) key[4 * c + i] = live && e + i < E ? order_key(v[i]) : 0;
     }
 }
 
@@ -79,13 +91,19 @@ struct RouteArgs {
     float* weights;
     int32_t* offsets;
     int32_t* positions;
-    int32_t* table;   // [blocks][E] counts, then their exclusive prefix over the blocks; then [E] totals
+    void* table;   // counts per block and expert, see moe_select_kernel
     int64_t T, blocks;
     int32_t E, k, renormalize;
 };
 
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
-constexpr int kRouteTokens = 64;   // tokens per block: one 64-bit mask per expert
+constexpr int kRouteTokens = 64;   // tokens per block: four per wave, one 64-bit mask per expert
+// up to this many blocks moe_place_kernel sums the earlier blocks' counts
+// itself (each block reads every count, E bytes per block: 64 KB of L2 reads
+// each for 16384 tokens on 256 experts); beyond, a scan kernel does it once
+constexpr int64_t kRouteBytes = 512;
+
+__device__ __forceinline__ int table_stride(int E) { return (E + 3) & ~3; }
 
 // Exclusive scan of one value per thread (thread order), of at most 1024
 // threads; `tmp` holds a word per wave.  Called by all threads.
@@ -108,81 +126,70 @@ __device__ __forceinline__ int32_t block_prefix(int32_t v, int32_t* tmp) {
 // the same expert.  The rank comes from one bit per token and expert: the
 // tokens of a block are ordered by their bit, so ranks and counts are
 // popcounts, whatever order the bits were set in.  With a single block the
-// offsets and final positions are written here; otherwise the counts go to
-// the table and positions hold the ranks for moe_place_kernel.
-template <int V>
+// offsets and final positions are written here; otherwise positions hold the
+// ranks for moe_place_kernel and the counts go to the table: bytes (at most
+// 64 each) [blocks][E rounded up to 4], or with more than kRouteBytes blocks
+// words [blocks][E] for moe_scan_kernel.
+// Bound by the vector unit: 8 us for 16384 tokens, k = 8 of 256 experts
+// (2.1 TB/s of logits); with a wave per token and shuffles through LDS it
+// was 21 us.
+template <int V, int S>
 __global__ __launch_bounds__(kRouteThreads) void moe_select_kernel(RouteArgs a) {
-    __shared__ unsigned long long mask[256 * V];
-    __shared__ int32_t start[256 * V], tmp[kRouteWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ unsigned long long mask[16 * V];
+    __shared__ int32_t start[16 * V], tmp[kRouteWaves];
+    const int lane = threadIdx.x & 63, l = lane & 15;
     const int E = a.E, k = a.k;
     for (int e = threadIdx.x; e < E; e += kRouteThreads) mask[e] = 0;
     __syncthreads();
-    const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens;
-    constexpr int kPer = kRouteTokens / kRouteWaves;
-    int32_t mine[kPer];
+    const int tl = threadIdx.x >> 4;   // token of the block
+    const int64_t t = (int64_t)blockIdx.x * kRouteTokens + tl;
+    const bool live = t < a.T;
+    uint32_t key[V], kept[S], top = 0;
+    int32_t mine[S];
+    load_keys<V>(key, a.logits + t * E, E, l, live);
+    for (int j = 0; j < k; ++j) {
+        uint32_t m = key[0];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int tl = i * kRouteWaves + wave;
-        const int64_t t = t0 + tl;
-        mine[i] = 0;
-        if (t >= a.T) continue;
-        uint32_t key[V][4];
-        load_keys<V>(key, a.logits + t * E, E, lane);
-        uint32_t top = 0, kept = 0;
-        for (int j = 0; j < k; ++j) {
-            uint32_t m = 0;
+        for (int i = 1; i < V; ++i) m = max(m, key[i]);
+        const uint32_t best = row_max(m);
+        uint32_t at = 0xFFFFu;
 #pragma unroll
-            for (int c = 0; c < V; ++c)
+        for (int i = V - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)(64 * (i >> 2) + (i & 3)) : at;
+        const uint32_t e = row_min(at == 0xFFFFu ? at : at + 4 * l);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) m = key[c][q] > m ? key[c][q] : m;
-            const uint32_t best = wave_max_u32(m);
-            // the lowest expert with that key: groups in order, then lanes, then the lane's four
-            int32_t e = 0;
-            bool done = false;
+        for (int i = 0; i < V; ++i) key[i] = e == (uint32_t)(64 * (i >> 2) + (i & 3)) + 4 * l ? 0u : key[i];
+        if (j == 0) top = best;
 #pragma unroll
-            for (int c = 0; c < V; ++c) {
-                int q = 4;
-#pragma unroll
-                for (int r = 3; r >= 0; --r) q = key[c][r] == best ? r : q;
-                const unsigned long long has = __ballot(q < 4);
-                if (!done && has) {
-                    const int l = __ffsll((long long)has) - 1;
-                    e = 256 * c + 4 * l + __shfl(q, l, 64);
-                    if (lane == l) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) key[c][r] = r == q ? 0 : key[c][r];
-                    }
-                    done = true;
-                }
+        for (int s = 0; s < S; ++s)
+            if (j == 16 * s + l) {
+                kept[s] = best;
+                mine[s] = (int32_t)e;
             }
-            if (j == 0) top = best;
-            if (lane == j) {
-                kept = best;
-                mine[i] = e;
-            }
-        }
-        // softmax over the chosen (lanes 0 .. k-1), or over all experts
-        const float most = key_value(top), v = key_value(kept);
-        const bool none = most == -INFINITY;   // every expert is masked: all weights 0
-        float p = lane < k && !none ? expf(v - most) : 0.f, total;
-        if (a.renormalize) {
-            total = wave_sum(p);
-        } else {
-            // the keys of the chosen are gone: their terms are the p of lanes 0 .. k-1
-            float s = p;
-            if (!none) {
+    }
+    // softmax over the chosen, or over all experts (the keys of the chosen
+    // are gone, their terms are the p)
+    const float most = key_value(top);
+    const bool none = most == -INFINITY;   // every expert is masked: all weights 0
+    float p[S], total = 0.f;
 #pragma unroll
-                for (int c = 0; c < V; ++c)
+    for (int s = 0; s < S; ++s) {
+        p[s] = 16 * s + l < k && !none ? expf(key_value(kept[s]) - most) : 0.f;
+        total += p[s];
+    }
+    if (!a.renormalize && !none) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) s += key[c][q] ? expf(key_value(key[c][q]) - most) : 0.f;
+        for (int i = 0; i < V; ++i) total += key[i] ? expf(key_value(key[i]) - most) : 0.f;
+    }
+    total = row_sum(total);
+    if (live) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int j = 16 * s + l;
+            if (j < k) {
+                a.experts[t * k + j] = mine[s];
+                a.weights[t * k + j] = none ? 0.f : p[s] / total;
+                atomicOr(&mask[mine[s]], 1ull << tl);
             }
-            total = wave_sum(s);
-        }
-        if (lane < k) {
-            a.experts[t * k + lane] = mine[i];
-            a.weights[t * k + lane] = none ? 0.f : p / total;
-            atomicOr(&mask[mine[i]], 1ull << tl);
         }
     }
     __syncthreads();
@@ -196,26 +203,32 @@ __global__ __launch_bounds__(kRouteThreads) void moe_select_kernel(RouteArgs a) 
             if ((int)threadIdx.x == E - 1) a.offsets[E] = s + n;
         }
         __syncthreads();
+    } else if (a.blocks <= kRouteBytes) {
+        const int stride = table_stride(E);
+        for (int e = threadIdx.x; e < stride; e += kRouteThreads)
+            static_cast<uint8_t*>(a.table)[(int64_t)blockIdx.x * stride + e] = e < E ? (uint8_t)__popcll(mask[e]) : 0;
     } else {
         for (int e = threadIdx.x; e < E; e += kRouteThreads)
-            a.table[(int64_t)blockIdx.x * E + e] = __popcll(mask[e]);
+            static_cast<int32_t*>(a.table)[(int64_t)blockIdx.x * E + e] = __popcll(mask[e]);
     }
+    if (!live) return;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int tl = i * kRouteWaves + wave;
-        const int64_t t = t0 + tl;
-        if (t >= a.T || lane >= k) continue;
-        const int e = mine[i];
-        const int32_t r = __popcll(mask[e] & ((1ull << tl) - 1));
-        a.positions[t * k + lane] = single ? start[e] + r : r;
+    for (int s = 0; s < S; ++s) {
+        const int j = 16 * s + l;
+        if (j < k) {
+            const int32_t r = __popcll(mask[mine[s]] & ((1ull << tl) - 1));
+            a.positions[t * k + j] = single ? start[mine[s]] + r : r;
+        }
     }
 }
 
-// The table's columns to exclusive prefixes over the blocks, and each
-// expert's total.  One lane per expert; the 16 waves of a workgroup each take
-// a run of blocks, sum it, and write its prefixes.
+// More than kRouteBytes blocks: the table's columns to exclusive prefixes over
+// the blocks, and each expert's total after them.  One lane per expert; the
+// 16 waves of a workgroup each take a run of blocks, sum it, and write its
+// prefixes.
 __global__ __launch_bounds__(kRouteThreads) void moe_scan_kernel(RouteArgs a) {
     __shared__ int32_t sums[kRouteWaves][64];
+    int32_t* table = static_cast<int32_t*>(a.table);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int e = blockIdx.x * 64 + lane;
     const bool ok = e < a.E;
@@ -223,30 +236,64 @@ __global__ __launch_bounds__(kRouteThreads) void moe_scan_kernel(RouteArgs a) {
     const int64_t lo = min(wave * per, a.blocks), hi = min(lo + per, a.blocks);
     int32_t s = 0;
     if (ok)
-        for (int64_t b = lo; b < hi; ++b) s += a.table[b * a.E + e];
+        for (int64_t b = lo; b < hi; ++b) s += table[b * a.E + e];
     sums[wave][lane] = s;
     __syncthreads();
     int32_t acc = 0;
     for (int w = 0; w < wave; ++w) acc += sums[w][lane];
     if (ok) {
         for (int64_t b = lo; b < hi; ++b) {
-            const int32_t n = a.table[b * a.E + e];
-            a.table[b * a.E + e] = acc;
+            const int32_t n = table[b * a.E + e];
+            table[b * a.E + e] = acc;
             acc += n;
         }
-        if (wave == kRouteWaves - 1) a.table[a.blocks * a.E + e] = acc;
+        if (wave == kRouteWaves - 1) table[a.blocks * a.E + e] = acc;
     }
 }
 
-// positions += the expert's offset + its pairs in earlier blocks.
+// positions += the expert's offset + its pairs in earlier blocks.  BYTES: the
+// block sums the count bytes of all blocks itself, four experts per thread
+// and the blocks cut into slices over the other threads; two 16-bit sums per
+// word hold them (kRouteBytes * 64 < 2^16).
+template <bool BYTES>
 __global__ __launch_bounds__(kRouteThreads) void moe_place_kernel(RouteArgs a) {
     __shared__ int32_t base[kMaxExperts], tmp[kRouteWaves];
-    const int E = a.E;
-    const int tid = threadIdx.x;
-    const int32_t n = tid < E ? a.table[a.blocks * E + tid] : 0;
+    __shared__ u32x4 part[BYTES ? kRouteThreads : 1];
+    const int E = a.E, tid = threadIdx.x;
+    int32_t before = 0, n = 0;   // of expert tid: pairs in earlier blocks, and in all
+    if constexpr (BYTES) {
+        static_assert(kRouteBytes * kRouteTokens < 65536, "16-bit sums");
+        const int quads = table_stride(E) / 4, slices = kRouteThreads / quads;
+        const int q = tid % quads, sl = tid / quads, blocks = (int)a.blocks, me = (int)blockIdx.x;
+        u32x4 s = {0, 0, 0, 0};   // earlier: experts 0 and 2, 1 and 3 of the quad; all: the same
+        if (sl < slices) {
+            const uint32_t* col = static_cast<const uint32_t*>(a.table) + q;
+            for (int b = sl; b < blocks; b += slices) {
+                const uint32_t v = col[(int64_t)b * quads];
+                const uint32_t even = v & 0x00FF00FFu, odd = (v >> 8) & 0x00FF00FFu;
+                s[0] += b < me ? even : 0;
+                s[1] += b < me ? odd : 0;
+                s[2] += even;
+                s[3] += odd;
+            }
+        }
+        part[tid] = s;
+        __syncthreads();
+        if (tid < E) {
+            const int i = tid & 3;
+            for (int w = 0; w < slices; ++w) {
+                const u32x4 v = part[w * quads + tid / 4];
+                before += (v[i & 1] >> (8 * (i & 2))) & 0xFFFFu;
+                n += (v[2 + (i & 1)] >> (8 * (i & 2))) & 0xFFFFu;
+            }
+        }
+    } else if (tid < E) {
+        before = static_cast<const int32_t*>(a.table)[(int64_t)blockIdx.x * E + tid];
+        n = static_cast<const int32_t*>(a.table)[a.blocks * E + tid];
+    }
     const int32_t s = block_prefix(n, tmp);
     if (tid < E) {
-        base[tid] = s + a.table[(int64_t)blockIdx.x * E + tid];
+        base[tid] = s + before;
         if (blockIdx.x == 0) {
             a.offsets[tid] = s;
             if (tid == E - 1) a.offsets[E] = s + n;
@@ -268,86 +315,73 @@ struct RouteGradArgs {
     int32_t E, k, renormalize;
 };
 
-// dlogits of one token per wave.  With s = sum_j w_j dw_j:
+// dlogits, sixteen lanes per token as above.  With s = sum_j w_j dw_j:
 //   softmax over the chosen: w_j (dw_j - s) at the chosen, 0 elsewhere;
-//   softmax over all: p_e ((dw at the chosen, else 0) - s), where the p of
-//   every expert is recomputed from the logits.
-// Lane j holds pair j; every lane writes its experts 4l .. 4l+3 of each 256.
+//   softmax over all: p_e (dw_e - s), dw_e = 0 but at the chosen, where p_e
+//   is w_j; the p are recomputed from the logits.
+// The row is first written as if no expert were chosen, then lane j writes
+// the chosen ones; the fence between makes the second store the last.
 template <int V>
 __global__ __launch_bounds__(256) void moe_route_grad_kernel(RouteGradArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= a.T) return;
+    const int l = threadIdx.x & 15;
+    const int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int E = a.E, k = a.k;
-    int32_t e = -1;
-    float w = 0.f, d = 0.f;
-    if (lane < k) {
-        e = a.experts[t * k + lane];
-        w = a.weights[t * k + lane];
-        d = a.dweights[t * k + lane];
-    }
-    const float s = wave_sum(w * d);
-    float g[V][4];
+    const bool live = t < a.T;
+    float s = 0.f;
+    if (live)
+        for (int j = l; j < k; j += 16) s += a.weights[t * k + j] * a.dweights[t * k + j];
+    s = row_sum(s);
+    float g[V];
     if (a.renormalize) {
-        const float v = w * (d - s);
 #pragma unroll
-        for (int c = 0; c < V; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[c][i] = 0.f;
-        for (int j = 0; j < k; ++j) {
-            const int32_t ej = __shfl(e, j, 64);
-            const float vj = __shfl(v, j, 64);
-#pragma unroll
-            for (int c = 0; c < V; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) g[c][i] = ej == 256 * c + 4 * lane + i ? vj : g[c][i];
-        }
+        for (int i = 0; i < V; ++i) g[i] = 0.f;
     } else {
-        uint32_t key[V][4], m = 0;
-        load_keys<V>(key, a.logits + t * E, E, lane);
+        uint32_t key[V], m = 0;
+        load_keys<V>(key, a.logits + t * E, E, l, live);
 #pragma unroll
-        for (int c = 0; c < V; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                m = key[c][i] > m ? key[c][i] : m;
-                g[c][i] = -s;
-            }
-        for (int j = 0; j < k; ++j) {
-            const int32_t ej = __shfl(e, j, 64);
-            const float dj = __shfl(d, j, 64);
-#pragma unroll
-            for (int c = 0; c < V; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) g[c][i] = ej == 256 * c + 4 * lane + i ? dj - s : g[c][i];
-        }
-        const float most = key_value(wave_max_u32(m));
+        for (int i = 0; i < V; ++i) m = max(m, key[i]);
+        const float most = key_value(row_max(m));
         const bool none = most == -INFINITY;
-        float total = 0.f, p[V][4];
+        float total = 0.f;
 #pragma unroll
-        for (int c = 0; c < V; ++c)
+        for (int i = 0; i < V; ++i) {
+            g[i] = key[i] && !none ? expf(key_value(key[i]) - most) : 0.f;
+            total += g[i];
+        }
+        total = row_sum(total);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[c][i] = key[c][i] && !none ? expf(key_value(key[c][i]) - most) : 0.f;
-                total += p[c][i];
-            }
-        total = wave_sum(total);
-#pragma unroll
-        for (int c = 0; c < V; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[c][i] = none ? 0.f : p[c][i] / total * g[c][i];
+        for (int i = 0; i < V; ++i) g[i] = none ? 0.f : -s * (g[i] / total);
     }
     float* out = a.dlogits + t * E;
+    if (live) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-        const int e0 = 256 * c + 4 * lane;
-        if ((E & 3) == 0) {
-            if (e0 < E) *reinterpret_cast<f32x4*>(out + e0) = f32x4{g[c][0], g[c][1], g[c][2], g[c][3]};
-        } else {
+        for (int c = 0; c < V / 4; ++c) {
+            const int e = 64 * c + 4 * l;
+            if ((E & 3) == 0) {
+                if (e < E) *reinterpret_cast<f32x4*>(out + e) = f32x4{g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]};
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (e0 + i < E) out[e0 + i] = g[c][i];
+                for (int i = 0; i < 4; ++i)
+                    if (e + i < E) out[e + i] = g[4 * c + i];
+            }
         }
     }
+    __syncthreads();   // the row's stores are performed before the ones below
+    if (live)
+        for (int j = l; j < k; j += 16) {
+            const int32_t e = a.experts[t * k + j];
+            if (e >= 0 && e < E) out[e] = a.weights[t * k + j] * (a.dweights[t * k + j] - s);
+        }
+}
+
+// fn(V), the keys per lane for E experts, as an integral constant
+template <class Fn>
+void for_experts(int32_t E, Fn&& fn) {
+    if (E <= 64) fn(std::integral_constant<int, 4>{});
+    else if (E <= 128) fn(std::integral_constant<int, 8>{});
+    else if (E <= 256) fn(std::integral_constant<int, 16>{});
+    else if (E <= 512) fn(std::integral_constant<int, 32>{});
+    else fn(std::integral_constant<int, 64>{});
 }
 
 // ---------------------------------------------------------------------------
@@ -501,40 +535,46 @@ dim3 row_block(int64_t C) {
 }  // namespace
 
 // one block also without tokens: it writes the offsets
-int64_t route_blocks(int64_t T) { return T > 0 ? ceil_div(T, kRouteTokens) : 1; }
+static int64_t route_blocks(int64_t T) { return T > 0 ? ceil_div(T, kRouteTokens) : 1; }
+
+size_t route_table_bytes(int64_t T, int32_t E) {
+    const int64_t n = route_blocks(T);   // at most 2^25, so the table stays below 2^38 bytes
+    if (n == 1) return 0;
+    return (size_t)(n <= kRouteBytes ? n * round_up(E, 4) : (n + 1) * E * 4);
+}
 
 hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
-                            float* weights, int32_t* offsets, int32_t* positions, int32_t* table, hipStream_t s) {
+                            float* weights, int32_t* offsets, int32_t* positions, void* table, hipStream_t s) {
     RouteArgs a{logits, experts, weights, offsets, positions, table, T, route_blocks(T), E, k, renormalize};
     const dim3 grid((unsigned)a.blocks), block(kRouteThreads);
     timing_mark("moe_select_kernel", s);
-    if (E <= 256) hipLaunchKernelGGL(moe_select_kernel<1>, grid, block, 0, s, a);
-    else if (E <= 512) hipLaunchKernelGGL(moe_select_kernel<2>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(moe_select_kernel<4>, grid, block, 0, s, a);
-    hipError_t err = hipGetLastError();
-    if (err == hipSuccess && a.blocks > 1) {
+    for_experts(E, [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        if (k <= 16) hipLaunchKernelGGL((moe_select_kernel<V, 1>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((moe_select_kernel<V, 4>), grid, block, 0, s, a);
+    });
+    if (a.blocks > kRouteBytes) {
         timing_mark("moe_scan_kernel", s);
         hipLaunchKernelGGL(moe_scan_kernel, dim3((unsigned)ceil_div(E, 64)), block, 0, s, a);
-        err = hipGetLastError();
-        if (err == hipSuccess) {
-            timing_mark("moe_place_kernel", s);
-            hipLaunchKernelGGL(moe_place_kernel, grid, block, 0, s, a);
-            err = hipGetLastError();
-        }
+    }
+    if (a.blocks > 1) {
+        timing_mark("moe_place_kernel", s);
+        if (a.blocks > kRouteBytes) hipLaunchKernelGGL(moe_place_kernel<false>, grid, block, 0, s, a);
+        else hipLaunchKernelGGL(moe_place_kernel<true>, grid, block, 0, s, a);
     }
     timing_end(s);
-    return err;
+    return hipGetLastError();
 }
 
 hipError_t launch_moe_route_grad(const float* dweights, const float* logits, const int32_t* experts,
                                  const float* weights, int64_t T, int32_t E, int32_t k, int renormalize,
                                  float* dlogits, hipStream_t s) {
     RouteGradArgs a{dweights, logits, experts, weights, dlogits, T, E, k, renormalize};
-    const dim3 grid((unsigned)ceil_div(T, 4)), block(256);
+    const dim3 grid((unsigned)ceil_div(T, 16)), block(256);
     timing_mark("moe_route_grad_kernel", s);
-    if (E <= 256) hipLaunchKernelGGL(moe_route_grad_kernel<1>, grid, block, 0, s, a);
-    else if (E <= 512) hipLaunchKernelGGL(moe_route_grad_kernel<2>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(moe_route_grad_kernel<4>, grid, block, 0, s, a);
+    for_experts(E, [&](auto v) {
+        hipLaunchKernelGGL(moe_route_grad_kernel<decltype(v)::value>, grid, block, 0, s, a);
+    });
     timing_end(s);
     return hipGetLastError();
 }

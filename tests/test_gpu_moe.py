@@ -129,6 +129,21 @@ def test_route(drgg, T, E, k, kind, renormalize):
         assert not w[np.isneginf(np.take_along_axis(logits, experts, 1))].any()
 
 
+@pytest.mark.parametrize("kind", ["normal", "ties"])
+@pytest.mark.parametrize("T,E,k", [(32768, 7, 3), (32769, 130, 2), (70001, 6, 1)])
+def test_route_many_tokens(drgg, T, E, k, kind):
+    logits = make_logits(kind, T, E, T + E)
+    r = drgg.moe_route(dev(logits), k)
+    experts = np.argsort(-(logits + 0.0), axis=1, kind="stable")[:, :k]
+    flat = experts.reshape(-1)
+    order = np.argsort(flat, kind="stable")
+    positions = np.empty(T * k, dtype=np.int64)
+    positions[order] = np.arange(T * k)
+    assert np.array_equal(host(r.experts), experts)
+    assert np.array_equal(host(r.positions).reshape(-1), positions)
+    assert np.array_equal(host(r.group_offsets), np.searchsorted(flat[order], np.arange(E + 1)))
+
+
 def test_route_nan_and_infinity(drgg):
     """NaN sorts first (either sign), then +inf; their softmax is NaN, and no other token's is."""
     logits = make_logits("normal", 70, 40, 3)
