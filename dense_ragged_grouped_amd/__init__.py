@@ -325,9 +325,15 @@ def workspace_size(op: int, E: int, M: int, N: int, K: int, out_dtype: int = BF1
 
 # ---- torch marshalling ---------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(dt) -> int:
@@ -726,18 +732,32 @@ def _call(name, stream, tensors, *args):
     """lib.<name>(*args, stream) on the device of `tensors` (None entries
     skipped).  These calls are short, so the usual case -- the tensors on the
     current device, its current stream -- reads the stream's handle directly
-    (torch's accessor for it, 0.1 us; the Stream object and the device guard
+    (torch's accessors, 0.1 us each; the Stream object and the device guard
     cost 3 us)."""
-    torch = _torch()
-    first = tensors[0]
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if stream is None and raw is not None:
-        index = torch.cuda.current_device()
-        if all(t is None or t.get_device() == index for t in tensors):
-            _check(getattr(lib, name)(*args, raw(index)), name)
+    C = _torch()._C
+    if stream is None and _RAW_STREAM:
+        index = C._cuda_getDevice()
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            st = getattr(lib, name)(*args, C._cuda_getCurrentRawStream(index))
+            if st:
+                raise DrggError(st, name)
             return
     with _on_one_device(stream, *tensors):
-        _check(getattr(lib, name)(*args, _stream(first.device, stream)), name)
+        _check(getattr(lib, name)(*args, _stream(tensors[0].device, stream)), name)
+
+
+def _raw_stream_accessors():
+    try:
+        C = _torch()._C
+    except ImportError:
+        return False
+    return hasattr(C, "_cuda_getCurrentRawStream") and hasattr(C, "_cuda_getDevice")
+
+
+_RAW_STREAM = _raw_stream_accessors()
 
 
 def _need_shape(t, dtype, shape, name):

@@ -131,18 +131,23 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
 // ---------------------------------------------------------------------------
 // product, few rows per group
 //
-// A workgroup takes 32 weight rows of one group (gated: 16 gate rows and
-// their 16 up rows) and the group's token rows in blocks of 16; its four
-// waves split K in steps of 64 values and add their integer sums through
+// A workgroup takes NB blocks of 16 weight rows of one group (gated: 16 gate
+// rows and their 16 up rows) and the group's token rows in blocks of 16; its
+// W waves split K in steps of 64 values and add their integer sums through
 // LDS.  Fragments go from memory to registers directly: lane l of a
 // v_mfma_i32_16x16x64_i8 holds values 16*(l/16) .. +15 of row l%16, one
 // 16-byte load, for the weights (first operand) as for the tokens; the result
 // has token l%16 and weight rows 4*(l/16) .. +3 in lane l.
-
-template <bool OUT_BF16, bool GATED>
-__global__ __launch_bounds__(256) void int8_rows_kernel(Int8Args a) {
-    __shared__ i32x4 sums[4][2][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+//
+// Bound by the weights' bytes, each read once from memory (further blocks of
+// tokens find them in L2): U steps are loaded before the first is used, so
+// that a CU has 32 KB and more in flight.
+template <bool OUT_BF16, bool GATED, int NB, int W>
+__global__ __launch_bounds__(64 * W) void int8_rows_kernel(Int8Args a) {
+    constexpr int U = 4;
+    static_assert(!GATED || NB == 2, "a gate block and its up block");
+    __shared__ i32x4 sums[W][NB][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int e = blockIdx.y;
     int64_t lo = 0, hi = a.M;
@@ -151,62 +156,77 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(Int8Args a) {
         hi = min<int64_t>(max<int64_t>(a.offs[e + 1], lo), a.M);
     }
     if (lo >= hi) return;
-    const int64_t NO = GATED ? a.N / 2 : a.N;   // output columns
-    constexpr int kCols = GATED ? 16 : 32;      // of them per workgroup
+    const int64_t NO = GATED ? a.N / 2 : a.N;       // output columns
+    constexpr int kCols = GATED ? 16 : 16 * NB;     // of them per workgroup
     const int64_t n0 = (int64_t)blockIdx.x * kCols;
-    // weight rows of the two blocks of 16; rows past the end repeat the last
-    // one, and their results are not stored
-    const int64_t nb0 = min(n0 + r, NO - 1);
-    const int64_t nb1 = GATED ? NO + nb0 : min(n0 + 16 + r, NO - 1);
-    const int8_t* w0 = a.W + ((int64_t)e * a.N + nb0) * a.K;
-    const int8_t* w1 = a.W + ((int64_t)e * a.N + nb1) * a.K;
+    // weight rows past the end repeat the last one, and their results are not stored
+    const int8_t* w[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int64_t n = GATED ? min(n0 + r, NO - 1) + b * NO : min(n0 + 16 * b + r, NO - 1);
+        w[b] = a.W + ((int64_t)e * a.N + n) * a.K;
+    }
     for (int64_t m0 = lo; m0 < hi; m0 += 16) {
         const int8_t* x = a.X + min(m0 + r, hi - 1) * a.K;
-        i32x4 acc0 = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
-        for (int64_t k0 = wave * 64; k0 < a.K; k0 += 256) {
-            const int64_t k = k0 + 16 * g;
-            i32x4 b = {0, 0, 0, 0}, v0 = b, v1 = b;
-            if (k < a.K) {
-                b = *reinterpret_cast<const i32x4*>(x + k);
-                v0 = *reinterpret_cast<const i32x4*>(w0 + k);
-                v1 = *reinterpret_cast<const i32x4*>(w1 + k);
+        i32x4 acc[NB] = {};
+        for (int k0 = wave * 64; k0 < a.K; k0 += 64 * W * U) {
+            i32x4 fx[U], fw[U][NB];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + 64 * W * u + 16 * g;
+                const bool in = k < a.K;
+                fx[u] = in ? *reinterpret_cast<const i32x4*>(x + k) : i32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    fw[u][b] = in ? *reinterpret_cast<const i32x4*>(w[b] + k) : i32x4{0, 0, 0, 0};
             }
-            acc0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(v0, b, acc0, 0, 0, 0);
-            acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(v1, b, acc1, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][b], fx[u], acc[b], 0, 0, 0);
         }
-        sums[wave][0][lane] = acc0;
-        sums[wave][1][lane] = acc1;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[b];
         __syncthreads();
         const int64_t t = m0 + r;
-        if (wave < (GATED ? 1 : 2) && t < hi) {
+        if (wave < (GATED ? 1 : NB) && t < hi) {
             const float xs = a.xs[t];
             const int64_t n = n0 + 16 * wave + 4 * g;
-            float y[4];
-            i32x4 c0 = sums[0][wave][lane], c1 = sums[0][1][lane];
+            i32x4 c0 = sums[0][wave][lane], c1 = sums[0][NB - 1][lane];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) {
-                c0 += sums[w][wave][lane];
-                c1 += sums[w][1][lane];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t ni = min(n + i, NO - 1);
-                y[i] = (float)c0[i] * a.ws[(int64_t)e * a.N + ni] * xs;
-                if constexpr (GATED) {
-                    y[i] = gate(y[i], (float)c1[i] * a.ws[(int64_t)e * a.N + NO + ni] * xs);
-                }
+            for (int v = 1; v < W; ++v) {
+                c0 += sums[v][wave][lane];
+                if constexpr (GATED) c1 += sums[v][1][lane];
             }
             if (n < NO) {   // NO is a multiple of 4
+                const f32x4 s0 = *reinterpret_cast<const f32x4*>(a.ws + (int64_t)e * a.N + n);
+                f32x4 y, s1 = s0;
+                if constexpr (GATED) s1 = *reinterpret_cast<const f32x4*>(a.ws + (int64_t)e * a.N + NO + n);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[i] = (float)c0[i] * s0[i] * xs;
+                    if constexpr (GATED) y[i] = gate(y[i], (float)c1[i] * s1[i] * xs);
+                }
                 if constexpr (OUT_BF16)
                     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + t * NO + n) =
                         u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
                 else
-                    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + t * NO + n) =
-                        f32x4{y[0], y[1], y[2], y[3]};
+                    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + t * NO + n) = y;
             }
         }
         __syncthreads();
     }
+}
+
+template <bool GATED, int NB, int W>
+hipError_t launch_int8_rows(const Int8Args& a, bool bf16, hipStream_t s) {
+    const dim3 grid((unsigned)ceil_div(GATED ? a.N / 2 : a.N, GATED ? 16 : 16 * NB), (unsigned)a.E), block(64 * W);
+    timing_mark("int8_rows_kernel", s);
+    if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, GATED, NB, W>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((int8_rows_kernel<false, GATED, NB, W>), grid, block, 0, s, a);
+    timing_end(s);
+    return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -348,17 +368,11 @@ hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, hipStr
         if (large) return launch_int8_tile<256, 256, 8>(a, gated, bf16, grid_n, s);
         return launch_int8_tile<128, 256, 4>(a, gated, bf16, grid_n, s);
     }
-    const dim3 grid((unsigned)ceil_div(gated ? a.N / 2 : a.N, gated ? 16 : 32), (unsigned)a.E), block(256);
-    timing_mark("int8_rows_kernel", s);
-    if (gated) {
-        if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, true>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((int8_rows_kernel<false, true>), grid, block, 0, s, a);
-    } else {
-        if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, false>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((int8_rows_kernel<false, false>), grid, block, 0, s, a);
-    }
-    timing_end(s);
-    return hipGetLastError();
+    if (gated) return launch_int8_rows<true, 2, 4>(a, bf16, s);
+    // one block of weight rows per workgroup, and more waves along K, where
+    // two would leave CUs without a workgroup or with only one
+    if (ceil_div(a.N, 32) * a.E < 2 * kRuleCUs) return launch_int8_rows<false, 1, 8>(a, bf16, s);
+    return launch_int8_rows<false, 2, 4>(a, bf16, s);
 }
 
 }  // namespace drgg

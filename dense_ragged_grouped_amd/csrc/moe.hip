@@ -147,7 +147,9 @@ __global__ __launch_bounds__(kRouteThreads) void moe_select_kernel(RouteArgs a) 
     uint32_t key[V], kept[S], top = 0;
     int32_t mine[S];
     load_keys<V>(key, a.logits + t * E, E, l, live);
-    for (int j = 0; j < k; ++j) {
+    // a wave without tokens does not compete with the others
+    const int rounds = (int64_t)blockIdx.x * kRouteTokens + (__builtin_amdgcn_readfirstlane(threadIdx.x) >> 4) < a.T ? k : 0;
+    for (int j = 0; j < rounds; ++j) {
         uint32_t m = key[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) m = max(m, key[i]);
@@ -253,8 +255,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_scan_kernel(RouteArgs a) {
 
 // positions += the expert's offset + its pairs in earlier blocks.  BYTES: the
 // block sums the count bytes of all blocks itself, four experts per thread
-// and the blocks cut into slices over the other threads; two 16-bit sums per
-// word hold them (kRouteBytes * 64 < 2^16).
+// and the blocks cut into at most 16 slices over the other threads; two
+// 16-bit sums per word hold them (kRouteBytes * 64 < 2^16).
 template <bool BYTES>
 __global__ __launch_bounds__(kRouteThreads) void moe_place_kernel(RouteArgs a) {
     __shared__ int32_t base[kMaxExperts], tmp[kRouteWaves];
@@ -263,11 +265,12 @@ __global__ __launch_bounds__(kRouteThreads) void moe_place_kernel(RouteArgs a) {
     int32_t before = 0, n = 0;   // of expert tid: pairs in earlier blocks, and in all
     if constexpr (BYTES) {
         static_assert(kRouteBytes * kRouteTokens < 65536, "16-bit sums");
-        const int quads = table_stride(E) / 4, slices = kRouteThreads / quads;
+        const int quads = table_stride(E) / 4, slices = min(kRouteThreads / quads, 16);
         const int q = tid % quads, sl = tid / quads, blocks = (int)a.blocks, me = (int)blockIdx.x;
         u32x4 s = {0, 0, 0, 0};   // earlier: experts 0 and 2, 1 and 3 of the quad; all: the same
         if (sl < slices) {
             const uint32_t* col = static_cast<const uint32_t*>(a.table) + q;
+#pragma unroll 8
             for (int b = sl; b < blocks; b += slices) {
                 const uint32_t v = col[(int64_t)b * quads];
                 const uint32_t even = v & 0x00FF00FFu, odd = (v >> 8) & 0x00FF00FFu;
