@@ -131,100 +131,179 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
 // ---------------------------------------------------------------------------
 // product, few rows per group
 //
-// A workgroup takes NB blocks of 16 weight rows of one group (gated: 16 gate
-// rows and their 16 up rows) and the group's token rows in blocks of 16; its
-// W waves split K in steps of 64 values and add their integer sums through
-// LDS.  Fragments go from memory to registers directly: lane l of a
-// v_mfma_i32_16x16x64_i8 holds values 16*(l/16) .. +15 of row l%16, one
-// 16-byte load, for the weights (first operand) as for the tokens; the result
-// has token l%16 and weight rows 4*(l/16) .. +3 in lane l.
+// A workgroup computes a block of 16*NB weight rows (gated: 8*NB gate rows and
+// their up rows) and up to TOK = 32 or 64 tokens of one group; its W waves
+// split K in steps of 64 values, each computing the whole block, and add their
+// integer sums through LDS.  Fragments go from memory to registers directly:
+// lane l of a v_mfma_i32_16x16x64_i8 holds values 16*(l/16) .. +15 of row
+// l%16, one 16-byte load, for the weights (first operand) as for the tokens;
+// the result has token l%16 and weight rows 4*(l/16) .. +3 in lane l.  There
+// is no barrier before the sums and a long reduction is W times shorter for
+// each wave, which is what counts while few blocks or few rows leave the CUs
+// idle; with more rows the tiles below move fewer bytes per product.
 //
-// Bound by the weights' bytes, each read once from memory (further blocks of
-// tokens find them in L2): U steps are loaded before the first is used, so
-// that a CU has 32 KB and more in flight.
-template <bool OUT_BF16, bool GATED, int NB, int W>
-__global__ __launch_bounds__(64 * W) void int8_rows_kernel(Int8Args a) {
-    constexpr int U = 4;
-    static_assert(!GATED || NB == 2, "a gate block and its up block");
-    __shared__ i32x4 sums[W][NB][64];
+// Blocks of tokens are 16, 32 or 64 long by what is left of the group; U steps
+// are loaded before the first is used.  Rows and reduction positions outside
+// the operands carry an out-of-range offset and read as zero.  launch_int8
+// says which NB, W and TOK run when.
+// The block of this workgroup among those of all groups (ntn column blocks
+// times ceil(T_e / TOK) token blocks each, token blocks innermost: their
+// weights are then read by one XCD), or false.  Every wave finds it by
+// itself: lane i holds group i of 64.
+struct RowsItem {
+    int e, nt;
+    int64_t m0, hi;
+};
+template <int TOK>
+__device__ __forceinline__ bool find_rows_item(const Int8Args& a, int32_t ntn, RowsItem* it) {
+    const int lane = threadIdx.x & 63;
+    auto bounds = [&](int e, int64_t* lo, int64_t* hi) {
+        if (!a.offs) {
+            *lo = 0;
+            *hi = a.M;
+        } else {
+            *lo = min<int64_t>(max<int64_t>(a.offs[e], 0), a.M);
+            *hi = min<int64_t>(max<int64_t>(a.offs[e + 1], *lo), a.M);
+        }
+    };
+    auto items = [&](int e) {
+        int64_t lo, hi;
+        bounds(e, &lo, &hi);
+        return (int32_t)((hi - lo + TOK - 1) / TOK) * ntn;
+    };
+    int32_t total = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64)
+        total += __shfl(wave_incl_sum(e0 + lane < a.E ? items(e0 + lane) : 0), 63, 64);
+    total = uni(total);
+    if ((int64_t)blockIdx.x >= total) return false;
+    int32_t w = (int32_t)xcd_remap(blockIdx.x, total);
+    for (int e0 = 0;; e0 += 64) {   // ends: w < total
+        const int32_t n = e0 + lane < a.E ? items(e0 + lane) : 0;
+        const int32_t incl = wave_incl_sum(n);
+        const unsigned long long past = __ballot(incl > w);
+        if (past) {
+            const int l = __ffsll((long long)past) - 1;
+            it->e = e0 + l;
+            w -= uni(__shfl(incl - n, l, 64));
+            break;
+        }
+        w -= uni(__shfl(incl, 63, 64));
+    }
+    int64_t lo;
+    bounds(it->e, &lo, &it->hi);
+    const int32_t rt = (int32_t)((it->hi - lo + TOK - 1) / TOK);
+    it->nt = w / rt;
+    it->m0 = lo + (int64_t)(w % rt) * TOK;
+    return true;
+}
+
+template <bool OUT_BF16, bool GATED, int NB, int MB, int W, int U>
+__device__ __forceinline__ void int8_rows_block(const Int8Args& a, const RowsItem& it, i32x4 (&sums)[W][NB][64]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int e = blockIdx.y;
-    int64_t lo = 0, hi = a.M;
-    if (a.offs) {
-        lo = min<int64_t>(max<int64_t>(a.offs[e], 0), a.M);
-        hi = min<int64_t>(max<int64_t>(a.offs[e + 1], lo), a.M);
-    }
-    if (lo >= hi) return;
-    const int64_t NO = GATED ? a.N / 2 : a.N;       // output columns
-    constexpr int kCols = GATED ? 16 : 16 * NB;     // of them per workgroup
-    const int64_t n0 = (int64_t)blockIdx.x * kCols;
-    // weight rows past the end repeat the last one, and their results are not stored
-    const int8_t* w[NB];
+    const int64_t NO = GATED ? a.N / 2 : a.N;
+    constexpr int NC = GATED ? NB / 2 : NB;          // blocks of 16 output columns
+    const int64_t n0 = (int64_t)it.nt * 16 * NC;
+    const int K = (int)a.K;
+    const auto rx = make_rsrc(a.X + it.m0 * a.K);
+    const int8_t* w0 = a.W + ((int64_t)it.e * a.N + n0) * a.K;
+    const auto rw = make_rsrc(w0);
+    const auto rw2 = make_rsrc(GATED ? w0 + NO * a.K : w0);
+    int off[4], xk[MB], wk[NC];   // a row's byte offset; reduction values it has from this lane's 16 on
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int64_t n = GATED ? min(n0 + r, NO - 1) + b * NO : min(n0 + 16 * b + r, NO - 1);
-        w[b] = a.W + ((int64_t)e * a.N + n) * a.K;
-    }
-    for (int64_t m0 = lo; m0 < hi; m0 += 16) {
-        const int8_t* x = a.X + min(m0 + r, hi - 1) * a.K;
-        i32x4 acc[NB] = {};
-        for (int k0 = wave * 64; k0 < a.K; k0 += 64 * W * U) {
-            i32x4 fx[U], fw[U][NB];
+    for (int b = 0; b < 4; ++b) off[b] = (16 * b + r) * K + 16 * g;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = k0 + 64 * W * u + 16 * g;
-                const bool in = k < a.K;
-                fx[u] = in ? *reinterpret_cast<const i32x4*>(x + k) : i32x4{0, 0, 0, 0};
+    for (int b = 0; b < MB; ++b) xk[b] = it.m0 + 16 * b + r < it.hi ? K - 16 * g : 0;
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    fw[u][b] = in ? *reinterpret_cast<const i32x4*>(w[b] + k) : i32x4{0, 0, 0, 0};
-            }
+    for (int b = 0; b < NC; ++b) wk[b] = n0 + 16 * b + r < NO ? K - 16 * g : 0;
+    i32x4 acc[NB][MB] = {};
+    for (int k0 = wave * 64; k0 < K; k0 += 64 * W * U) {
+        u32x4 fx[U][MB], fw[U][NB];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + 64 * W * u;
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][b], fx[u], acc[b], 0, 0, 0);
+            for (int b = 0; b < NB; ++b)
+                fw[u][b] = __builtin_amdgcn_raw_buffer_load_b128(b < NC ? rw : rw2,
+                                                                 k < wk[b % NC] ? (uint32_t)(off[b % NC] + k) : kOOB, 0, 0);
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+                fx[u][b] = __builtin_amdgcn_raw_buffer_load_b128(rx, k < xk[b] ? (uint32_t)(off[b] + k) : kOOB, 0, 0);
         }
 #pragma unroll
-        for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[b];
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+                    acc[b][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, fw[u][b]),
+                                                                      __builtin_bit_cast(i32x4, fx[u][m]), acc[b][m], 0, 0, 0);
+    }
+    // the waves' sums, one block of 16 tokens at a time
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+        if (m > 0) __syncthreads();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[b][m];
         __syncthreads();
-        const int64_t t = m0 + r;
-        if (wave < (GATED ? 1 : NB) && t < hi) {
+        if (wave >= NC) continue;
+        i32x4 c0 = sums[0][wave][lane], c1 = c0;
+        if constexpr (GATED) c1 = sums[0][NC + wave][lane];
+#pragma unroll
+        for (int v = 1; v < W; ++v) {
+            c0 += sums[v][wave][lane];
+            if constexpr (GATED) c1 += sums[v][NC + wave][lane];
+        }
+        const int64_t t = it.m0 + 16 * m + r, n = n0 + 16 * wave + 4 * g;
+        if (t < it.hi && n < NO) {   // NO is a multiple of 4
             const float xs = a.xs[t];
-            const int64_t n = n0 + 16 * wave + 4 * g;
-            i32x4 c0 = sums[0][wave][lane], c1 = sums[0][NB - 1][lane];
+            const float* ws = a.ws + (int64_t)it.e * a.N + n;
+            const f32x4 s0 = *reinterpret_cast<const f32x4*>(ws);
+            f32x4 y, s1 = s0;
+            if constexpr (GATED) s1 = *reinterpret_cast<const f32x4*>(ws + NO);
 #pragma unroll
-            for (int v = 1; v < W; ++v) {
-                c0 += sums[v][wave][lane];
-                if constexpr (GATED) c1 += sums[v][1][lane];
+            for (int i = 0; i < 4; ++i) {
+                y[i] = (float)c0[i] * s0[i] * xs;
+                if constexpr (GATED) y[i] = gate(y[i], (float)c1[i] * s1[i] * xs);
             }
-            if (n < NO) {   // NO is a multiple of 4
-                const f32x4 s0 = *reinterpret_cast<const f32x4*>(a.ws + (int64_t)e * a.N + n);
-                f32x4 y, s1 = s0;
-                if constexpr (GATED) s1 = *reinterpret_cast<const f32x4*>(a.ws + (int64_t)e * a.N + NO + n);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[i] = (float)c0[i] * s0[i] * xs;
-                    if constexpr (GATED) y[i] = gate(y[i], (float)c1[i] * s1[i] * xs);
-                }
-                if constexpr (OUT_BF16)
-                    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + t * NO + n) =
-                        u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-                else
-                    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + t * NO + n) = y;
-            }
+            if constexpr (OUT_BF16)
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + t * NO + n) =
+                    u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+            else
+                *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + t * NO + n) = y;
         }
-        __syncthreads();
     }
 }
 
-template <bool GATED, int NB, int W>
+// With TOK = 32 at most 80 registers (six waves per SIMD), so that the blocks
+// of many experts are resident at once.
+template <bool OUT_BF16, bool GATED, int NB, int W, int TOK>
+__global__ __launch_bounds__(64 * W, TOK == 32 ? 6 : 2) void int8_rows_kernel(Int8Args a) {
+    __shared__ i32x4 sums[W][NB][64];
+    RowsItem it;
+    const int64_t NO = GATED ? a.N / 2 : a.N;
+    constexpr int kCols = 16 * (GATED ? NB / 2 : NB);
+    if (!find_rows_item<TOK>(a, (int32_t)((NO + kCols - 1) / kCols), &it)) return;
+    const int64_t left = it.hi - it.m0;
+    if constexpr (TOK == 32) {
+        if (left <= 16) int8_rows_block<OUT_BF16, GATED, NB, 1, W, 2>(a, it, sums);
+        else int8_rows_block<OUT_BF16, GATED, NB, 2, W, 1>(a, it, sums);
+    } else {
+        if (left <= 16) int8_rows_block<OUT_BF16, GATED, NB, 1, W, 4>(a, it, sums);
+        else if (left <= 32) int8_rows_block<OUT_BF16, GATED, NB, 2, W, 4>(a, it, sums);
+        else int8_rows_block<OUT_BF16, GATED, NB, 4, W, 2>(a, it, sums);
+    }
+}
+
+template <bool GATED, int NB, int W, int TOK>
 hipError_t launch_int8_rows(const Int8Args& a, bool bf16, hipStream_t s) {
-    const dim3 grid((unsigned)ceil_div(GATED ? a.N / 2 : a.N, GATED ? 16 : 16 * NB), (unsigned)a.E), block(64 * W);
+    const int64_t ntn = ceil_div(GATED ? a.N / 2 : a.N, 16 * (GATED ? NB / 2 : NB));
+    // ceil(T_e / TOK) over the groups is at most M / TOK and one for each group with rows
+    const int64_t most = (a.M / TOK + (a.M < a.E ? a.M : a.E)) * ntn;
+    const dim3 grid((unsigned)most), block(64 * W);
     timing_mark("int8_rows_kernel", s);
-    if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, GATED, NB, W>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((int8_rows_kernel<false, GATED, NB, W>), grid, block, 0, s, a);
+    if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, GATED, NB, W, TOK>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((int8_rows_kernel<false, GATED, NB, W, TOK>), grid, block, 0, s, a);
     timing_end(s);
     return hipGetLastError();
 }
@@ -358,21 +437,37 @@ hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, 
     return hipGetLastError();
 }
 
+// Which program runs, from the sizes alone.  M rows in E groups of unknown
+// sizes make about M/64 + E/2 blocks of 64 tokens.
 hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, hipStream_t s) {
-    if (a.M > 32 * (int64_t)a.E) {
-        // tiles of 128x256 where those of 256x256 leave CUs without one
-        const int64_t nc = ceil_div(gated ? a.N / 2 : a.N, gated ? 128 : 256);
-        const bool large = (a.M / 256) * nc >= kRuleCUs;
-        const int64_t most = (a.M / (large ? 256 : 128) + a.E) * nc;
-        const int64_t grid_n = most < cus ? most : cus;
-        if (large) return launch_int8_tile<256, 256, 8>(a, gated, bf16, grid_n, s);
-        return launch_int8_tile<128, 256, 4>(a, gated, bf16, grid_n, s);
+    const int64_t cols = ceil_div(a.N, 64), blocks = cols * (ceil_div(a.M, 64) + (a.E - 1) / 2);
+    if (cols * a.E >= 2 * kRuleCUs && a.M <= 24 * (int64_t)a.E) {
+        // many experts' weights, few rows of each: read at memory speed (E = 32,
+        // 1536x2048: 256 rows 20 us, 512 rows 23, 768 rows 30; in 128x256 tiles
+        // 27, 28 and 29; 57 x 1000x1008, 1368 rows: 15 against 19)
+        return gated ? launch_int8_rows<true, 4, 4, 32>(a, bf16, s) : launch_int8_rows<false, 4, 4, 32>(a, bf16, s);
     }
-    if (gated) return launch_int8_rows<true, 2, 4>(a, bf16, s);
-    // one block of weight rows per workgroup, and more waves along K, where
-    // two would leave CUs without a workgroup or with only one
-    if (ceil_div(a.N, 32) * a.E < 2 * kRuleCUs) return launch_int8_rows<false, 1, 8>(a, bf16, s);
-    return launch_int8_rows<false, 2, 4>(a, bf16, s);
+    if (blocks <= 2 * kRuleCUs) {
+        // at most two blocks per CU: the largest blocks that leave none idle
+        // (4096x4096, one group: 1 row 8 us, 128 rows 16, 256 rows 20, 512
+        // rows 34; in 128x256 tiles 31 to 33)
+        if (blocks >= kRuleCUs)
+            return gated ? launch_int8_rows<true, 4, 8, 64>(a, bf16, s) : launch_int8_rows<false, 4, 8, 64>(a, bf16, s);
+        if (gated) return launch_int8_rows<true, 2, 8, 64>(a, bf16, s);
+        return 2 * blocks >= kRuleCUs ? launch_int8_rows<false, 2, 8, 64>(a, bf16, s)
+                                      : launch_int8_rows<false, 1, 8, 64>(a, bf16, s);
+    }
+    // the tile whose rounds of (about) full waves cost less, a 256x256 one
+    // taking 1.25 times as long as one of 128x256 (measured 1.1 to 1.3, alone
+    // on a CU; E = 32, 1536x2048: 4096 rows 34 against 51 us, 8192 rows 65
+    // against 53, 16384 rows 75 against 97)
+    const int64_t nc = ceil_div(gated ? a.N / 2 : a.N, gated ? 128 : 256);
+    auto rounds = [&](int64_t bm) { return ceil_div((ceil_div(a.M, bm) + (a.E - 1) / 2) * nc, kRuleCUs); };
+    const bool large = 5 * rounds(256) <= 4 * rounds(128);
+    const int64_t most = (a.M / (large ? 256 : 128) + (a.M < a.E ? a.M : a.E)) * nc;
+    const int64_t grid_n = most < cus ? most : cus;
+    if (large) return launch_int8_tile<256, 256, 8>(a, gated, bf16, grid_n, s);
+    return launch_int8_tile<128, 256, 4>(a, gated, bf16, grid_n, s);
 }
 
 }  // namespace drgg
