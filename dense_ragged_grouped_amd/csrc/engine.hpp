@@ -824,13 +824,9 @@ __device__ __forceinline__ void store_tile(const Mma& mma, void* out, int64_t ld
 // all it needs.  CPOL is the stores' cache policy: non-temporal for outputs;
 // 0 for data read back soon (the weight gradient's chunk partials, which the
 // fold then finds in the last-level cache).
-//
-// store_tile_values is the same for values that are made on the way: value(i,
-// j, q) gives the four of row block i at columns 32j + 8q + 4*(lane/32) .. +3
-// of the wave's part, which starts at column rb and has NJ blocks of 32.
-template <bool OUT_BF16, int R, int CPOL, class Mma, int NJ, class Value>
-__device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* scr, void* out, int64_t ld, int rows,
-                                                  int cols) {
+template <bool OUT_BF16, int R, int CPOL = kCpolNT, class Mma>
+__device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, void* out, int64_t ld, int rows,
+                                                 int cols) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -839,11 +835,11 @@ __device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* sc
     constexpr int BPS = SEG / 32;   // 32-column blocks per segment
     constexpr int CPL = R / 8;      // read-back chunks per lane and round
     static_assert(R == 8 || R == 16, "rounds of 8 or 16 rows");
-    static_assert(NJ % BPS == 0, "whole segments per wave");
+    static_assert(Mma::kBJ % BPS == 0, "whole segments per wave");
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ra = Mma::wave_row(wave);
+    const int ra = Mma::wave_row(wave), rb = Mma::wave_col(wave);
     lds_t* sw = scr + wave * (R * 128);
     const int r = lane & 31, h = lane >> 5;
     const int rr = r % R;   // this lane's scratch row in the round that owns it
@@ -853,20 +849,20 @@ __device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* sc
         const int r0 = ra + 32 * i;
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<char*>(out) + (int64_t)r0 * ld * ES);
 #pragma unroll
-        for (int g = 0; g < NJ / BPS; ++g) {
+        for (int g = 0; g < Mma::kBJ / BPS; ++g) {
             const int c0 = rb + g * SEG;
 #pragma unroll
             for (int s = 0; s < 32 / R; ++s) {
                 if (r / R == s) {
 #pragma unroll
                     for (int b = 0; b < BPS; ++b) {
+                        const f32x16& a = mma.acc[i][g * BPS + b];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const f32x4 a = value(i, g * BPS + b, q);
                             if constexpr (OUT_BF16) {
                                 // columns 32b + 8q + 4h .. +3: chunk 4b + q, its half h
-                                const bf16x2 lo = __builtin_convertvector((f32x2{a[0], a[1]}), bf16x2);
-                                const bf16x2 hi = __builtin_convertvector((f32x2{a[2], a[3]}), bf16x2);
+                                const bf16x2 lo = __builtin_convertvector((f32x2{a[4 * q], a[4 * q + 1]}), bf16x2);
+                                const bf16x2 hi = __builtin_convertvector((f32x2{a[4 * q + 2], a[4 * q + 3]}), bf16x2);
                                 *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(
                                     sw + rr * 128 + (((4 * b + q) ^ sx) << 4) + 8 * h) =
                                     u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
@@ -874,8 +870,8 @@ __device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* sc
                                 // columns 8q + 4h .. +3: chunk 2q + h
                                 *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(
                                     sw + rr * 128 + (((2 * q + h) ^ sx) << 4)) =
-                                    u32x4{__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
-                                          __float_as_uint(a[3])};
+                                    u32x4{__float_as_uint(a[4 * q]), __float_as_uint(a[4 * q + 1]),
+                                          __float_as_uint(a[4 * q + 2]), __float_as_uint(a[4 * q + 3])};
                             }
                         }
                     }
@@ -896,16 +892,83 @@ __device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* sc
         }
     }
 }
-template <bool OUT_BF16, int R, int CPOL = kCpolNT, class Mma>
-__device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, void* out, int64_t ld, int rows,
-                                                 int cols) {
-    const int rb = Mma::wave_col(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
-    store_tile_values<OUT_BF16, R, CPOL, Mma, Mma::kBJ>(
-        [&](int i, int j, int q) {
-            const f32x16& a = mma.acc[i][j];
-            return f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
-        },
-        rb, scr, out, ld, rows, cols);
+
+// store_tile_lines for values that are made on the way: value(i, j, q) gives
+// the four of row block i at columns 32j + 8q + 4*(lane/32) .. +3 of the
+// wave's part, which starts at column rb and has NJ blocks of 32.  A
+// segment's values are made by all lanes before its rounds, in which only the
+// lanes that own a round's rows write (made inside the rounds they would cost
+// 32/R times the instructions).
+template <bool OUT_BF16, int R, class Mma, int NJ, class Value>
+__device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* scr, void* out, int64_t ld, int rows,
+                                                  int cols) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    constexpr int ES = OUT_BF16 ? 2 : 4;
+    constexpr int SEG = 128 / ES;   // columns per 128-byte segment
+    constexpr int BPS = SEG / 32;   // 32-column blocks per segment
+    static_assert(R == 8 || R == 16, "rounds of 8 or 16 rows");
+    static_assert(NJ % BPS == 0, "whole segments per wave");
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ra = Mma::wave_row(wave);
+    lds_t* sw = scr + wave * (R * 128);
+    const int r = lane & 31, h = lane >> 5;
+    const int rr = r % R;   // this lane's scratch row in the round that owns it
+    const int sx = rr & 7;
+#pragma unroll
+    for (int i = 0; i < Mma::kBI; ++i) {
+        const int r0 = ra + 32 * i;
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<char*>(out) + (int64_t)r0 * ld * ES);
+#pragma unroll
+        for (int g = 0; g < NJ / BPS; ++g) {
+            const int c0 = rb + g * SEG;
+            u32x2 half[OUT_BF16 ? BPS : 1][4];
+            u32x4 full[OUT_BF16 ? 1 : BPS][4];
+#pragma unroll
+            for (int b = 0; b < BPS; ++b)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 a = value(i, g * BPS + b, q);
+                    if constexpr (OUT_BF16)
+                        half[b][q] = u32x2{
+                            __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a[0], a[1]}), bf16x2)),
+                            __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a[2], a[3]}), bf16x2))};
+                    else
+                        full[b][q] = __builtin_bit_cast(u32x4, a);
+                }
+#pragma unroll
+            for (int s = 0; s < 32 / R; ++s) {
+                if (r / R == s) {
+#pragma unroll
+                    for (int b = 0; b < BPS; ++b)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if constexpr (OUT_BF16)   // columns 32b + 8q + 4h .. +3: chunk 4b + q, its half h
+                                *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(
+                                    sw + rr * 128 + (((4 * b + q) ^ sx) << 4) + 8 * h) = half[b][q];
+                            else   // columns 8q + 4h .. +3: chunk 2q + h
+                                *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(
+                                    sw + rr * 128 + (((2 * q + h) ^ sx) << 4)) = full[b][q];
+                        }
+                }
+                wave_lds_sync();   // the round's rows are in the scratch
+#pragma unroll
+                for (int k = 0; k < R / 8; ++k) {
+                    const int idx = lane + 64 * k, row = idx >> 3, c = idx & 7;
+                    const u32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(
+                        sw + row * 128 + ((c ^ (row & 7)) << 4));
+                    const int rowb = s * R + row;            // row within the 32-row block
+                    const int col = c0 + c * (16 / ES);
+                    const uint32_t o = r0 + rowb < rows && col < cols ? (uint32_t)((rowb * ld + col) * ES) : kOOB;
+                    __builtin_amdgcn_raw_buffer_store_b128(v, rs, o, 0, kCpolNT);
+                }
+                wave_lds_sync();   // read back before the next round overwrites it
+            }
+        }
+    }
 }
 
 // Issue schedule of the stage loads of a 4-wave runner (steps t of the

@@ -400,7 +400,7 @@ __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
         };
         const int64_t o = t.o0 * NO + t.o1;
         void* base = OUT_BF16 ? (void*)(static_cast<uint16_t*>(a.out) + o) : (void*)(static_cast<float*>(a.out) + o);
-        store_tile_values<OUT_BF16, ep_rows(BM, BN), kCpolNT, Mma, NJ>(value, rb, (lds_t*)ep, base, NO, t.rows, t.cols);
+        store_tile_values<OUT_BF16, ep_rows(BM, BN), Mma, NJ>(value, rb, (lds_t*)ep, base, NO, t.rows, t.cols);
     };
     TileRunner<BM, BN, true, true, WAVES, Int8, GATED> runner;
     runner.st = stg;
