@@ -147,14 +147,14 @@ def _load(path=LIB_PATH):
     lib.drgg_timing_count.restype = c_int
     lib.drgg_timing_read.argtypes = [c_int, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float)]
     lib.drgg_timing_read.restype = c_int
-    lib.moe_route.argtypes = [vp, i64, i32, i32, c_int, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_route.argtypes = [vp, i64, i32, i32, c_int, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_route_workspace_size.argtypes = [i64, i32, i32, ctypes.POINTER(sz)]
     lib.moe_route_grad.argtypes = [vp, vp, vp, vp, i64, i32, i32, c_int, vp, vp]
     lib.moe_dispatch.argtypes = [vp, vp, i64, i32, i64, c_int, vp, vp]
     lib.moe_combine.argtypes = [vp, vp, vp, i64, i32, i64, c_int, vp, vp]
     lib.moe_combine_grad.argtypes = [vp, vp, vp, vp, i64, i32, i64, c_int, vp, vp, vp]
     lib.quantize_int8.argtypes = [vp, c_int, i64, i64, vp, i32, vp, vp, vp]
-    lib.grouped_gemm_int8.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, c_int, c_int, vp, vp]
+    lib.grouped_gemm_int8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, i64, c_int, c_int, vp, vp]
     lib.gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp]
     lib.moe_ffn_int8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, i64, c_int, vp, vp, sz, vp]
     lib.moe_ffn_int8_workspace_size.argtypes = [i64, i32, i32, i64, i64, ctypes.POINTER(sz)]
@@ -434,9 +434,9 @@ def _workspace(device, nbytes, workspace, deterministic, kind="wgrad", stream=No
         # keyed by the program that runs (`deterministic` here: whether the
         # deterministic program runs): a non-deterministic call routed to it
         # shares its buffer of partials, the split program has its own,
-        # zeroed one; the data gradient's W^T, the router's reduction slices
-        # and the selection's counts have their own
-        prog = kind if kind in ("dgrad", "router", "route") else bool(deterministic)
+        # zeroed one; the data gradient's W^T and the router's reduction
+        # slices have their own
+        prog = kind if kind in ("dgrad", "router") else bool(deterministic)
         key = (str(device), s.cuda_stream, prog)
         if key not in _default_ws:
             _default_ws[key] = Workspace(device)
@@ -726,6 +726,7 @@ class Routing(NamedTuple):
     weights: "torch.Tensor"         # [T, k] float32
     group_offsets: "torch.Tensor"   # [E+1] int32, as the grouped products take them
     positions: "torch.Tensor"       # [T, k] int32, each pair's row in the grouped order
+    tokens: "torch.Tensor"          # [T*k] int32, each row's token
 
 
 def _call(name, stream, tensors, *args):
@@ -799,15 +800,32 @@ def moe_route(logits, k, renormalize=True, workspace=None, stream=None):
     T, E = logits.shape
     k = int(k)
     nbytes = route_workspace_size(T, E, k)
+    R = T * k
     weights = logits.new_empty((T, k))
-    experts = logits.new_empty((T, k), dtype=torch.int32)
-    positions = logits.new_empty((T, k), dtype=torch.int32)
-    offsets = logits.new_empty((E + 1,), dtype=torch.int32)
-    ws_ptr, ws_bytes = (_workspace(logits.device, nbytes, workspace, True, kind="route", stream=stream) if nbytes
-                        else (None, 0))
-    _call("moe_route", stream, (logits,), logits.data_ptr(), T, E, k, 1 if renormalize else 0, experts.data_ptr(),
-          weights.data_ptr(), offsets.data_ptr(), positions.data_ptr(), ws_ptr, ws_bytes)
-    return Routing(experts, weights, offsets, positions)
+    # one allocation for the integers (four would cost three times as much)
+    ints = logits.new_empty((3 * R + E + 1,), dtype=torch.int32)
+    experts, positions = ints.as_strided((T, k), (k, 1)), ints.as_strided((T, k), (k, 1), R)
+    tokens, offsets = ints.as_strided((R,), (1,), 2 * R), ints.as_strided((E + 1,), (1,), 3 * R)
+    ws_ptr, ws_bytes = None, 0
+    if nbytes and workspace is None:
+        scratch = _scratch(logits, nbytes, stream)
+        ws_ptr, ws_bytes = scratch.data_ptr(), nbytes
+    elif nbytes:
+        ws_ptr, ws_bytes = _workspace(logits.device, nbytes, workspace, True, stream=stream)
+    at = ints.data_ptr()
+    _call("moe_route", stream, (logits,), logits.data_ptr(), T, E, k, 1 if renormalize else 0, at, weights.data_ptr(),
+          at + 12 * R, at + 4 * R, at + 8 * R, ws_ptr, ws_bytes)
+    return Routing(experts, weights, offsets, positions, tokens)
+
+
+def _scratch(like, nbytes, stream):
+    """A workspace for one call, which needs no initialisation.  Allocated on
+    the stream that uses it, so that its memory is handed out again in order."""
+    torch = _torch()
+    if stream is None:
+        return like.new_empty((nbytes,), dtype=torch.uint8)
+    with torch.cuda.stream(stream):
+        return like.new_empty((nbytes,), dtype=torch.uint8)
 
 
 def moe_route_grad(dweights, logits, experts, weights, renormalize=True, out=None, stream=None):
@@ -895,39 +913,48 @@ def quantize_int8(X, positions=None, stream=None):
     return q, scale
 
 
-def _int8_operands(Xq, x_scale, Wq, w_scale, wdim, gated, out_dtype, out):
+def _int8_operands(Xq, x_scale, Wq, w_scale, wdim, M, gated, out_dtype, out):
     torch = _torch()
     _need(Xq, torch.int8, "Xq", 2)
     _need(Wq, torch.int8, "Wq", wdim)
     _need(x_scale, torch.float32, "x_scale", 1)
     _need(w_scale, torch.float32, "w_scale", wdim - 1)
-    M, K = Xq.shape
+    T, K = Xq.shape
     N = Wq.shape[-2]
-    if Wq.shape[-1] != K or x_scale.shape[0] != M or w_scale.shape != Wq.shape[:-1]:
+    if Wq.shape[-1] != K or x_scale.shape[0] != T or w_scale.shape != Wq.shape[:-1]:
         raise ValueError(f"shape mismatch: Xq {tuple(Xq.shape)}, x_scale {tuple(x_scale.shape)}, "
                          f"Wq {tuple(Wq.shape)}, w_scale {tuple(w_scale.shape)}")
     code = BF16 if out_dtype is None else _dtype_code(out_dtype)
-    return M, N, K, code, _out(out, _torch_dtype(code), (M, N // 2 if gated else N), Xq)
+    out = _out(out, _torch_dtype(code), (T if M is None else M, N // 2 if gated else N), Xq)
+    return T, N, K, code, out
 
 
-def grouped_gemm_int8(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, out_dtype=None, out=None, stream=None):
+def grouped_gemm_int8(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, rows=None, out_dtype=None, out=None,
+                      stream=None):
     """Y[t] = x_scale[t] * w_scale[e(t)] * (Xq[t] Wq[e(t)]^T) for int8 codes Xq
     [M, K], Wq [E, N, K] and FP32 scales [M], [E, N]: an exact integer sum,
     scaled in FP32 and rounded once to out_dtype (bf16 by default).  gated:
-    the N = 2I columns are gate and up halves, and Y [M, I] = silu(gate) * up."""
+    the N = 2I columns are gate and up halves, and Y [M, I] = silu(gate) * up.
+    rows (int32 [M], moe_route's tokens): row t of the product is row rows[t]
+    of Xq [T, K] and x_scale [T], T*K < 2^31 - 4096."""
+    torch = _torch()
     E = _offsets(group_offsets)
-    M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 3, gated, out_dtype, out)
+    M = at = None
+    if rows is not None:
+        _need(rows, torch.int32, "rows", 1)
+        M, at = rows.numel(), rows.data_ptr()
+    T, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 3, M, gated, out_dtype, out)
     if Wq.shape[0] != E:
         raise ValueError(f"shape mismatch: Wq {tuple(Wq.shape)}, E={E}")
-    _call("grouped_gemm_int8", stream, (Xq, x_scale, Wq, w_scale, group_offsets, out), Xq.data_ptr(),
-          x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(), group_offsets.data_ptr(), E, M, N, K,
-          1 if gated else 0, code, out.data_ptr())
+    _call("grouped_gemm_int8", stream, (Xq, x_scale, Wq, w_scale, group_offsets, rows, out), Xq.data_ptr(),
+          x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(), group_offsets.data_ptr(), at, T, E,
+          T if M is None else M, N, K, 1 if gated else 0, code, out.data_ptr())
     return out
 
 
 def gemm_int8(Xq, x_scale, Wq, w_scale, gated=False, out_dtype=None, out=None, stream=None):
     """The one-group case of grouped_gemm_int8: Wq [N, K], w_scale [N]."""
-    M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 2, gated, out_dtype, out)
+    M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 2, None, gated, out_dtype, out)
     _call("gemm_int8", stream, (Xq, x_scale, Wq, w_scale, out), Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(),
           w_scale.data_ptr(), M, N, K, 1 if gated else 0, code, out.data_ptr())
     return out
@@ -935,8 +962,8 @@ def gemm_int8(Xq, x_scale, Wq, w_scale, gated=False, out_dtype=None, out=None, s
 
 def moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True, out=None, workspace=None, stream=None):
     """A gated feed-forward block of E experts in one call: moe_route on logits
-    [T, E], quantize_int8 of X [T, H] (BF16) into the grouped order, the gated
-    product with W1q [E, 2I, H] (FP32 result), quantize_int8 of it, the product
+    [T, E], quantize_int8 of X [T, H] (BF16), the gated product of its rows in
+    the grouped order with W1q [E, 2I, H] (FP32 result), quantize_int8 of it, the product
     with W2q [E, H, I] (BF16) and moe_combine: [T, H] BF16.  `workspace`: a
     device tensor of at least ffn_workspace_size bytes, or None for one
     allocated for this call."""
@@ -955,9 +982,7 @@ def moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True, o
     _need_shape(w2_scale, torch.float32, (E, H), "w2_scale")
     out = _out(out, torch.bfloat16, (T, H), X)
     if workspace is None:
-        nbytes = ffn_workspace_size(T, E, k, H, I)
-        with torch.cuda.stream(stream):   # freed memory stays ordered on the stream that uses it
-            workspace = X.new_empty((nbytes,), dtype=torch.uint8)
+        workspace = _scratch(X, ffn_workspace_size(T, E, k, H, I), stream)
     _call("moe_ffn_int8", stream, (X, logits, W1q, w1_scale, W2q, w2_scale, out, workspace), X.data_ptr(),
           logits.data_ptr(), W1q.data_ptr(), w1_scale.data_ptr(), W2q.data_ptr(), w2_scale.data_ptr(), T, E, int(k), H,
           I, 1 if renormalize else 0, out.data_ptr(), workspace.data_ptr(),

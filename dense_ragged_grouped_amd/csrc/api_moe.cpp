@@ -35,17 +35,21 @@ drgg_status check_rows(int64_t T, int32_t k, int64_t H, drgg_dtype dt) {
     return H % 8 ? DRGG_EALIGN : DRGG_OK;
 }
 
+// whether T rows of K codes can be gathered: their offsets are 32 bits wide
+bool can_gather(int64_t T, int64_t K) { return T * K <= INT32_MAX - 4096; }
+
 drgg_status run_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, const float* w_scale,
-                     const int32_t* offs, int32_t E, int64_t M, int64_t N, int64_t K, int gated, drgg_dtype dt, void* Y,
-                     hipStream_t s) {
+                     const int32_t* offs, const int32_t* rows, int64_t T, int32_t E, int64_t M, int64_t N, int64_t K,
+                     int gated, drgg_dtype dt, void* Y, hipStream_t s) {
     if (E < 1 || E > kMaxExperts) return DRGG_EINVAL;
     if (dt != DRGG_BF16 && dt != DRGG_FP32) return DRGG_EINVAL;
     const int64_t na = gated ? 16 : 8;
     if (M < 0 || M > INT32_MAX || N < na || N > (1 << 22) || K < 16 || K > kInt8MaxK) return DRGG_ESHAPE;
     if (N % na || K % 16) return DRGG_EALIGN;
+    if (rows && (T < 1 || T > INT32_MAX || !can_gather(T, K))) return DRGG_ESHAPE;
     if (!Wq || !w_scale || (M > 0 && (!Xq || !x_scale || !Y))) return DRGG_EINVAL;
     if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || !aligned16(w_scale) || !aligned4(x_scale) ||
-        !aligned4(offs))
+        !aligned4(offs) || !aligned4(rows))
         return DRGG_EALIGN;
     if (offs && checks_offsets()) {
         drgg_status st = check_offsets_sync(offs, E, M, s);
@@ -55,15 +59,18 @@ drgg_status run_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, c
     int cus = 0;
     drgg_status st = current_cu_count(&cus);
     if (st != DRGG_OK) return st;
-    Int8Args a{Xq, Wq, x_scale, w_scale, offs, Y, M, N, K, E};
+    Int8Args a{Xq, Wq, x_scale, w_scale, offs, Y, M, N, K, E, rows, T};
     return launch_status(launch_int8(a, gated != 0, dt == DRGG_BF16, cus, s));
 }
 
 // The parts of moe_ffn_int8's workspace (byte offsets, multiples of 256).  The
-// experts' outputs y take the place of the grouped codes and the activation,
-// which are no longer needed by then.
+// experts' outputs y take the place of the codes of X and the activation,
+// which are no longer needed by then.  X is quantised once per token and its
+// rows gathered by the first product, or, where they are too many for that,
+// written k times into the grouped order.
 struct FfnLayout {
-    int64_t experts, weights, offsets, positions, table, xs, hs, hq, x, h, y, bytes;
+    int64_t experts, weights, offsets, positions, tokens, table, xs, hs, hq, x, h, y, bytes;
+    bool gather;
 };
 drgg_status ffn_layout(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I, FfnLayout* L) {
     drgg_status st = check_route(T, E, k);
@@ -81,13 +88,16 @@ drgg_status ffn_layout(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I, Ff
     L->weights = part(R * 4);
     L->offsets = part(((int64_t)E + 1) * 4);
     L->positions = part(R * 4);
+    L->tokens = part(R * 4);
     L->table = part((int64_t)route_table_bytes(T, E));
     L->xs = part(R * 4);
     L->hs = part(R * 4);
     L->hq = part(R * I);
+    L->gather = can_gather(T, H);
+    const int64_t x = round_up((L->gather ? T : R) * H, 256);
     L->x = L->y = at;
-    L->h = at + round_up(R * H, 256);
-    const int64_t both = round_up(R * H, 256) + round_up(R * I * 4, 256), y = round_up(R * H * 2, 256);
+    L->h = at + x;
+    const int64_t both = x + round_up(R * I * 4, 256), y = round_up(R * H * 2, 256);
     L->bytes = at + (both > y ? both : y);
     return DRGG_OK;
 }
@@ -108,13 +118,13 @@ drgg_status moe_route_workspace_size(int64_t T, int32_t E, int32_t k, size_t* by
 }
 
 drgg_status moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
-                      float* weights, int32_t* group_offsets, int32_t* positions, void* workspace,
+                      float* weights, int32_t* group_offsets, int32_t* positions, int32_t* tokens, void* workspace,
                       size_t workspace_bytes, hipStream_t stream) {
     drgg_status st = check_route(T, E, k);
     if (st != DRGG_OK) return st;
     if (!group_offsets || (T > 0 && (!logits || !experts || !weights || !positions))) return DRGG_EINVAL;
     if (!aligned16(logits) || !aligned4(experts) || !aligned4(weights) || !aligned4(group_offsets) ||
-        !aligned4(positions))
+        !aligned4(positions) || !aligned4(tokens))
         return DRGG_EALIGN;
     const size_t need = route_table_bytes(T, E);
     if (need > 0) {
@@ -122,7 +132,7 @@ drgg_status moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int 
         if (!aligned16(workspace)) return DRGG_EALIGN;
     }
     return launch_status(launch_moe_route(logits, T, E, k, renormalize != 0, experts, weights, group_offsets, positions,
-                                          workspace, stream));
+                                          tokens, workspace, stream));
 }
 
 drgg_status moe_route_grad(const float* dweights, const float* logits, const int32_t* experts, const float* weights,
@@ -186,15 +196,15 @@ drgg_status quantize_int8(const void* X, drgg_dtype dtype, int64_t T, int64_t K,
 }
 
 drgg_status grouped_gemm_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, const float* w_scale,
-                              const int32_t* group_offsets, int32_t E, int64_t M, int64_t N, int64_t K, int gated,
-                              drgg_dtype out_dtype, void* Y, hipStream_t stream) {
+                              const int32_t* group_offsets, const int32_t* rows, int64_t T, int32_t E, int64_t M,
+                              int64_t N, int64_t K, int gated, drgg_dtype out_dtype, void* Y, hipStream_t stream) {
     if (!group_offsets) return DRGG_EINVAL;
-    return run_int8(Xq, x_scale, Wq, w_scale, group_offsets, E, M, N, K, gated, out_dtype, Y, stream);
+    return run_int8(Xq, x_scale, Wq, w_scale, group_offsets, rows, T, E, M, N, K, gated, out_dtype, Y, stream);
 }
 
 drgg_status gemm_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, const float* w_scale, int64_t M,
                       int64_t N, int64_t K, int gated, drgg_dtype out_dtype, void* Y, hipStream_t stream) {
-    return run_int8(Xq, x_scale, Wq, w_scale, nullptr, 1, M, N, K, gated, out_dtype, Y, stream);
+    return run_int8(Xq, x_scale, Wq, w_scale, nullptr, nullptr, 0, 1, M, N, K, gated, out_dtype, Y, stream);
 }
 
 drgg_status moe_ffn_int8_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I, size_t* bytes) {
@@ -225,6 +235,7 @@ drgg_status moe_ffn_int8(const void* X, const float* logits, const int8_t* W1q, 
     auto* weights = reinterpret_cast<float*>(ws + L.weights);
     auto* offsets = reinterpret_cast<int32_t*>(ws + L.offsets);
     auto* positions = reinterpret_cast<int32_t*>(ws + L.positions);
+    auto* tokens = reinterpret_cast<int32_t*>(ws + L.tokens);
     auto* xs = reinterpret_cast<float*>(ws + L.xs);
     auto* hs = reinterpret_cast<float*>(ws + L.hs);
     auto* hq = reinterpret_cast<int8_t*>(ws + L.hq);
@@ -234,10 +245,12 @@ drgg_status moe_ffn_int8(const void* X, const float* logits, const int8_t* W1q, 
     if (st != DRGG_OK) return st;
     const int64_t R = T * k;
     hipError_t e = launch_moe_route(logits, T, E, k, renormalize != 0, experts, weights, offsets, positions,
-                                    ws + L.table, stream);
-    if (e == hipSuccess) e = launch_quantize_int8(X, true, T, H, positions, k, x, xs, stream);
+                                    L.gather ? tokens : nullptr, ws + L.table, stream);
     if (e == hipSuccess)
-        e = launch_int8(Int8Args{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E}, true, false, cus, stream);
+        e = launch_quantize_int8(X, true, T, H, L.gather ? nullptr : positions, L.gather ? 1 : k, x, xs, stream);
+    if (e == hipSuccess)
+        e = launch_int8(Int8Args{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E, L.gather ? tokens : nullptr, T},
+                        true, false, cus, stream);
     if (e == hipSuccess) e = launch_quantize_int8(ws + L.h, false, R, I, nullptr, 1, hq, hs, stream);
     if (e == hipSuccess)
         e = launch_int8(Int8Args{hq, W2q, hs, w2_scale, offsets, ws + L.y, R, H, I, E}, false, true, cus, stream);

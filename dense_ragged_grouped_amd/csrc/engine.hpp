@@ -441,6 +441,10 @@ struct Operand {
     int32_t nvalid;
     int32_t klen;
     int64_t pair = 0;
+    // A gathered operand (K-major): tile row i is row index[i] of the `of` rows
+    // at base; a row whose index is outside reads as zero.
+    const int32_t* index = nullptr;
+    int64_t of = 0;
 };
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -568,7 +572,7 @@ __device__ __forceinline__ int swzMN(int row) {
 // of the 4 waves issues a quarter.  Lane l of instruction g writes LDS bytes
 // [g*1024 + 16*l, +16); the swizzle is applied by choosing which global
 // chunk the lane fetches.
-template <int ROWS, bool KMAJ, int WAVES, bool PAIRED = false>
+template <int ROWS, bool KMAJ, int WAVES, bool PAIRED = false, bool GATHERED = false>
 struct StageLoader {
     static constexpr int kSpan = KMAJ ? 2 : 1;   // stages per load
     static constexpr int kPerWave = ROWS * kStageK * 2 * kSpan / 1024 / WAVES;
@@ -599,8 +603,14 @@ struct StageLoader {
             const int row = b / kRowBytes, phys = (b % kRowBytes) / 16;
             if constexpr (KMAJ) {
                 const int logical = phys ^ swzK(row);
-                const int from = PAIRED ? (row & 31) + 32 * (row >> 6) : row;
-                off[i] = from < op.nvalid ? (uint32_t)(from * op.ld * 2 + logical * 16) : kOOB;
+                int from = PAIRED ? (row & 31) + 32 * (row >> 6) : row;
+                bool ok = from < op.nvalid;
+                if constexpr (GATHERED) {
+                    static_assert(KMAJ, "rows are gathered whole");
+                    from = ok ? op.index[from] : 0;
+                    ok = ok && (uint32_t)from < (uint32_t)op.of;   // of * ld * 2 < 2^31, checked by the caller
+                }
+                off[i] = ok ? (uint32_t)(from * op.ld * 2 + logical * 16) : kOOB;
                 kp[i] = logical * 8;
             } else {
                 const int col = (phys ^ swzMN<kCPR>(row)) * 8;
@@ -1021,10 +1031,11 @@ struct NoLoads {
 // tile (so after every wave has left the epilogue before the current tile),
 // and what it loads has landed for every wave by the tile's epilogue.  Must be
 // called by all threads.
-template <int BM, int BN, bool AK, bool BK, int WAVES = kGemmWaves, class El = Bf16, bool PAIRED_B = false>
+template <int BM, int BN, bool AK, bool BK, int WAVES = kGemmWaves, class El = Bf16, bool PAIRED_B = false,
+          bool GATHERED_A = false>
 struct TileRunner {
     using Mma = TileMma<BM, BN, AK, BK, WAVES, El>;
-    using LA = StageLoader<BM, AK, WAVES>;
+    using LA = StageLoader<BM, AK, WAVES, false, GATHERED_A>;
     using LB = StageLoader<BN, BK, WAVES, PAIRED_B>;
     using Plan = IssuePlan<AK, BK, LA::kPerWave, LB::kPerWave>;
     Mma mma;

@@ -197,7 +197,15 @@ __device__ __forceinline__ bool find_rows_item(const Int8Args& a, int32_t ntn, R
     return true;
 }
 
-template <bool OUT_BF16, bool GATED, int NB, int MB, int W, int U>
+// the scale of product row t (0 for a gathered row that is none)
+template <bool GATHERED>
+__device__ __forceinline__ float x_scale(const Int8Args& a, int64_t t) {
+    if constexpr (!GATHERED) return a.xs[t];
+    const int32_t from = a.rows[t];
+    return (uint32_t)from < (uint32_t)a.T ? a.xs[from] : 0.f;
+}
+
+template <bool OUT_BF16, bool GATED, bool GATHERED, int NB, int MB, int W, int U>
 __device__ __forceinline__ void int8_rows_block(const Int8Args& a, const RowsItem& it, i32x4 (&sums)[W][NB][64]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -205,15 +213,25 @@ __device__ __forceinline__ void int8_rows_block(const Int8Args& a, const RowsIte
     constexpr int NC = GATED ? NB / 2 : NB;          // blocks of 16 output columns
     const int64_t n0 = (int64_t)it.nt * 16 * NC;
     const int K = (int)a.K;
-    const auto rx = make_rsrc(a.X + it.m0 * a.K);
+    const auto rx = make_rsrc(GATHERED ? a.X : a.X + it.m0 * a.K);
     const int8_t* w0 = a.W + ((int64_t)it.e * a.N + n0) * a.K;
     const auto rw = make_rsrc(w0);
     const auto rw2 = make_rsrc(GATED ? w0 + NO * a.K : w0);
-    int off[4], xk[MB], wk[NC];   // a row's byte offset; reduction values it has from this lane's 16 on
+    // a row's byte offset; reduction values it has from this lane's 16 on
+    int off[4], xoff[MB], xk[MB], wk[NC];
 #pragma unroll
     for (int b = 0; b < 4; ++b) off[b] = (16 * b + r) * K + 16 * g;
 #pragma unroll
-    for (int b = 0; b < MB; ++b) xk[b] = it.m0 + 16 * b + r < it.hi ? K - 16 * g : 0;
+    for (int b = 0; b < MB; ++b) {
+        const bool ok = it.m0 + 16 * b + r < it.hi;
+        xoff[b] = off[b];
+        xk[b] = ok ? K - 16 * g : 0;
+        if constexpr (GATHERED) {   // T * K < 2^31
+            const int32_t from = ok ? a.rows[it.m0 + 16 * b + r] : -1;
+            if ((uint32_t)from < (uint32_t)a.T) xoff[b] = from * K + 16 * g;
+            else xk[b] = 0;
+        }
+    }
 #pragma unroll
     for (int b = 0; b < NC; ++b) wk[b] = n0 + 16 * b + r < NO ? K - 16 * g : 0;
     i32x4 acc[NB][MB] = {};
@@ -228,7 +246,7 @@ __device__ __forceinline__ void int8_rows_block(const Int8Args& a, const RowsIte
                                                                  k < wk[b % NC] ? (uint32_t)(off[b % NC] + k) : kOOB, 0, 0);
 #pragma unroll
             for (int b = 0; b < MB; ++b)
-                fx[u][b] = __builtin_amdgcn_raw_buffer_load_b128(rx, k < xk[b] ? (uint32_t)(off[b] + k) : kOOB, 0, 0);
+                fx[u][b] = __builtin_amdgcn_raw_buffer_load_b128(rx, k < xk[b] ? (uint32_t)(xoff[b] + k) : kOOB, 0, 0);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -256,7 +274,7 @@ __device__ __forceinline__ void int8_rows_block(const Int8Args& a, const RowsIte
         }
         const int64_t t = it.m0 + 16 * m + r, n = n0 + 16 * wave + 4 * g;
         if (t < it.hi && n < NO) {   // NO is a multiple of 4
-            const float xs = a.xs[t];
+            const float xs = x_scale<GATHERED>(a, t);
             const float* ws = a.ws + (int64_t)it.e * a.N + n;
             const f32x4 s0 = *reinterpret_cast<const f32x4*>(ws);
             f32x4 y, s1 = s0;
@@ -277,7 +295,7 @@ __device__ __forceinline__ void int8_rows_block(const Int8Args& a, const RowsIte
 
 // With TOK = 32 at most 80 registers (six waves per SIMD), so that the blocks
 // of many experts are resident at once.
-template <bool OUT_BF16, bool GATED, int NB, int W, int TOK>
+template <bool OUT_BF16, bool GATED, bool GATHERED, int NB, int W, int TOK>
 __global__ __launch_bounds__(64 * W, TOK == 32 ? 6 : 2) void int8_rows_kernel(Int8Args a) {
     __shared__ i32x4 sums[W][NB][64];
     RowsItem it;
@@ -286,12 +304,12 @@ __global__ __launch_bounds__(64 * W, TOK == 32 ? 6 : 2) void int8_rows_kernel(In
     if (!find_rows_item<TOK>(a, (int32_t)((NO + kCols - 1) / kCols), &it)) return;
     const int64_t left = it.hi - it.m0;
     if constexpr (TOK == 32) {
-        if (left <= 16) int8_rows_block<OUT_BF16, GATED, NB, 1, W, 2>(a, it, sums);
-        else int8_rows_block<OUT_BF16, GATED, NB, 2, W, 1>(a, it, sums);
+        if (left <= 16) int8_rows_block<OUT_BF16, GATED, GATHERED, NB, 1, W, 2>(a, it, sums);
+        else int8_rows_block<OUT_BF16, GATED, GATHERED, NB, 2, W, 1>(a, it, sums);
     } else {
-        if (left <= 16) int8_rows_block<OUT_BF16, GATED, NB, 1, W, 4>(a, it, sums);
-        else if (left <= 32) int8_rows_block<OUT_BF16, GATED, NB, 2, W, 4>(a, it, sums);
-        else int8_rows_block<OUT_BF16, GATED, NB, 4, W, 2>(a, it, sums);
+        if (left <= 16) int8_rows_block<OUT_BF16, GATED, GATHERED, NB, 1, W, 4>(a, it, sums);
+        else if (left <= 32) int8_rows_block<OUT_BF16, GATED, GATHERED, NB, 2, W, 4>(a, it, sums);
+        else int8_rows_block<OUT_BF16, GATED, GATHERED, NB, 4, W, 2>(a, it, sums);
     }
 }
 
@@ -302,8 +320,13 @@ hipError_t launch_int8_rows(const Int8Args& a, bool bf16, hipStream_t s) {
     const int64_t most = (a.M / TOK + (a.M < a.E ? a.M : a.E)) * ntn;
     const dim3 grid((unsigned)most), block(64 * W);
     timing_mark("int8_rows_kernel", s);
-    if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, GATED, NB, W, TOK>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((int8_rows_kernel<false, GATED, NB, W, TOK>), grid, block, 0, s, a);
+    if (a.rows) {
+        if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, GATED, true, NB, W, TOK>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((int8_rows_kernel<false, GATED, true, NB, W, TOK>), grid, block, 0, s, a);
+    } else {
+        if (bf16) hipLaunchKernelGGL((int8_rows_kernel<true, GATED, false, NB, W, TOK>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((int8_rows_kernel<false, GATED, false, NB, W, TOK>), grid, block, 0, s, a);
+    }
     timing_end(s);
     return hipGetLastError();
 }
@@ -317,7 +340,7 @@ hipError_t launch_int8_rows(const Int8Args& a, bool bf16, hipStream_t s) {
 // blocks of 32 (a paired operand), so that a lane holds a gate and its up in
 // the accumulators of neighbouring blocks.  The epilogue scales (and gates)
 // the sums as they pass to the staged whole-line stores.
-template <int BM, int BN, bool OUT_BF16, bool GATED, int WAVES>
+template <int BM, int BN, bool OUT_BF16, bool GATED, bool GATHERED, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
     DRGG_STAGES(BM, BN, true, true, stg);
     __shared__ Sched sch;
@@ -342,7 +365,8 @@ __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
         t.rows = (int32_t)min<int64_t>(BM, oe1 - t.o0);
         t.cols = (int32_t)min<int64_t>(BC, NO - t.o1);
         t.e = e;
-        t.A = Operand{reinterpret_cast<const uint16_t*>(a.X + t.o0 * a.K), K2, t.rows, (int32_t)K2};
+        t.A = GATHERED ? Operand{reinterpret_cast<const uint16_t*>(a.X), K2, t.rows, (int32_t)K2, 0, a.rows + t.o0, a.T}
+                       : Operand{reinterpret_cast<const uint16_t*>(a.X + t.o0 * a.K), K2, t.rows, (int32_t)K2};
         t.B = Operand{reinterpret_cast<const uint16_t*>(a.W + ((int64_t)e * a.N + t.o1) * a.K), K2, t.cols,
                       (int32_t)K2, NO * a.K};
         w += G;
@@ -364,8 +388,14 @@ __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
             const bool up = GATED && c >= BM + BC;
             const float* from = c < BM ? a.xs + t.o0 + c : ws + (up ? NO - BC : 0) + (c - BM);
             const int left = c < BM ? t.rows - c : t.cols - (c - BM - (up ? BC : 0));
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                make_rsrc(from), (lds_void_t*)((lds_t*)scales[put] + c * 4), 4, lane < left ? lane * 4 : kOOB, 0, 0, 0);
+            uint32_t at = lane < left ? lane * 4 : kOOB;
+            if (GATHERED && c < BM) {
+                const int32_t row = lane < left ? a.rows[t.o0 + c + lane] : -1;
+                at = (uint32_t)row < (uint32_t)a.T ? (uint32_t)row * 4 : kOOB;
+                from = a.xs;
+            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(from), (lds_void_t*)((lds_t*)scales[put] + c * 4), 4, at, 0,
+                                                     0, 0);
         }
         put ^= 1;
     };
@@ -402,22 +432,26 @@ __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
         void* base = OUT_BF16 ? (void*)(static_cast<uint16_t*>(a.out) + o) : (void*)(static_cast<float*>(a.out) + o);
         store_tile_values<OUT_BF16, ep_rows(BM, BN), Mma, NJ>(value, rb, (lds_t*)ep, base, NO, t.rows, t.cols);
     };
-    TileRunner<BM, BN, true, true, WAVES, Int8, GATED> runner;
+    TileRunner<BM, BN, true, true, WAVES, Int8, GATED, GATHERED> runner;
     runner.st = stg;
     runner.run(more, next, finish, loads);
 }
 
+template <int BM, int BN, int WAVES, bool GATED, bool GATHERED>
+void launch_int8_tile_t(const Int8Args& a, bool bf16, dim3 grid, hipStream_t s) {
+    const dim3 block(64 * WAVES);
+    if (bf16) hipLaunchKernelGGL((int8_tile_kernel<BM, BN, true, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((int8_tile_kernel<BM, BN, false, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+}
+
 template <int BM, int BN, int WAVES>
 hipError_t launch_int8_tile(const Int8Args& a, bool gated, bool bf16, int64_t grid_n, hipStream_t s) {
-    const dim3 grid((unsigned)grid_n), block(64 * WAVES);
+    const dim3 grid((unsigned)grid_n);
     timing_mark("int8_tile_kernel", s);
-    if (gated) {
-        if (bf16) hipLaunchKernelGGL((int8_tile_kernel<BM, BN, true, true, WAVES>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((int8_tile_kernel<BM, BN, false, true, WAVES>), grid, block, 0, s, a);
-    } else {
-        if (bf16) hipLaunchKernelGGL((int8_tile_kernel<BM, BN, true, false, WAVES>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((int8_tile_kernel<BM, BN, false, false, WAVES>), grid, block, 0, s, a);
-    }
+    if (gated && a.rows) launch_int8_tile_t<BM, BN, WAVES, true, true>(a, bf16, grid, s);
+    else if (gated) launch_int8_tile_t<BM, BN, WAVES, true, false>(a, bf16, grid, s);
+    else if (a.rows) launch_int8_tile_t<BM, BN, WAVES, false, true>(a, bf16, grid, s);
+    else launch_int8_tile_t<BM, BN, WAVES, false, false>(a, bf16, grid, s);
     timing_end(s);
     return hipGetLastError();
 }

@@ -87,7 +87,8 @@ hipError_t launch_hold_cus(int n, uint64_t ticks, hipStream_t s);
 
 size_t route_table_bytes(int64_t T, int32_t E);   // the selection's workspace; 0 for one workgroup
 hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
-                            float* weights, int32_t* offsets, int32_t* positions, void* table, hipStream_t s);
+                            float* weights, int32_t* offsets, int32_t* positions, int32_t* tokens, void* table,
+                            hipStream_t s);
 hipError_t launch_moe_route_grad(const float* dweights, const float* logits, const int32_t* experts,
                                  const float* weights, int64_t T, int32_t E, int32_t k, int renormalize,
                                  float* dlogits, hipStream_t s);
@@ -112,6 +113,8 @@ struct Int8Args {
     void* out;
     int64_t M, N, K;
     int32_t E;
+    const int32_t* rows = nullptr;   // row r of the product is row rows[r] of X [T,K] and xs [T] (null: row r)
+    int64_t T = 0;
 };
 // the longest reduction whose sum fits 32 bits for any codes: 131056 * 128^2 < 2^31
 constexpr int64_t kInt8MaxK = 131056;

@@ -91,6 +91,7 @@ struct RouteArgs {
     float* weights;
     int32_t* offsets;
     int32_t* positions;
+    int32_t* tokens;   // may be null
     void* table;   // counts per block and expert, see moe_select_kernel
     int64_t T, blocks;
     int32_t E, k, renormalize;
@@ -218,8 +219,12 @@ __global__ __launch_bounds__(kRouteThreads) void moe_select_kernel(RouteArgs a) 
     for (int s = 0; s < S; ++s) {
         const int j = 16 * s + l;
         if (j < k) {
-            const int32_t r = __popcll(mask[mine[s]] & ((1ull << tl) - 1));
-            a.positions[t * k + j] = single ? start[mine[s]] + r : r;
+            int32_t r = __popcll(mask[mine[s]] & ((1ull << tl) - 1));
+            if (single) {
+                r += start[mine[s]];
+                if (a.tokens) a.tokens[r] = (int32_t)t;
+            }
+            a.positions[t * k + j] = r;
         }
     }
 }
@@ -305,7 +310,11 @@ __global__ __launch_bounds__(kRouteThreads) void moe_place_kernel(RouteArgs a) {
     __syncthreads();
     const int64_t p0 = (int64_t)blockIdx.x * kRouteTokens * a.k;
     const int64_t p1 = min(p0 + (int64_t)kRouteTokens * a.k, a.T * a.k);
-    for (int64_t p = p0 + tid; p < p1; p += kRouteThreads) a.positions[p] += base[a.experts[p]];
+    for (int64_t p = p0 + tid; p < p1; p += kRouteThreads) {
+        const int32_t at = a.positions[p] + base[a.experts[p]];
+        a.positions[p] = at;
+        if (a.tokens) a.tokens[at] = (int32_t)((uint32_t)p / (uint32_t)a.k);   // p < T * k < 2^31
+    }
 }
 
 struct RouteGradArgs {
@@ -547,8 +556,9 @@ size_t route_table_bytes(int64_t T, int32_t E) {
 }
 
 hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
-                            float* weights, int32_t* offsets, int32_t* positions, void* table, hipStream_t s) {
-    RouteArgs a{logits, experts, weights, offsets, positions, table, T, route_blocks(T), E, k, renormalize};
+                            float* weights, int32_t* offsets, int32_t* positions, int32_t* tokens, void* table,
+                            hipStream_t s) {
+    RouteArgs a{logits, experts, weights, offsets, positions, tokens, table, T, route_blocks(T), E, k, renormalize};
     const dim3 grid((unsigned)a.blocks), block(kRouteThreads);
     timing_mark("moe_select_kernel", s);
     for_experts(E, [&](auto v) {

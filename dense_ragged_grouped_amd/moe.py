@@ -12,7 +12,7 @@ W2 [E, H, I].
 """
 import torch
 
-from . import (moe_combine, moe_combine_grad, moe_dispatch, moe_ffn_int8, moe_route, moe_route_grad,
+from . import (Routing, moe_combine, moe_combine_grad, moe_dispatch, moe_ffn_int8, moe_route, moe_route_grad,
                quantize_int8)
 from .autograd import grouped_linear
 
@@ -40,11 +40,11 @@ class _Route(torch.autograd.Function):
         r = moe_route(logits, k, renormalize=renormalize)
         ctx.save_for_backward(logits, r.experts, r.weights)
         ctx.renormalize = renormalize
-        ctx.mark_non_differentiable(r.experts, r.group_offsets, r.positions)
+        ctx.mark_non_differentiable(r.experts, r.group_offsets, r.positions, r.tokens)
         return tuple(r)
 
     @staticmethod
-    def backward(ctx, _experts, dweights, _offsets, _positions):
+    def backward(ctx, _experts, dweights, _offsets, _positions, _tokens):
         logits, experts, weights = ctx.saved_tensors
         return moe_route_grad(dweights.contiguous(), logits, experts, weights, renormalize=ctx.renormalize), None, None
 
@@ -73,9 +73,9 @@ class _Combine(torch.autograd.Function):
 
 
 def route(logits, k, renormalize=True):
-    """moe_route, differentiable: (experts, weights, group_offsets, positions)
-    with the weights differentiable in the logits."""
-    return _Route.apply(logits, k, renormalize)
+    """moe_route, differentiable: a Routing whose weights are differentiable in
+    the logits."""
+    return Routing(*_Route.apply(logits, k, renormalize))
 
 
 def dispatch(X, positions):
@@ -91,7 +91,7 @@ def combine(rows, positions, weights):
 def ffn(X, logits, W1, W2, k, renormalize=True, deterministic=True):
     """The block in BF16, differentiable in X [T, H], logits [T, E] (FP32), W1
     and W2; the weight gradients as autograd.grouped_linear computes them."""
-    _, weights, offsets, positions = route(logits, k, renormalize)
-    gate, up = grouped_linear(dispatch(X, positions), W1, offsets, deterministic).chunk(2, dim=1)
+    r = route(logits, k, renormalize)
+    gate, up = grouped_linear(dispatch(X, r.positions), W1, r.group_offsets, deterministic).chunk(2, dim=1)
     h = torch.nn.functional.silu(gate) * up
-    return combine(grouped_linear(h, W2, offsets, deterministic), positions, weights)
+    return combine(grouped_linear(h, W2, r.group_offsets, deterministic), r.positions, r.weights)

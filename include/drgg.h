@@ -493,14 +493,15 @@ drgg_status drgg_tailsplit_units(int64_t tiles, int64_t workers, int64_t *out);
  * softmax runs over gets NaN weights.
  * The pairs are put in the order of their expert, pairs of one expert in
  * order of t: group_offsets [E+1] int32 as the grouped products take them
- * (o[E] = T*k), positions [T, k] int32 the row of each pair in that order.
+ * (o[E] = T*k), positions [T, k] int32 the row of each pair in that order, and,
+ * unless NULL, tokens [T*k] int32 the token of each row.
  * Workspace: moe_route_workspace_size bytes (0 for one workgroup's worth of
  * tokens), no initialisation; calls in flight at once must not share it.
  */
 drgg_status moe_route(const float *logits, int64_t T, int32_t E, int32_t k, int renormalize,
                       int32_t *experts, float *weights, int32_t *group_offsets,
-                      int32_t *positions, void *workspace, size_t workspace_bytes,
-                      hipStream_t stream);
+                      int32_t *positions, int32_t *tokens, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream);
 drgg_status moe_route_workspace_size(int64_t T, int32_t E, int32_t k, size_t *bytes);
 
 /*
@@ -559,23 +560,28 @@ drgg_status quantize_int8(const void *X, drgg_dtype dtype, int64_t T, int64_t K,
  * before M) are not written.
  * gated != 0: N = 2I, Y [M,I] = silu(g) * u with g and u columns i and I + i of
  * the product (in FP32), silu(g) = g / (1 + exp(-g)).
+ * rows (int32 [M] on the device, NULL for none; moe_route's tokens): row t of
+ * the product is row rows[t] of Xq [T,K] and x_scale [T], so that tokens need
+ * not be copied into the grouped order; T*K <= 2^31 - 4097 then (DRGG_ESHAPE).
+ * An index outside [0, T) is a row of zeros.
  * N a multiple of 8 (gated: 16), K of 16, 16 <= K <= 131056 (so that the sum
  * fits 32 bits), M < 2^31, N <= 2^22.  gemm_int8 is the one-group case
  * without offsets.  No workspace.
  */
 drgg_status grouped_gemm_int8(const int8_t *Xq, const float *x_scale, const int8_t *Wq,
-                              const float *w_scale, const int32_t *group_offsets, int32_t E,
-                              int64_t M, int64_t N, int64_t K, int gated, drgg_dtype out_dtype,
-                              void *Y, hipStream_t stream);
+                              const float *w_scale, const int32_t *group_offsets,
+                              const int32_t *rows, int64_t T, int32_t E, int64_t M, int64_t N,
+                              int64_t K, int gated, drgg_dtype out_dtype, void *Y,
+                              hipStream_t stream);
 drgg_status gemm_int8(const int8_t *Xq, const float *x_scale, const int8_t *Wq,
                       const float *w_scale, int64_t M, int64_t N, int64_t K, int gated,
                       drgg_dtype out_dtype, void *Y, hipStream_t stream);
 
 /*
  * A gated feed-forward block of E experts on 8-bit weights, the operators
- * above in one call: moe_route(logits), quantize_int8 of X [T,H] BF16 into the
- * grouped order, the gated product with W1q [E,2I,H] (gate rows, then up
- * rows; FP32 result [T*k,I]), quantize_int8 of that, the product with W2q
+ * above in one call: moe_route(logits), quantize_int8 of X [T,H] BF16, the
+ * gated product of its rows in the grouped order with W1q [E,2I,H] (gate rows,
+ * then up rows; FP32 result [T*k,I]), quantize_int8 of that, the product with W2q
  * [E,H,I] (BF16), and moe_combine into out [T,H] BF16.  The same results as
  * the single calls.  H and I multiples of 16.  Workspace:
  * moe_ffn_int8_workspace_size bytes, 16-byte aligned, no initialisation;

@@ -211,6 +211,28 @@ def test_rows_do_not_depend_on_their_company(drgg, counts):
         assert torch.equal(alone[0], out[t])
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,counts,N,K", [(3, [1, 0, 2], 48, 80), (40, [70, 0, 3, 7], 272, 336),
+                                          (500, [700, 260, 40], 144, 208), (900, [9000, 1, 7000], 1040, 144)])
+def test_gathered_rows(drgg, T, counts, N, K, dtype, gated):
+    """rows= gives the same bits as the rows copied out, in every program; an index outside is a row of zeros."""
+    rng = np.random.default_rng(T + N)
+    M, E = sum(counts), len(counts)
+    X, xs, W, ws = (dev(a) for a in operands(T, N, K, E, T + K))
+    offsets = dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    rows = rng.integers(0, T, M).astype(np.int32)
+    at = torch.from_numpy(rows).long().cuda()
+    want = drgg.grouped_gemm_int8(X[at], xs[at], W, ws, offsets, gated=gated, out_dtype=dtype)
+    got = drgg.grouped_gemm_int8(X, xs, W, ws, offsets, gated=gated, rows=dev(rows), out_dtype=dtype)
+    assert torch.equal(got, want)
+    bad = rng.choice(M, max(1, M // 50), replace=False)
+    rows[bad] = rng.choice([-1, T, 2 ** 31 - 1, -2 ** 31], len(bad))
+    got = drgg.grouped_gemm_int8(X, xs, W, ws, offsets, gated=gated, rows=dev(rows), out_dtype=dtype)
+    want[torch.from_numpy(bad).cuda()] = 0
+    assert torch.equal(got, want)
+
+
 def test_graph_and_stream(drgg):
     X, xs, W, ws = (dev(a) for a in operands(70, 64, 256, 2, 4))
     offsets = dev(np.array([0, 50, 70], np.int32))
@@ -230,6 +252,24 @@ def test_graph_and_stream(drgg):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(first, out)
+
+
+@pytest.mark.parametrize("T,H", [(16500, 131056)])
+def test_ffn_too_large_to_gather(drgg, T, H):
+    """T * H beyond 2^31: the block copies its tokens into the grouped order
+    instead.  Rows do not depend on their company: the first and the last
+    tokens give the same bits in a small call."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    X = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    logits = torch.randn((T, 2), generator=g, device="cuda")
+    w1 = torch.randint(-127, 128, (2, 32, H), generator=g, device="cuda", dtype=torch.int8)
+    w2 = torch.randint(-127, 128, (2, H, 16), generator=g, device="cuda", dtype=torch.int8)
+    s1, s2 = torch.full((2, 32), 1e-4, device="cuda"), torch.full((2, H), 1e-3, device="cuda")
+    out = drgg.moe_ffn_int8(X, logits, w1, s1, w2, s2, 1)
+    few = torch.cat([torch.arange(5), torch.arange(T - 5, T)]).cuda()
+    small = drgg.moe_ffn_int8(X[few], logits[few], w1, s1, w2, s2, 1)
+    assert torch.equal(out[few], small)
 
 
 # ---- the block ----------------------------------------------------------------------
@@ -339,6 +379,8 @@ def test_refusals(drgg):
     with pytest.raises(drgg.DrggError):   # a sum that may not fit 32 bits
         drgg.gemm_int8(torch.zeros((1, 131072), dtype=torch.int8, device="cuda"), xs[:1].contiguous(),
                        torch.zeros((8, 131072), dtype=torch.int8, device="cuda"), ws[0, :8].contiguous())
+    with pytest.raises(TypeError):
+        drgg.grouped_gemm_int8(X, xs, W, ws, offsets, rows=torch.zeros(4, dtype=torch.int64, device="cuda"))
     with pytest.raises(ValueError):
         drgg.gemm_int8(X, xs, W[0], ws[0], out_dtype=torch.float16)
     with pytest.raises(drgg.DrggError):

@@ -123,6 +123,7 @@ def test_route(drgg, T, E, k, kind, renormalize):
     assert np.array_equal(host(r.experts), experts)
     assert np.array_equal(host(r.positions), positions)
     assert np.array_equal(host(r.group_offsets), offsets)
+    assert np.array_equal(host(r.tokens)[positions.reshape(-1)], np.repeat(np.arange(T), k))
     w, want = host(r.weights), weights64(logits, experts, renormalize)
     assert np.all(np.abs(w - want) <= weight_tolerance(logits, experts) * want + 2.0 ** -126)
     if kind == "masked":
@@ -141,6 +142,7 @@ def test_route_many_tokens(drgg, T, E, k, kind):
     positions[order] = np.arange(T * k)
     assert np.array_equal(host(r.experts), experts)
     assert np.array_equal(host(r.positions).reshape(-1), positions)
+    assert np.array_equal(host(r.tokens), order // k)
     assert np.array_equal(host(r.group_offsets), np.searchsorted(flat[order], np.arange(E + 1)))
 
 
