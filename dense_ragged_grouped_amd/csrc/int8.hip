@@ -74,7 +74,9 @@ __device__ __forceinline__ void load16(float (&f)[16], const void* X, int64_t i)
     }
 }
 
-template <bool BF16>
+// HELD: a thread's values of the row (at most 16) stay in registers between
+// the maximum and the codes; longer rows are read again, from L2.
+template <bool BF16, bool HELD>
 __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
     __shared__ uint32_t part[4];
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -82,12 +84,13 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
     // the largest magnitude as bits: their unsigned order is the order of the
     // magnitudes, with infinity and NaN above every finite value
     uint32_t m = 0;
+    float f[16];
     if (live)
         for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
-            float f[16];
             load16<BF16>(f, a.X, t * a.C + c);
 #pragma unroll
             for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+            if constexpr (HELD) break;
         }
     const int width = blockDim.x < 64 ? blockDim.x : 64;
     for (int d = 1; d < width; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
@@ -106,8 +109,7 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
     const float by = bad || m == 0 ? 1.f : most * down;
     const int64_t R = a.T * a.k;
     for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
-        float f[16];
-        load16<BF16>(f, a.X, t * a.C + c);
+        if constexpr (!HELD) load16<BF16>(f, a.X, t * a.C + c);
         u32x4 out;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -125,6 +127,7 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
             reinterpret_cast<u32x4*>(a.q)[p * a.C + c] = out;
             if (c == 0) a.scale[p] = scale;
         }
+        if constexpr (HELD) break;
     }
 }
 
@@ -465,8 +468,13 @@ hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, 
     while (x < 256 && x < a.C) x *= 2;
     const dim3 block(x, 256 / x), grid((unsigned)ceil_div(T, block.y));
     timing_mark("quantize_int8_kernel", s);
-    if (bf16) hipLaunchKernelGGL(quantize_int8_kernel<true>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(quantize_int8_kernel<false>, grid, block, 0, s, a);
+    if (a.C <= x) {
+        if (bf16) hipLaunchKernelGGL((quantize_int8_kernel<true, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((quantize_int8_kernel<false, true>), grid, block, 0, s, a);
+    } else {
+        if (bf16) hipLaunchKernelGGL((quantize_int8_kernel<true, false>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((quantize_int8_kernel<false, false>), grid, block, 0, s, a);
+    }
     timing_end(s);
     return hipGetLastError();
 }

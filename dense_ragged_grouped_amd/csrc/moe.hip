@@ -151,16 +151,27 @@ __global__ __launch_bounds__(kRouteThreads) void moe_select_kernel(RouteArgs a) 
     // a wave without tokens does not compete with the others
     const int rounds = (int64_t)blockIdx.x * kRouteTokens + (__builtin_amdgcn_readfirstlane(threadIdx.x) >> 4) < a.T ? k : 0;
     for (int j = 0; j < rounds; ++j) {
-        uint32_t m = key[0];
+        uint32_t m[V];
 #pragma unroll
-        for (int i = 1; i < V; ++i) m = max(m, key[i]);
-        const uint32_t best = row_max(m);
-        uint32_t at = 0xFFFFu;
+        for (int i = 0; i < V; ++i) m[i] = key[i];
 #pragma unroll
-        for (int i = V - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)(64 * (i >> 2) + (i & 3)) : at;
-        const uint32_t e = row_min(at == 0xFFFFu ? at : at + 4 * l);
+        for (int d = 1; d < V; d *= 2)
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = e == (uint32_t)(64 * (i >> 2) + (i & 3)) + 4 * l ? 0u : key[i];
+            for (int i = 0; i < V; i += 2 * d) m[i] = max(m[i], m[i + d]);
+        const uint32_t best = row_max(m[0]);
+        // the lane's lowest expert with that key (no chain through the keys:
+        // a wave alone on its SIMD waits for every dependent result)
+        uint32_t is[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) is[i] = key[i] == best ? (uint32_t)(64 * (i >> 2) + (i & 3)) : 0xFFFFu;
+#pragma unroll
+        for (int d = 1; d < V; d *= 2)
+#pragma unroll
+            for (int i = 0; i < V; i += 2 * d) is[i] = min(is[i], is[i + d]);
+        const uint32_t e = row_min(is[0] + 4 * l);   // above every index where there is none
+        const uint32_t mine_at = e - 4 * l;          // the taken key's place, if it is this lane's
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = mine_at == (uint32_t)(64 * (i >> 2) + (i & 3)) ? 0u : key[i];
         if (j == 0) top = best;
 #pragma unroll
         for (int s = 0; s < S; ++s)
@@ -310,10 +321,12 @@ __global__ __launch_bounds__(kRouteThreads) void moe_place_kernel(RouteArgs a) {
     __syncthreads();
     const int64_t p0 = (int64_t)blockIdx.x * kRouteTokens * a.k;
     const int64_t p1 = min(p0 + (int64_t)kRouteTokens * a.k, a.T * a.k);
+    // pair / k by a multiplication, exact for the block's pairs (below 64 * 64)
+    const uint32_t by_k = ((1u << 20) + a.k - 1) / a.k;
     for (int64_t p = p0 + tid; p < p1; p += kRouteThreads) {
         const int32_t at = a.positions[p] + base[a.experts[p]];
         a.positions[p] = at;
-        if (a.tokens) a.tokens[at] = (int32_t)((uint32_t)p / (uint32_t)a.k);   // p < T * k < 2^31
+        if (a.tokens) a.tokens[at] = (int32_t)(blockIdx.x * kRouteTokens + (((uint32_t)(p - p0) * by_k) >> 20));
     }
 }
 
@@ -468,22 +481,44 @@ __global__ __launch_bounds__(256) void moe_dispatch_kernel(RowArgs a) {
     }
 }
 
-// FP32 sum over j in order, one rounding.
+// The grouped rows of pairs j0 .. j0+3 of token t and their weights; row -1
+// for a pair past k, a position outside the rows, or a token past the end.
+constexpr int kPairs = 4;
+__device__ __forceinline__ void load_pairs(const RowArgs& a, int64_t t, int j0, int64_t (&row)[kPairs],
+                                           float (&w)[kPairs]) {
+    const int64_t R = a.T * a.k;
+#pragma unroll
+    for (int u = 0; u < kPairs; ++u) {
+        const bool in = t < a.T && j0 + u < a.k;
+        const int64_t p = in ? a.positions[t * a.k + j0 + u] : -1;
+        row[u] = p < R ? p : -1;
+        w[u] = in && a.weights ? a.weights[t * a.k + j0 + u] : 1.f;
+    }
+}
+
+// FP32 sum over j in order, one rounding.  Four rows are loaded before the
+// first is added: 604 MB for 16384 tokens, k = 8, H = 2048 in BF16 in 140 us
+// with one row at a time.
 template <bool BF16>
 __global__ __launch_bounds__(256) void moe_combine_kernel(RowArgs a) {
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
-    const int64_t R = a.T * a.k;
     for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
         float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t p = a.positions[t * a.k + j];
-            if (p < 0 || p >= R) continue;
-            const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
-            Piece<BF16> x;
-            x.load(a.src, p * a.C + c);
+        for (int j0 = 0; j0 < a.k; j0 += kPairs) {
+            int64_t row[kPairs];
+            float w[kPairs];
+            load_pairs(a, t, j0, row, w);
+            Piece<BF16> x[kPairs];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] += w * x.get(i);
+            for (int u = 0; u < kPairs; ++u)
+                if (row[u] >= 0) x[u].load(a.src, row[u] * a.C + c);
+#pragma unroll
+            for (int u = 0; u < kPairs; ++u)
+                if (row[u] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[i] += w[u] * x[u].get(i);
+                }
         }
         Piece<BF16> y;
         y.set(s);
@@ -493,47 +528,60 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(RowArgs a) {
 
 // drows[position] = w * dout (one rounding) and dweights = <dout, row>, an
 // FP32 sum: per thread over its pieces, then over the token's threads in a
-// fixed tree.
+// fixed tree.  Four pairs at a time.
 template <bool BF16>
 __global__ __launch_bounds__(256) void moe_combine_grad_kernel(RowArgs a) {
-    __shared__ float part[4];
+    __shared__ float part[4][kPairs];
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int64_t R = a.T * a.k;
-    const bool live = t < a.T;
-    for (int j = 0; j < a.k; ++j) {
-        float dot = 0.f;
-        int64_t p = live ? a.positions[t * a.k + j] : -1;
-        if (p >= R) p = -1;
-        if (p >= 0) {
-            const float w = a.weights[t * a.k + j];
+    for (int j0 = 0; j0 < a.k; j0 += kPairs) {
+        int64_t row[kPairs];
+        float w[kPairs], dot[kPairs] = {0.f, 0.f, 0.f, 0.f};
+        load_pairs(a, t, j0, row, w);
+        if (t < a.T)
             for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
-                Piece<BF16> g, x, y;
+                Piece<BF16> g, x[kPairs];
                 g.load(a.src, t * a.C + c);
-                x.load(a.rows, p * a.C + c);
-                float f[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dot += g.get(i) * x.get(i);
-                    f[i] = w * g.get(i);
-                }
-                y.set(f);
-                y.store(a.dst, p * a.C + c);
+                for (int u = 0; u < kPairs; ++u)
+                    if (row[u] >= 0) x[u].load(a.rows, row[u] * a.C + c);
+#pragma unroll
+                for (int u = 0; u < kPairs; ++u)
+                    if (row[u] >= 0) {
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            dot[u] += g.get(i) * x[u].get(i);
+                            f[i] = w[u] * g.get(i);
+                        }
+                        Piece<BF16> y;
+                        y.set(f);
+                        y.store(a.dst, row[u] * a.C + c);
+                    }
             }
-        }
         // the token's threads: up to 64 lanes of one wave, then whole waves
         const int width = blockDim.x < 64 ? blockDim.x : 64;
-        for (int m = 1; m < width; m <<= 1) dot += __shfl_xor(dot, m, 64);
+        for (int m = 1; m < width; m <<= 1)
+#pragma unroll
+            for (int u = 0; u < kPairs; ++u) dot[u] += __shfl_xor(dot[u], m, 64);
         if (blockDim.x > 64) {
             const int wave = (threadIdx.y * blockDim.x + threadIdx.x) >> 6;
             __syncthreads();
-            if ((threadIdx.x & 63) == 0) part[wave] = dot;
+            if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                for (int u = 0; u < kPairs; ++u) part[wave][u] = dot[u];
             __syncthreads();
             if (threadIdx.x == 0) {
-                dot = 0.f;
-                for (unsigned q = 0; q < blockDim.x / 64; ++q) dot += part[wave + q];
+#pragma unroll
+                for (int u = 0; u < kPairs; ++u) dot[u] = 0.f;
+                for (unsigned q = 0; q < blockDim.x / 64; ++q)
+#pragma unroll
+                    for (int u = 0; u < kPairs; ++u) dot[u] += part[wave + q][u];
             }
         }
-        if (threadIdx.x == 0 && live) a.dweights[t * a.k + j] = dot;
+        if (threadIdx.x == 0 && t < a.T)
+#pragma unroll
+            for (int u = 0; u < kPairs; ++u)
+                if (j0 + u < a.k) a.dweights[t * a.k + j0 + u] = dot[u];
     }
 }
 
