@@ -52,6 +52,8 @@ drgg_status device_error(hipError_t e) {
     return DRGG_EDEVICE;
 }
 
+int knob_tile() { return (int)g_knob_tile.load(); }
+
 bool checks_offsets() { return g_knob_check_offsets.load() != 0 || env_flag("DRGG_CHECK_OFFSETS"); }
 
 // CU count of the current device, cached per device.

@@ -60,7 +60,7 @@ drgg_status run_int8(const int8_t* Xq, const float* x_scale, const int8_t* Wq, c
     drgg_status st = current_cu_count(&cus);
     if (st != DRGG_OK) return st;
     Int8Args a{Xq, Wq, x_scale, w_scale, offs, Y, M, N, K, E, rows, T};
-    return launch_status(launch_int8(a, gated != 0, dt == DRGG_BF16, cus, s));
+    return launch_status(launch_int8(a, gated != 0, dt == DRGG_BF16, cus, knob_tile(), s));
 }
 
 // The parts of moe_ffn_int8's workspace (byte offsets, multiples of 256).  The
@@ -250,10 +250,10 @@ drgg_status moe_ffn_int8(const void* X, const float* logits, const int8_t* W1q, 
         e = launch_quantize_int8(X, true, T, H, L.gather ? nullptr : positions, L.gather ? 1 : k, x, xs, stream);
     if (e == hipSuccess)
         e = launch_int8(Int8Args{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E, L.gather ? tokens : nullptr, T},
-                        true, false, cus, stream);
+                        true, false, cus, knob_tile(), stream);
     if (e == hipSuccess) e = launch_quantize_int8(ws + L.h, false, R, I, nullptr, 1, hq, hs, stream);
     if (e == hipSuccess)
-        e = launch_int8(Int8Args{hq, W2q, hs, w2_scale, offsets, ws + L.y, R, H, I, E}, false, true, cus, stream);
+        e = launch_int8(Int8Args{hq, W2q, hs, w2_scale, offsets, ws + L.y, R, H, I, E}, false, true, cus, knob_tile(), stream);
     if (e == hipSuccess) e = launch_moe_combine(ws + L.y, positions, weights, T, k, H, true, out, stream);
     return launch_status(e);
 }

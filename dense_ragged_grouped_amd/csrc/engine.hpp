@@ -75,11 +75,14 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t h) {
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) char lds_t;
 
-struct Sched {
+// SCAN: words of scratch; the schedule alone needs one per wave and one more.
+template <int SCAN>
+struct SchedOf {
     int32_t offs[kMaxExperts + 1];    // clamped, non-decreasing offsets
     int32_t prefix[kMaxExperts + 1];  // exclusive prefix of work per expert
-    int32_t scan[kMaxGemmThreads];
+    int32_t scan[SCAN];
 };
+using Sched = SchedOf<kMaxGemmThreads>;
 
 // Exclusive scan of v over the workgroup's threads (in thread order), with
 // the sum (MAX = false) or the maximum (MAX = true, identity 0: the values
@@ -157,8 +160,8 @@ __device__ __forceinline__ int32_t wave_incl_sum(int32_t x) {
 // uniform: offs[e] = e * T.  With fewer than kWaveExperts experts wave 0
 // does it all (offsets on lanes 0..E, shuffle scans).  Must be called by all
 // threads; ends with a barrier.
-template <class WorkFn>
-__device__ void build_schedule(Sched& s, const int32_t* __restrict__ offs, int E, int64_t M, int64_t T,
+template <int SCAN, class WorkFn>
+__device__ void build_schedule(SchedOf<SCAN>& s, const int32_t* __restrict__ offs, int E, int64_t M, int64_t T,
                                WorkFn work) {
     const int tid = threadIdx.x, nthr = blockDim.x;
     if (E < kWaveExperts) {
@@ -328,7 +331,8 @@ __device__ __forceinline__ int32_t uni(int32_t v) { return __builtin_amdgcn_read
 // Largest e < n with prefix[e] <= w (so that prefix[e] <= w < prefix[e+1]
 // when w < prefix[n]); n is the number of experts, or of positions of a
 // plan's walk.
-__device__ __forceinline__ int find_expert(const Sched& s, int n, int32_t w) {
+template <int SCAN>
+__device__ __forceinline__ int find_expert(const SchedOf<SCAN>& s, int n, int32_t w) {
     int lo = 0, hi = n;   // answer in [0, n)
     while (lo < hi) {
         int mid = (lo + hi + 1) >> 1;

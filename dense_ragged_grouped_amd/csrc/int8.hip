@@ -346,7 +346,7 @@ hipError_t launch_int8_rows(const Int8Args& a, bool bf16, hipStream_t s) {
 template <int BM, int BN, bool OUT_BF16, bool GATED, bool GATHERED, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
     DRGG_STAGES(BM, BN, true, true, stg);
-    __shared__ Sched sch;
+    __shared__ SchedOf<16> sch;
     __shared__ __attribute__((aligned(16))) char ep[WAVES * ep_rows(BM, BN) * 128];
     using Mma = TileMma<BM, BN, true, true, WAVES, Int8>;
     constexpr int BC = GATED ? BN / 2 : BN;             // output columns per tile
@@ -443,8 +443,13 @@ __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
 template <int BM, int BN, int WAVES, bool GATED, bool GATHERED>
 void launch_int8_tile_t(const Int8Args& a, bool bf16, dim3 grid, hipStream_t s) {
     const dim3 block(64 * WAVES);
-    if (bf16) hipLaunchKernelGGL((int8_tile_kernel<BM, BN, true, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((int8_tile_kernel<BM, BN, false, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+    constexpr bool kBf16 = !GATED || BN >= 256;   // a gated 128x128 tile has 32 columns per wave, half a BF16 line
+    if constexpr (kBf16)
+        if (bf16) {
+            hipLaunchKernelGGL((int8_tile_kernel<BM, BN, true, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+            return;
+        }
+    hipLaunchKernelGGL((int8_tile_kernel<BM, BN, false, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
 }
 
 template <int BM, int BN, int WAVES>
@@ -479,17 +484,21 @@ hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, 
     return hipGetLastError();
 }
 
-// Which program runs, from the sizes alone.  M rows in E groups of unknown
+// Which program runs, from the sizes alone (forced_tile: the test knob; a tile
+// this product has, or none).  M rows in E groups of unknown
 // sizes make about M/64 + E/2 blocks of 64 tokens.
-hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, hipStream_t s) {
+hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s) {
+    const bool may128 = !(gated && bf16);
+    int tile = forced_tile;
+    if (tile != kTile256x256 && tile != kTile128x256 && !(tile == kTile128x128 && may128)) tile = kTileAuto;
     const int64_t cols = ceil_div(a.N, 64), blocks = cols * (ceil_div(a.M, 64) + (a.E - 1) / 2);
-    if (cols * a.E >= 2 * kRuleCUs && a.M <= 24 * (int64_t)a.E) {
+    if (tile == kTileAuto && cols * a.E >= 2 * kRuleCUs && a.M <= 24 * (int64_t)a.E) {
         // many experts' weights, few rows of each: read at memory speed (E = 32,
         // 1536x2048: 256 rows 20 us, 512 rows 23, 768 rows 30; in 128x256 tiles
         // 27, 28 and 29; 57 x 1000x1008, 1368 rows: 15 against 19)
         return gated ? launch_int8_rows<true, 4, 4, 32>(a, bf16, s) : launch_int8_rows<false, 4, 4, 32>(a, bf16, s);
     }
-    if (blocks <= 2 * kRuleCUs) {
+    if (tile == kTileAuto && blocks <= 2 * kRuleCUs) {
         // at most two blocks per CU: the largest blocks that leave none idle
         // (4096x4096, one group: 1 row 8 us, 128 rows 16, 256 rows 20, 512
         // rows 34; in 128x256 tiles 31 to 33)
@@ -499,17 +508,16 @@ hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, hipStr
         return 2 * blocks >= kRuleCUs ? launch_int8_rows<false, 2, 8, 64>(a, bf16, s)
                                       : launch_int8_rows<false, 1, 8, 64>(a, bf16, s);
     }
-    // the tile whose rounds of (about) full waves cost less, a 256x256 one
-    // taking 1.25 times as long as one of 128x256 (measured 1.1 to 1.3, alone
-    // on a CU; E = 32, 1536x2048: 4096 rows 34 against 51 us, 8192 rows 65
-    // against 53, 16384 rows 75 against 97)
-    const int64_t nc = ceil_div(gated ? a.N / 2 : a.N, gated ? 128 : 256);
-    auto rounds = [&](int64_t bm) { return ceil_div((ceil_div(a.M, bm) + (a.E - 1) / 2) * nc, kRuleCUs); };
-    const bool large = 5 * rounds(256) <= 4 * rounds(128);
-    const int64_t most = (a.M / (large ? 256 : 128) + (a.M < a.E ? a.M : a.E)) * nc;
-    const int64_t grid_n = most < cus ? most : cus;
-    if (large) return launch_int8_tile<256, 256, 8>(a, gated, bf16, grid_n, s);
-    return launch_int8_tile<128, 256, 4>(a, gated, bf16, grid_n, s);
+    const int64_t cols_out = gated ? a.N / 2 : a.N, bc = gated ? 128 : 256;
+    if (tile == kTileAuto)
+        tile = int8_tile(a.E, a.M, a.K, ceil_div(cols_out, bc), ceil_div(cols_out, bc / 2), may128);
+    auto grid = [&](int64_t bm, int64_t bcols, int64_t per_cu) {
+        const int64_t most = (a.M / bm + (a.M < a.E ? a.M : a.E)) * ceil_div(cols_out, bcols);
+        return most < per_cu * cus ? most : per_cu * cus;
+    };
+    if (tile == kTile256x256) return launch_int8_tile<256, 256, 8>(a, gated, bf16, grid(256, bc, 1), s);
+    if (tile == kTile128x256) return launch_int8_tile<128, 256, 4>(a, gated, bf16, grid(128, bc, 1), s);
+    return launch_int8_tile<128, 128, 4>(a, gated, bf16, grid(128, bc / 2, 2), s);
 }
 
 }  // namespace drgg

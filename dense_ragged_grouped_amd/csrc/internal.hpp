@@ -30,6 +30,9 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 drgg_status device_error(hipError_t e);
 inline drgg_status launch_status(hipError_t e) { return e == hipSuccess ? DRGG_OK : device_error(e); }
 
+// DRGG_KNOB_TILE (api.cpp)
+int knob_tile();
+
 // CU count of the current device (api.cpp)
 drgg_status current_cu_count(int* cus);
 
@@ -118,7 +121,7 @@ struct Int8Args {
 };
 // the longest reduction whose sum fits 32 bits for any codes: 131056 * 128^2 < 2^31
 constexpr int64_t kInt8MaxK = 131056;
-hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, hipStream_t s);
+hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s);
 
 // Per-launch timing marks (a measurement knob, off by default): when on, an
 // event is recorded on the stream before every kernel launch of a call and

@@ -342,7 +342,9 @@ drgg_status drgg_wgrad_chunking(int64_t T, int64_t chunk_max, int64_t *chunk_len
 /*
  * Test knobs (process-wide; not thread-safe; 0 restores the default):
  *   DRGG_KNOB_TILE        force the output tile of fwd/dgrad/det-wgrad:
- *                         1 = 256x256, 2 = 128x128, 3 = 256x128, 4 = 128x256
+ *                         1 = 256x256, 2 = 128x128, 3 = 256x128, 4 = 128x256;
+ *                         an 8-bit product then runs in that tile (1, 2, 4;
+ *                         2 not for a gated BF16 result) whatever its rows
  *   DRGG_KNOB_GRID        force the workgroup count of the persistent kernels
  *                         (every program)
  *   DRGG_KNOB_REVERSE     1 = walk the work items in reverse order

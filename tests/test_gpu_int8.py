@@ -172,6 +172,34 @@ def test_dense(drgg, M, N, K, gated):
 
 
 @pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("tile", [1, 2, 4])
+@pytest.mark.parametrize("counts,N,K", [([1], 16, 16), ([0, 130, 5, 64], 48, 80), ([300, 1, 0, 257, 128], 528, 1040),
+                                        ([9] * 70, 272, 336), ([2000, 3000], 1040, 272)])
+def test_every_tile(drgg, counts, N, K, tile, gated):
+    """Each output tile, forced, gives the bits of the program chosen for the sizes (the sums are exact and scaled in one
+    way), and the exact product within the tolerance; with and without gathered rows."""
+    E, M = len(counts), sum(counts)
+    X, xs, W, ws = operands(M, N, K, E, M + K)
+    if gated:
+        xs = xs / np.float32(16 * np.sqrt(K))
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    args = [dev(a) for a in (X, xs, W, ws, offsets)]
+    rows = torch.randperm(M, device="cuda").to(torch.int32)
+    back = torch.argsort(rows)
+    for dtype in (torch.bfloat16, torch.float32):
+        free = drgg.grouped_gemm_int8(*args, gated=gated, out_dtype=dtype)
+        drgg.set_knob(drgg.KNOB_TILE, tile)
+        try:
+            got = drgg.grouped_gemm_int8(*args, gated=gated, out_dtype=dtype)
+            gathered = drgg.grouped_gemm_int8(args[0][rows.long()], args[1][rows.long()], *args[2:], gated=gated,
+                                              rows=back.to(torch.int32), out_dtype=dtype)
+        finally:
+            drgg.set_knob(drgg.KNOB_TILE, 0)
+        assert torch.equal(got, free) and torch.equal(gathered, free)
+        check(host(got), grouped64(X, xs, W, ws, offsets), dtype, gated)
+
+
+@pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("N,K", [(1040, 208), (2064, 16), (1040, 528)])
 def test_many_rows(drgg, N, K, dtype, gated):
