@@ -24,6 +24,7 @@ drgg_status check_pairs(int64_t T, int32_t k) {
 
 drgg_status check_route(int64_t T, int32_t E, int32_t k) {
     if (E < 1 || E > kMaxExperts || k > E) return DRGG_EINVAL;
+    if (T > (int64_t(1) << 27)) return DRGG_ESHAPE;   // 16 threads per token in one launch
     return check_pairs(T, k);
 }
 

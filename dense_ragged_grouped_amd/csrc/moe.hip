@@ -131,9 +131,10 @@ __device__ __forceinline__ int32_t block_prefix(int32_t v, int32_t* tmp) {
 // ranks for moe_place_kernel and the counts go to the table: bytes (at most
 // 64 each) [blocks][E rounded up to 4], or with more than kRouteBytes blocks
 // words [blocks][E] for moe_scan_kernel.
-// Bound by the vector unit: 8 us for 16384 tokens, k = 8 of 256 experts
-// (2.1 TB/s of logits); with a wave per token and shuffles through LDS it
-// was 21 us.
+// Bound by the latency of the k dependent rounds: 12 us for 16384 tokens, k = 8
+// of 256 experts (16.8 MB of logits, 3.4 us at the rate of a large copy), 4 us
+// for 2039 tokens, k = 2 of 32; with a wave per token and shuffles through LDS
+// 21 and 12 us.
 template <int V, int S>
 __global__ __launch_bounds__(kRouteThreads) void moe_select_kernel(RouteArgs a) {
     __shared__ unsigned long long mask[16 * V];
@@ -468,17 +469,16 @@ struct RowArgs {
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void moe_dispatch_kernel(RowArgs a) {
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= a.T) return;
-    const int64_t R = a.T * a.k;
-    for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
-        Piece<BF16> x;
-        x.load(a.src, t * a.C + c);
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t p = a.positions[t * a.k + j];
-            if (p >= 0 && p < R) x.store(a.dst, p * a.C + c);
+    const int64_t R = a.T * a.k, step = (int64_t)gridDim.x * blockDim.y;
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += step)
+        for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
+            Piece<BF16> x;
+            x.load(a.src, t * a.C + c);
+            for (int j = 0; j < a.k; ++j) {
+                const int64_t p = a.positions[t * a.k + j];
+                if (p >= 0 && p < R) x.store(a.dst, p * a.C + c);
+            }
         }
-    }
 }
 
 // The grouped rows of pairs j0 .. j0+3 of token t and their weights; row -1
@@ -497,91 +497,97 @@ __device__ __forceinline__ void load_pairs(const RowArgs& a, int64_t t, int j0, 
 }
 
 // FP32 sum over j in order, one rounding.  Four rows are loaded before the
-// first is added: 604 MB for 16384 tokens, k = 8, H = 2048 in BF16 in 140 us
-// with one row at a time.
+// first is added.  Bound by memory: 604 MB for 16384 tokens, k = 8, H = 2048 in
+// BF16 in 117 to 135 us (5.2 to 4.5 TB/s; a large copy reaches 5.0), 140 us with
+// one row at a time.  Non-temporal loads and stores gained 7 % there and cost
+// 15 to 25 % where the rows or the result still fit the last-level cache.
 template <bool BF16>
 __global__ __launch_bounds__(256) void moe_combine_kernel(RowArgs a) {
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= a.T) return;
-    for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
-        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int j0 = 0; j0 < a.k; j0 += kPairs) {
-            int64_t row[kPairs];
-            float w[kPairs];
-            load_pairs(a, t, j0, row, w);
-            Piece<BF16> x[kPairs];
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += step)
+        for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
+            float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int j0 = 0; j0 < a.k; j0 += kPairs) {
+                int64_t row[kPairs];
+                float w[kPairs];
+                load_pairs(a, t, j0, row, w);
+                Piece<BF16> x[kPairs];
 #pragma unroll
-            for (int u = 0; u < kPairs; ++u)
-                if (row[u] >= 0) x[u].load(a.src, row[u] * a.C + c);
+                for (int u = 0; u < kPairs; ++u)
+                    if (row[u] >= 0) x[u].load(a.src, row[u] * a.C + c);
 #pragma unroll
-            for (int u = 0; u < kPairs; ++u)
-                if (row[u] >= 0) {
+                for (int u = 0; u < kPairs; ++u)
+                    if (row[u] >= 0) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[i] += w[u] * x[u].get(i);
-                }
+                        for (int i = 0; i < 8; ++i) s[i] += w[u] * x[u].get(i);
+                    }
+            }
+            Piece<BF16> y;
+            y.set(s);
+            y.store(a.dst, t * a.C + c);
         }
-        Piece<BF16> y;
-        y.set(s);
-        y.store(a.dst, t * a.C + c);
-    }
 }
 
 // drows[position] = w * dout (one rounding) and dweights = <dout, row>, an
 // FP32 sum: per thread over its pieces, then over the token's threads in a
-// fixed tree.  Four pairs at a time.
+// fixed tree.  Four pairs at a time.  Bound by memory: 1.14 GB at those sizes
+// in 210 to 226 us.
 template <bool BF16>
 __global__ __launch_bounds__(256) void moe_combine_grad_kernel(RowArgs a) {
     __shared__ float part[4][kPairs];
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    for (int j0 = 0; j0 < a.k; j0 += kPairs) {
-        int64_t row[kPairs];
-        float w[kPairs], dot[kPairs] = {0.f, 0.f, 0.f, 0.f};
-        load_pairs(a, t, j0, row, w);
-        if (t < a.T)
-            for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
-                Piece<BF16> g, x[kPairs];
-                g.load(a.src, t * a.C + c);
+    // whole blocks of tokens: every thread takes part in the sums
+    for (int64_t t0 = (int64_t)blockIdx.x * blockDim.y; t0 < a.T; t0 += (int64_t)gridDim.x * blockDim.y) {
+        const int64_t t = t0 + threadIdx.y;
+        for (int j0 = 0; j0 < a.k; j0 += kPairs) {
+            int64_t row[kPairs];
+            float w[kPairs], dot[kPairs] = {0.f, 0.f, 0.f, 0.f};
+            load_pairs(a, t, j0, row, w);
+            if (t < a.T)
+                for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
+                    Piece<BF16> g, x[kPairs];
+                    g.load(a.src, t * a.C + c);
 #pragma unroll
-                for (int u = 0; u < kPairs; ++u)
-                    if (row[u] >= 0) x[u].load(a.rows, row[u] * a.C + c);
+                    for (int u = 0; u < kPairs; ++u)
+                        if (row[u] >= 0) x[u].load(a.rows, row[u] * a.C + c);
 #pragma unroll
-                for (int u = 0; u < kPairs; ++u)
-                    if (row[u] >= 0) {
-                        float f[8];
+                    for (int u = 0; u < kPairs; ++u)
+                        if (row[u] >= 0) {
+                            float f[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            dot[u] += g.get(i) * x[u].get(i);
-                            f[i] = w[u] * g.get(i);
+                            for (int i = 0; i < 8; ++i) {
+                                dot[u] += g.get(i) * x[u].get(i);
+                                f[i] = w[u] * g.get(i);
+                            }
+                            Piece<BF16> y;
+                            y.set(f);
+                            y.store(a.dst, row[u] * a.C + c);
                         }
-                        Piece<BF16> y;
-                        y.set(f);
-                        y.store(a.dst, row[u] * a.C + c);
-                    }
+                }
+            // the token's threads: up to 64 lanes of one wave, then whole waves
+            const int width = blockDim.x < 64 ? blockDim.x : 64;
+            for (int m = 1; m < width; m <<= 1)
+#pragma unroll
+                for (int u = 0; u < kPairs; ++u) dot[u] += __shfl_xor(dot[u], m, 64);
+            if (blockDim.x > 64) {
+                const int wave = (threadIdx.y * blockDim.x + threadIdx.x) >> 6;
+                __syncthreads();
+                if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                    for (int u = 0; u < kPairs; ++u) part[wave][u] = dot[u];
+                __syncthreads();
+                if (threadIdx.x == 0) {
+#pragma unroll
+                    for (int u = 0; u < kPairs; ++u) dot[u] = 0.f;
+                    for (unsigned q = 0; q < blockDim.x / 64; ++q)
+#pragma unroll
+                        for (int u = 0; u < kPairs; ++u) dot[u] += part[wave + q][u];
+                }
             }
-        // the token's threads: up to 64 lanes of one wave, then whole waves
-        const int width = blockDim.x < 64 ? blockDim.x : 64;
-        for (int m = 1; m < width; m <<= 1)
+            if (threadIdx.x == 0 && t < a.T)
 #pragma unroll
-            for (int u = 0; u < kPairs; ++u) dot[u] += __shfl_xor(dot[u], m, 64);
-        if (blockDim.x > 64) {
-            const int wave = (threadIdx.y * blockDim.x + threadIdx.x) >> 6;
-            __syncthreads();
-            if ((threadIdx.x & 63) == 0)
-#pragma unroll
-                for (int u = 0; u < kPairs; ++u) part[wave][u] = dot[u];
-            __syncthreads();
-            if (threadIdx.x == 0) {
-#pragma unroll
-                for (int u = 0; u < kPairs; ++u) dot[u] = 0.f;
-                for (unsigned q = 0; q < blockDim.x / 64; ++q)
-#pragma unroll
-                    for (int u = 0; u < kPairs; ++u) dot[u] += part[wave + q][u];
-            }
+                for (int u = 0; u < kPairs; ++u)
+                    if (j0 + u < a.k) a.dweights[t * a.k + j0 + u] = dot[u];
         }
-        if (threadIdx.x == 0 && t < a.T)
-#pragma unroll
-            for (int u = 0; u < kPairs; ++u)
-                if (j0 + u < a.k) a.dweights[t * a.k + j0 + u] = dot[u];
     }
 }
 
@@ -590,6 +596,11 @@ dim3 row_block(int64_t C) {
     unsigned x = 1;
     while (x < 256 && x < C) x *= 2;
     return dim3(x, 256 / x);
+}
+// a launch has fewer than 2^32 threads: blocks walk the tokens beyond
+dim3 row_grid(int64_t T, dim3 block) {
+    const int64_t n = ceil_div(T, block.y), most = 65536;
+    return dim3((unsigned)(n < most ? n : most));
 }
 
 }  // namespace
@@ -643,7 +654,7 @@ hipError_t launch_moe_route_grad(const float* dweights, const float* logits, con
 hipError_t launch_moe_dispatch(const void* X, const int32_t* positions, int64_t T, int32_t k, int64_t H, bool bf16,
                                void* rows, hipStream_t s) {
     RowArgs a{X, nullptr, positions, nullptr, rows, nullptr, T, H / 8, k};
-    const dim3 block = row_block(a.C), grid((unsigned)ceil_div(T, block.y));
+    const dim3 block = row_block(a.C), grid = row_grid(T, block);
     timing_mark("moe_dispatch_kernel", s);
     if (bf16) hipLaunchKernelGGL(moe_dispatch_kernel<true>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(moe_dispatch_kernel<false>, grid, block, 0, s, a);
@@ -654,7 +665,7 @@ hipError_t launch_moe_dispatch(const void* X, const int32_t* positions, int64_t 
 hipError_t launch_moe_combine(const void* rows, const int32_t* positions, const float* weights, int64_t T, int32_t k,
                               int64_t H, bool bf16, void* out, hipStream_t s) {
     RowArgs a{rows, nullptr, positions, weights, out, nullptr, T, H / 8, k};
-    const dim3 block = row_block(a.C), grid((unsigned)ceil_div(T, block.y));
+    const dim3 block = row_block(a.C), grid = row_grid(T, block);
     timing_mark("moe_combine_kernel", s);
     if (bf16) hipLaunchKernelGGL(moe_combine_kernel<true>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(moe_combine_kernel<false>, grid, block, 0, s, a);
@@ -666,7 +677,7 @@ hipError_t launch_moe_combine_grad(const void* dout, const void* rows, const int
                                    int64_t T, int32_t k, int64_t H, bool bf16, void* drows, float* dweights,
                                    hipStream_t s) {
     RowArgs a{dout, rows, positions, weights, drows, dweights, T, H / 8, k};
-    const dim3 block = row_block(a.C), grid((unsigned)ceil_div(T, block.y));
+    const dim3 block = row_block(a.C), grid = row_grid(T, block);
     timing_mark("moe_combine_grad_kernel", s);
     if (bf16) hipLaunchKernelGGL(moe_combine_grad_kernel<true>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(moe_combine_grad_kernel<false>, grid, block, 0, s, a);

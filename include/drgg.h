@@ -481,7 +481,7 @@ drgg_status drgg_tailsplit_units(int64_t tiles, int64_t workers, int64_t *out);
  *
  * T tokens with k experts each make R = T*k pairs, pair t*k + j being token t
  * and its j-th expert.  Limits: 1 <= E <= 1024, 1 <= k <= min(E, 64),
- * T*k < 2^31.
+ * T*k < 2^31, and T <= 2^27 for the selection.
  */
 
 /*

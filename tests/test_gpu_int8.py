@@ -282,6 +282,23 @@ def test_graph_and_stream(drgg):
         assert torch.equal(first, out)
 
 
+def test_long_buffers(drgg):
+    """Codes and results beyond 2^32 bytes: the last rows as in a small call."""
+    M, N, K = 300007, 4096, 16384
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    X = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    q, s = drgg.quantize_int8(X)
+    few = drgg.quantize_int8(X[-70:].contiguous())
+    assert torch.equal(q[-70:], few[0]) and torch.equal(s[-70:], few[1])
+    W = torch.randint(-127, 128, (2, N, K), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.rand((2, N), generator=g, device="cuda")
+    offsets = torch.tensor([0, 9, M], dtype=torch.int32, device="cuda")
+    y = drgg.grouped_gemm_int8(q, s, W, ws, offsets, out_dtype=torch.float32)
+    assert torch.equal(y[-70:], drgg.gemm_int8(q[-70:], s[-70:], W[1], ws[1], out_dtype=torch.float32))
+    assert torch.equal(y[:9], drgg.gemm_int8(q[:9], s[:9], W[0], ws[0], out_dtype=torch.float32))
+
+
 @pytest.mark.parametrize("T,H", [(16500, 131056)])
 def test_ffn_too_large_to_gather(drgg, T, H):
     """T * H beyond 2^31: the block copies its tokens into the grouped order

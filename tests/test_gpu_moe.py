@@ -288,6 +288,46 @@ def test_combine_grad(drgg, T, k, H, dtype):
     assert torch.equal(drows, again[0]) and torch.equal(dweights, again[1])
 
 
+def test_many_tokens_and_long_buffers(drgg):
+    """Rows beyond 2^31 values and 2^32 bytes, and more tokens than a launch has blocks: with weights 1/4 the sum of
+    four copies of a row is the row."""
+    T, k, H = 140001, 4, 4096
+    X = torch.randn((T, H), device="cuda", dtype=torch.bfloat16)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    positions = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32).view(T, k)
+    rows = drgg.moe_dispatch(X, positions)
+    assert torch.equal(rows[positions[-1].long()], X[-1:].expand(k, H))
+    w = torch.full((T, k), 0.25, device="cuda")
+    assert torch.equal(drgg.moe_combine(rows, positions, w), X)
+    drows, dweights = drgg.moe_combine_grad(X, rows, positions, w)
+    assert torch.equal(drows[positions[:, 3].long()], X * 0.25)
+    few = [0, 70000, T - 1]
+    want = X[few].double().square().sum(1, keepdim=True).expand(-1, k)
+    assert torch.all((dweights[few].double() - want).abs() <= H * U * want)
+
+
+def test_long_logits(drgg):
+    """Logits beyond 2^31 values: the last tokens are chosen as in a small call."""
+    T, E, k = 2200000, 1024, 2
+    logits = torch.randn((T, E), device="cuda")
+    r = drgg.moe_route(logits, k)
+    last = drgg.moe_route(logits[-50:], k)
+    assert torch.equal(r.experts[-50:], last.experts) and torch.equal(r.weights[-50:], last.weights)
+    counts = torch.bincount(r.experts.flatten(), minlength=E)
+    assert torch.equal(r.group_offsets[1:].long(), counts.cumsum(0)) and int(r.group_offsets[0]) == 0
+    at = r.positions.flatten().long()
+    assert torch.equal(torch.bincount(at, minlength=T * k), torch.ones_like(at))
+    assert torch.equal(r.tokens[at], torch.arange(T, device="cuda", dtype=torch.int32).repeat_interleave(k))
+    by_row = torch.empty_like(at)
+    by_row[at] = r.experts.flatten().long()
+    assert bool((by_row[1:] >= by_row[:-1]).all())
+    same = by_row[1:] == by_row[:-1]
+    assert bool((r.tokens[1:] > r.tokens[:-1])[same].all())
+    d = drgg.moe_route_grad(torch.ones_like(r.weights), logits, r.experts, r.weights)
+    assert float(d[-50:].abs().max()) <= 8 * U
+
+
 def test_masked_pairs_do_not_spread_nan(drgg):
     """An entry outside the rows is skipped: its row's NaN does not reach the sum, and nothing is written through it."""
     T, k, H = 6, 3, 48
