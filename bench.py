@@ -217,7 +217,7 @@ def cpu_model():
 
 
 PROFILE = os.path.join(ROOT, "profiles", "gg_kernels_moe_gate_up_e8_t131072_k2048_n1536.md")
-KERNEL_SRC = os.path.join(ROOT, "dense_ragged_grouped_amd", "csrc", "kernels.hip")
+KERNEL_SRCS = tuple(os.path.join(ROOT, "dense_ragged_grouped_amd", "csrc", f) for f in ("engine.hpp", "kernels.hip"))
 # library timing names -> kernel symbols in the rocprofv3 summary (the data
 # gradient runs on a transposed copy of W when it has a workspace, as here)
 PROFILE_KEYS = {"gg_fwd_kernel": "gg_fwd_dgrad_kernel<0,", "gg_dgrad_kernel": "gg_fwd_dgrad_kernel<2,",
@@ -225,12 +225,12 @@ PROFILE_KEYS = {"gg_fwd_kernel": "gg_fwd_dgrad_kernel<0,", "gg_dgrad_kernel": "g
                 "gg_wgrad_det_kernel": "gg_wgrad_det_kernel<", "gg_wgrad_fold_kernel": "gg_wgrad_fold_kernel<"}
 
 
-def kernel_source_digest(path=KERNEL_SRC):
-    """Digest of the kernel source with comments and whitespace removed: it
+def kernel_source_digest(paths=KERNEL_SRCS):
+    """Digest of the kernel sources with comments and whitespace removed: it
     changes when the code does, not when a comment does."""
     import hashlib
     import re
-    text = open(path).read()
+    text = "".join(open(path).read() for path in paths)
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     text = re.sub(r"//[^\n]*", "", text)
     text = re.sub(r"\s+", "", text)

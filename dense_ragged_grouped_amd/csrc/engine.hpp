@@ -907,84 +907,6 @@ __device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, voi
     }
 }
 
-// store_tile_lines for values that are made on the way: value(i, j, q) gives
-// the four of row block i at columns 32j + 8q + 4*(lane/32) .. +3 of the
-// wave's part, which starts at column rb and has NJ blocks of 32.  A
-// segment's values are made by all lanes before its rounds, in which only the
-// lanes that own a round's rows write (made inside the rounds they would cost
-// 32/R times the instructions).
-template <bool OUT_BF16, int R, class Mma, int NJ, class Value>
-__device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* scr, void* out, int64_t ld, int rows,
-                                                  int cols) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    constexpr int ES = OUT_BF16 ? 2 : 4;
-    constexpr int SEG = 128 / ES;   // columns per 128-byte segment
-    constexpr int BPS = SEG / 32;   // 32-column blocks per segment
-    static_assert(R == 8 || R == 16, "rounds of 8 or 16 rows");
-    static_assert(NJ % BPS == 0, "whole segments per wave");
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ra = Mma::wave_row(wave);
-    lds_t* sw = scr + wave * (R * 128);
-    const int r = lane & 31, h = lane >> 5;
-    const int rr = r % R;   // this lane's scratch row in the round that owns it
-    const int sx = rr & 7;
-#pragma unroll
-    for (int i = 0; i < Mma::kBI; ++i) {
-        const int r0 = ra + 32 * i;
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<char*>(out) + (int64_t)r0 * ld * ES);
-#pragma unroll
-        for (int g = 0; g < NJ / BPS; ++g) {
-            const int c0 = rb + g * SEG;
-            u32x2 half[OUT_BF16 ? BPS : 1][4];
-            u32x4 full[OUT_BF16 ? 1 : BPS][4];
-#pragma unroll
-            for (int b = 0; b < BPS; ++b)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4 a = value(i, g * BPS + b, q);
-                    if constexpr (OUT_BF16)
-                        half[b][q] = u32x2{
-                            __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a[0], a[1]}), bf16x2)),
-                            __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a[2], a[3]}), bf16x2))};
-                    else
-                        full[b][q] = __builtin_bit_cast(u32x4, a);
-                }
-#pragma unroll
-            for (int s = 0; s < 32 / R; ++s) {
-                if (r / R == s) {
-#pragma unroll
-                    for (int b = 0; b < BPS; ++b)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if constexpr (OUT_BF16)   // columns 32b + 8q + 4h .. +3: chunk 4b + q, its half h
-                                *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(
-                                    sw + rr * 128 + (((4 * b + q) ^ sx) << 4) + 8 * h) = half[b][q];
-                            else   // columns 8q + 4h .. +3: chunk 2q + h
-                                *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(
-                                    sw + rr * 128 + (((2 * q + h) ^ sx) << 4)) = full[b][q];
-                        }
-                }
-                wave_lds_sync();   // the round's rows are in the scratch
-#pragma unroll
-                for (int k = 0; k < R / 8; ++k) {
-                    const int idx = lane + 64 * k, row = idx >> 3, c = idx & 7;
-                    const u32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(
-                        sw + row * 128 + ((c ^ (row & 7)) << 4));
-                    const int rowb = s * R + row;            // row within the 32-row block
-                    const int col = c0 + c * (16 / ES);
-                    const uint32_t o = r0 + rowb < rows && col < cols ? (uint32_t)((rowb * ld + col) * ES) : kOOB;
-                    __builtin_amdgcn_raw_buffer_store_b128(v, rs, o, 0, kCpolNT);
-                }
-                wave_lds_sync();   // read back before the next round overwrites it
-            }
-        }
-    }
-}
-
 // Issue schedule of the stage loads of a 4-wave runner (steps t of the
 // global step sequence; the prologue acts as steps -4 .. -1).  A K-major operand loads stages t+3
 // and t+4 at odd steps (into the pair buffer whose two stages t-1 and t were

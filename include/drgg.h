@@ -346,7 +346,7 @@ drgg_status drgg_wgrad_chunking(int64_t T, int64_t chunk_max, int64_t *chunk_len
  *                         an 8-bit product then runs in that tile (1, 2, 4;
  *                         2 not for a gated BF16 result) whatever its rows
  *   DRGG_KNOB_GRID        force the workgroup count of the persistent kernels
- *                         (every program)
+ *                         (every BF16 program)
  *   DRGG_KNOB_REVERSE     1 = walk the work items in reverse order
  *   DRGG_KNOB_NONDET      1 = a non-deterministic weight gradient runs the
  *                         split program (atomic tile sums) instead of being
