@@ -29,8 +29,9 @@ def ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True):
     """The block on 8-bit weights (codes and scales as quantize_weights gives
     them): X [T, H] BF16 to [T, H] BF16.  Rows are quantised per token before
     each product; the activation between the products stays in FP32 until
-    then (rounded to BF16 first, a row's values would often take another
-    code: 1.2 % of the result's norm instead of 0.2 %)."""
+    then (rounded to BF16 first, values near the border of two codes would
+    take the other one, which moves the result by 0.75 % of its norm).  The
+    experts' outputs are rounded to BF16 before they are added in FP32."""
     return moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=renormalize)
 
 
