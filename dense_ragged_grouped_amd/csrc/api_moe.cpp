@@ -245,9 +245,15 @@ drgg_status moe_ffn_int8(const void* X, const float* logits, const int8_t* W1q, 
     st = current_cu_count(&cus);
     if (st != DRGG_OK) return st;
     const int64_t R = T * k;
+    // the selection's launch quantises the rows too, where they are gathered,
+    // fit it and are few: its workgroups of 1024 threads move rows more slowly
+    // (16384 tokens of 2048: 36 us against 6 + 26), which a launch less
+    // outweighs up to some thousand tokens (8 tokens: 5.3 us against 3.7 + 3.6)
+    const QuantArgs rows{X, nullptr, x, xs, T, H / 16, 1};
+    const bool together = L.gather && H <= kSelectQuantizeK && T * H <= kSelectQuantizeMost;
     hipError_t e = launch_moe_route(logits, T, E, k, renormalize != 0, experts, weights, offsets, positions,
-                                    L.gather ? tokens : nullptr, ws + L.table, stream);
-    if (e == hipSuccess)
+                                    L.gather ? tokens : nullptr, ws + L.table, stream, together ? &rows : nullptr);
+    if (e == hipSuccess && !together)
         e = launch_quantize_int8(X, true, T, H, L.gather ? nullptr : positions, L.gather ? 1 : k, x, xs, stream);
     if (e == hipSuccess)
         e = launch_int8(Int8Args{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E, L.gather ? tokens : nullptr, T},

@@ -12,6 +12,7 @@
 #include "engine.hpp"
 #include "internal.hpp"
 #include "plan.hpp"
+#include "quantize.hpp"
 
 namespace drgg {
 
@@ -33,107 +34,11 @@ __device__ __forceinline__ float gate(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }
 
-// ---------------------------------------------------------------------------
-// quantisation
-//
-// 16 values of a row per thread and step (16-byte code stores).  127 x is
-// exact for BF16 x, so that x = max|x| / 2 is a true tie (63.5, to 64); the
-// division is the correctly rounded one.  Rows whose largest value is beyond
-// 2^120 are scaled by 2^-8 first (exact), so that 127 x stays finite.  A row
-// that holds an infinity or NaN gets scale NaN and codes 0: every product
-// with it is NaN, and no other row's is.
-
-struct QuantArgs {
-    const void* X;
-    const int32_t* positions;   // null: row t stays row t
-    int8_t* q;
-    float* scale;
-    int64_t T, C;               // C: groups of 16 values per row
-    int32_t k;
-};
-
-template <bool BF16>
-__device__ __forceinline__ void load16(float (&f)[16], const void* X, int64_t i) {
-    if constexpr (BF16) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const u32x4 v = reinterpret_cast<const u32x4*>(X)[2 * i + h];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                f[8 * h + 2 * r] = __uint_as_float(v[r] << 16);
-                f[8 * h + 2 * r + 1] = __uint_as_float(v[r] & 0xFFFF0000u);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const f32x4 v = reinterpret_cast<const f32x4*>(X)[4 * i + h];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) f[4 * h + r] = v[r];
-        }
-    }
-}
-
-// HELD: a thread's values of the row (at most 16) stay in registers between
-// the maximum and the codes; longer rows are read again, from L2.  Bound by
-// memory: 504 MB for 131072 FP32 rows of 768 in 87 us (5.8 TB/s), 101 MB for
-// 16384 BF16 rows of 2048 in 26 us, 94 and 30 us when the row is read twice.
+// quantisation (quantize.hpp): blockDim.x threads along a row
 template <bool BF16, bool HELD>
 __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
     __shared__ uint32_t part[4];
-    const int64_t R = a.T * a.k;
-    // whole blocks of rows: every thread takes part in the maxima
-    for (int64_t t0 = (int64_t)blockIdx.x * blockDim.y; t0 < a.T; t0 += (int64_t)gridDim.x * blockDim.y) {
-        const int64_t t = t0 + threadIdx.y;
-        const bool live = t < a.T;
-        // the largest magnitude as bits: their unsigned order is the order of
-        // the magnitudes, with infinity and NaN above every finite value
-        uint32_t m = 0;
-        float f[16];
-        if (live)
-            for (int64_t c = threadIdx.x; c < a.C; c += blockDim.x) {
-                load16<BF16>(f, a.X, t * a.C + c);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-                if constexpr (HELD) break;
-            }
-        const int width = blockDim.x < 64 ? blockDim.x : 64;
-        for (int d = 1; d < width; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
-        if (blockDim.x > 64) {
-            const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-            __syncthreads();   // the last rows' maxima have been read
-            if ((tid & 63) == 0) part[tid >> 6] = m;
-            __syncthreads();
-            const int w0 = threadIdx.y * (blockDim.x / 64);
-            for (unsigned w = 0; w < blockDim.x / 64; ++w) m = max(m, part[w0 + w]);
-        }
-        const bool bad = m >= 0x7F800000u;
-        const float most = __uint_as_float(m);
-        const float scale = bad ? __uint_as_float(0x7FC00000u) : most / 127.f;
-        const float down = most > 0x1p120f ? 0x1p-8f : 1.f;
-        const float by = bad || m == 0 ? 1.f : most * down;
-        for (int64_t c = threadIdx.x; live && c < a.C; c += blockDim.x) {
-            if constexpr (!HELD) load16<BF16>(f, a.X, t * a.C + c);
-            u32x4 out;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t v = 0;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int q = bad ? 0 : (int)rintf(f[4 * h + r] * down * 127.f / by);
-                    v |= (uint32_t)(q & 0xFF) << (8 * r);
-                }
-                out[h] = v;
-            }
-            for (int j = 0; j < a.k; ++j) {
-                const int64_t p = a.positions ? a.positions[t * a.k + j] : t;
-                if (p < 0 || p >= R) continue;
-                reinterpret_cast<u32x4*>(a.q)[p * a.C + c] = out;
-                if (c == 0) a.scale[p] = scale;
-            }
-            if constexpr (HELD) break;
-        }
-    }
+    quantize_rows<BF16, HELD>(a, part, threadIdx.x, threadIdx.y, blockDim.x, blockDim.y, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -561,8 +466,7 @@ hipError_t launch_int8_tile(const Int8Args& a, bool gated, bool bf16, int64_t gr
 hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, const int32_t* positions, int32_t k,
                                 int8_t* q, float* scale, hipStream_t s) {
     QuantArgs a{X, positions, q, scale, T, K / 16, k};
-    unsigned x = 1;
-    while (x < 256 && x < a.C) x *= 2;
+    const unsigned x = quantize_threads(a.C);
     // a launch has fewer than 2^32 threads: blocks walk the rows beyond
     const dim3 block(x, 256 / x);
     const int64_t n = ceil_div(T, block.y), most = 65536;

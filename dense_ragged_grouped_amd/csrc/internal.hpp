@@ -88,10 +88,22 @@ hipError_t launch_hold_cus(int n, uint64_t ticks, hipStream_t s);
 
 // ---- the expert layer's operators (moe.hip, int8.hip) -----------------------
 
+// Arguments of the row quantisation (quantize.hpp): X [T, 16 C] to codes and scales.
+struct QuantArgs {
+    const void* X;
+    const int32_t* positions;   // null: row t stays row t
+    int8_t* q;
+    float* scale;
+    int64_t T, C;               // C: groups of 16 values per row
+    int32_t k;
+};
+// the longest BF16 rows, and the most values, that the selection's launch quantises too
+constexpr int64_t kSelectQuantizeK = 4096, kSelectQuantizeMost = int64_t(1) << 23;
+
 size_t route_table_bytes(int64_t T, int32_t E);   // the selection's workspace; 0 for one workgroup
 hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
                             float* weights, int32_t* offsets, int32_t* positions, int32_t* tokens, void* table,
-                            hipStream_t s);
+                            hipStream_t s, const QuantArgs* quantize = nullptr);
 hipError_t launch_moe_route_grad(const float* dweights, const float* logits, const int32_t* experts,
                                  const float* weights, int64_t T, int32_t E, int32_t k, int renormalize,
                                  float* dlogits, hipStream_t s);

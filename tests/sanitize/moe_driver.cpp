@@ -53,7 +53,8 @@ bool checks_offsets() { return false; }
 drgg_status check_offsets_sync(const int32_t*, int32_t, int64_t, hipStream_t) { return DRGG_OK; }
 size_t route_table_bytes(int64_t T, int32_t E) { return T > 64 ? (size_t)(T / 64 + 2) * (size_t)E * 4 : 0; }
 hipError_t launch_moe_route(const float*, int64_t T, int32_t E, int32_t k, int, int32_t* experts, float* weights,
-                            int32_t* offsets, int32_t* positions, int32_t* tokens, void* table, hipStream_t) {
+                            int32_t* offsets, int32_t* positions, int32_t* tokens, void* table, hipStream_t,
+                            const QuantArgs* quantize) {
     steps.push_back("route");
     const int64_t R = T * k;
     routed = {{experts, R * 4}, {weights, R * 4}, {offsets, (E + 1) * 4}, {positions, R * 4}};
@@ -63,6 +64,14 @@ hipError_t launch_moe_route(const float*, int64_t T, int32_t E, int32_t k, int, 
     for (size_t i = 0; i < routed.size(); ++i) {
         EXPECT(inside(routed[i]));
         for (size_t j = 0; j < i; ++j) EXPECT(routed[i].apart(routed[j]));
+    }
+    if (quantize) {
+        EXPECT(gathers && quantize->k == 1 && !quantize->positions && quantize->T == T);
+        codes = Span(quantize->q, T * quantize->C * 16);
+        scales = Span(quantize->scale, T * 4);
+        apart_from_routed(codes);
+        apart_from_routed(scales);
+        EXPECT(codes.apart(scales));
     }
     return hipSuccess;
 }
@@ -124,7 +133,7 @@ int main() {
     auto* b = reinterpret_cast<int8_t*>(A);
     const int64_t cases[][5] = {{1, 8, 2, 16, 16}, {63, 57, 7, 1776, 528}, {65, 1024, 64, 48, 16},
                                 {16384, 32, 8, 2048, 768}, {16500, 2, 1, 131056, 16}, {33, 4, 4, 16, 4096},
-                                {100000, 3, 3, 32768, 32}};
+                                {100000, 3, 3, 32768, 32}, {70, 8, 2, 4112, 48}, {70, 8, 2, 4096, 48}};
     for (const auto& c : cases) {
         size_t need = 0;
         EXPECT(moe_ffn_int8_workspace_size(c[0], (int32_t)c[1], (int32_t)c[2], c[3], c[4], &need) == DRGG_OK);
@@ -134,7 +143,8 @@ int main() {
         result = Span(nullptr, 0);
         EXPECT(moe_ffn_int8(A, f, b, f, b, f, c[0], (int32_t)c[1], (int32_t)c[2], c[3], c[4], 1, A,
                             const_cast<char*>(ws_lo), need, nullptr) == DRGG_OK);
-        EXPECT(steps.size() == 6);
+        const bool together = c[3] <= kSelectQuantizeK && c[0] * c[3] <= kSelectQuantizeMost;
+        EXPECT(steps.size() == (together ? 5 : 6));
         EXPECT(gathers == (c[0] * c[3] <= INT32_MAX - 4096));
         EXPECT(moe_ffn_int8(A, f, b, f, b, f, c[0], (int32_t)c[1], (int32_t)c[2], c[3], c[4], 1, A,
                             const_cast<char*>(ws_lo), need - 1, nullptr) == DRGG_EWORKSPACE);

@@ -353,7 +353,8 @@ def test_ffn_int8(drgg, T, E, k, H, I):
     assert err < 2.0 ** -8, err
 
 
-@pytest.mark.parametrize("T,E,k,H,I", [(0, 4, 2, 64, 32), (5, 8, 3, 96, 16), (700, 5, 2, 144, 272)])
+@pytest.mark.parametrize("T,E,k,H,I", [(0, 4, 2, 64, 32), (5, 8, 3, 96, 16), (700, 5, 2, 144, 272), (65, 1000, 20, 48, 16),
+                                       (3, 300, 8, 4096, 32), (129, 130, 1, 4112, 16), (33000, 3, 1, 16, 16)])
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_ffn_is_its_operators(drgg, T, E, k, H, I, renormalize):
     """The one call gives the same bits as the operators called one by one, also on a side stream, into a given
@@ -388,8 +389,9 @@ def test_ffn_is_its_operators(drgg, T, E, k, H, I, renormalize):
     if T:
         with pytest.raises(drgg.DrggError):
             drgg.moe_ffn_int8(*args, workspace=ws[:64])
-        with pytest.raises(ValueError):
-            drgg.moe_ffn_int8(X, logits, w1, s1, w2.transpose(1, 2).contiguous(), s2, k)
+        if H != I:   # else the transpose has the right shape
+            with pytest.raises(ValueError):
+                drgg.moe_ffn_int8(X, logits, w1, s1, w2.transpose(1, 2).contiguous(), s2, k)
         with pytest.raises(TypeError):
             drgg.moe_ffn_int8(X.float(), logits, w1, s1, w2, s2, k)
 
