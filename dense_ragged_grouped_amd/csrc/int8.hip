@@ -56,10 +56,13 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
 // idle; with more rows the tiles below move fewer bytes per product.
 //
 // Blocks of tokens are 16, 32 or 64 long by what is left of the group; U steps
-// are loaded before the first is used.  64 rows on 32 experts (1536x2048, 88 MB
-// of weights) take 17 us, 5.0 TB/s; one row through 4096x4096 6 us.  Rows and reduction positions outside
+// are loaded before the first is used.  Rows and reduction positions outside
 // the operands carry an out-of-range offset and read as zero.  launch_int8
 // says which NB, W and TOK run when.
+//
+// Bound by the weights' bytes on many experts (64 rows on 32 of 1536x2048, 88
+// MB: 17 us, 5.0 TB/s), by latency on one (one row through 4096x4096: 6 us).
+
 // The block of this workgroup among those of all groups (ntn column blocks
 // times ceil(T_e / TOK) token blocks each, token blocks innermost: their
 // weights are then read by one XCD), or false.  Every wave finds it by
