@@ -325,14 +325,15 @@ def workspace_size(op: int, E: int, M: int, N: int, K: int, out_dtype: int = BF1
 
 # ---- torch marshalling ---------------------------------------------------------
 
-_torch_module = None
+try:
+    import torch as _torch_module
+except ImportError:   # the host-only queries work without it
+    _torch_module = None
 
 
 def _torch():
-    global _torch_module
     if _torch_module is None:
-        import torch
-        _torch_module = torch
+        raise ImportError("this call needs torch")
     return _torch_module
 
 
@@ -351,8 +352,7 @@ def _torch_dtype(code: int):
 
 
 def _need(t, dtype, name, ndim):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch_module.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -735,14 +735,13 @@ def _call(name, stream, tensors, *args):
     current device, its current stream -- reads the stream's handle directly
     (torch's accessors, 0.1 us each; the Stream object and the device guard
     cost 3 us)."""
-    C = _torch()._C
     if stream is None and _RAW_STREAM:
-        index = C._cuda_getDevice()
+        index = _torch_module._C._cuda_getDevice()
         for t in tensors:
             if t is not None and t.get_device() != index:
                 break
         else:
-            st = getattr(lib, name)(*args, C._cuda_getCurrentRawStream(index))
+            st = getattr(lib, name)(*args, _torch_module._C._cuda_getCurrentRawStream(index))
             if st:
                 raise DrggError(st, name)
             return
@@ -751,10 +750,7 @@ def _call(name, stream, tensors, *args):
 
 
 def _raw_stream_accessors():
-    try:
-        C = _torch()._C
-    except ImportError:
-        return False
+    C = getattr(_torch_module, "_C", None)
     return hasattr(C, "_cuda_getCurrentRawStream") and hasattr(C, "_cuda_getDevice")
 
 
@@ -776,7 +772,7 @@ def _out(out, dtype, shape, like):
 
 def _row_code(t, name):
     """The dtype code of a contiguous 2-d row tensor, BF16 or FP32."""
-    torch = _torch()
+    torch = _torch_module
     if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor")
     _need(t, t.dtype, name, 2)
@@ -795,7 +791,7 @@ def moe_route(logits, k, renormalize=True, workspace=None, stream=None):
     with renormalize=False), and the stable grouping of the T*k pairs by
     expert, as a Routing.  A masked (-inf) logit gets weight 0, also when all
     of a token's are."""
-    torch = _torch()
+    torch = _torch_module
     _need(logits, torch.float32, "logits", 2)
     T, E = logits.shape
     k = int(k)
@@ -821,7 +817,7 @@ def moe_route(logits, k, renormalize=True, workspace=None, stream=None):
 def _scratch(like, nbytes, stream):
     """A workspace for one call, which needs no initialisation.  Allocated on
     the stream that uses it, so that its memory is handed out again in order."""
-    torch = _torch()
+    torch = _torch_module
     if stream is None:
         return like.new_empty((nbytes,), dtype=torch.uint8)
     with torch.cuda.stream(stream):
@@ -830,7 +826,7 @@ def _scratch(like, nbytes, stream):
 
 def moe_route_grad(dweights, logits, experts, weights, renormalize=True, out=None, stream=None):
     """dlogits [T, E] from the gradient of moe_route's weights."""
-    torch = _torch()
+    torch = _torch_module
     _need(logits, torch.float32, "logits", 2)
     T, E = logits.shape
     _need(experts, torch.int32, "experts", 2)
@@ -847,7 +843,7 @@ def moe_route_grad(dweights, logits, experts, weights, renormalize=True, out=Non
 def moe_dispatch(X, positions, out=None, stream=None):
     """Rows in the grouped order: out[positions[t, j]] = X[t] for X [T, H]
     (BF16 or FP32, H a multiple of 8); out [T*k, H]."""
-    torch = _torch()
+    torch = _torch_module
     code = _row_code(X, "X")
     T, H = X.shape
     _need(positions, torch.int32, "positions", 2)
@@ -861,7 +857,7 @@ def moe_dispatch(X, positions, out=None, stream=None):
 
 def _grouped_rows(rows, positions, weights):
     """(dtype code, T, k, H) of rows [T*k, H], positions and weights [T, k]."""
-    torch = _torch()
+    torch = _torch_module
     code = _row_code(rows, "rows")
     R, H = rows.shape
     _need(positions, torch.int32, "positions", 2)
@@ -899,7 +895,7 @@ def quantize_int8(X, positions=None, stream=None):
     """Codes and scales of the rows of X [T, K] (BF16 or FP32, K a multiple of
     16): (q int8 [T, K], scale FP32 [T]).  With positions [T, k] each token's
     codes go to its k rows of the grouped order: q [T*k, K], scale [T*k]."""
-    torch = _torch()
+    torch = _torch_module
     code = _row_code(X, "X")
     T, K = X.shape
     k, at = 1, None
@@ -914,7 +910,7 @@ def quantize_int8(X, positions=None, stream=None):
 
 
 def _int8_operands(Xq, x_scale, Wq, w_scale, wdim, M, gated, out_dtype, out):
-    torch = _torch()
+    torch = _torch_module
     _need(Xq, torch.int8, "Xq", 2)
     _need(Wq, torch.int8, "Wq", wdim)
     _need(x_scale, torch.float32, "x_scale", 1)
@@ -937,7 +933,7 @@ def grouped_gemm_int8(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, rows
     the N = 2I columns are gate and up halves, and Y [M, I] = silu(gate) * up.
     rows (int32 [M], moe_route's tokens): row t of the product is row rows[t]
     of Xq [T, K] and x_scale [T], T*K < 2^31 - 4096."""
-    torch = _torch()
+    torch = _torch_module
     E = _offsets(group_offsets)
     M = at = None
     if rows is not None:
@@ -967,7 +963,7 @@ def moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True, o
     with W2q [E, H, I] (BF16) and moe_combine: [T, H] BF16.  `workspace`: a
     device tensor of at least ffn_workspace_size bytes, or None for one
     allocated for this call."""
-    torch = _torch()
+    torch = _torch_module
     _need(X, torch.bfloat16, "X", 2)
     T, H = X.shape
     _need(logits, torch.float32, "logits", 2)
