@@ -488,29 +488,42 @@ hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, 
 
 // Which program runs, from the sizes alone (forced_tile: the test knob; a tile
 // this product has, or none).  M rows in E groups of unknown
-// sizes make about M/64 + E/2 blocks of 64 tokens.
+// sizes make about M/64 + E/2 blocks of 64 tokens, and up to 48 rows a group
+// about one for each.
 hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s) {
     const bool may128 = !(gated && bf16);
     int tile = forced_tile;
     if (tile != kTile256x256 && tile != kTile128x256 && !(tile == kTile128x128 && may128)) tile = kTileAuto;
     // a launch has fewer than 2^32 threads (the tiles walk theirs)
     const bool rows = tile == kTileAuto && (a.M / 32 + a.E) * ceil_div(a.N, 16) < int64_t(1) << 22;
-    const int64_t cols = ceil_div(a.N, 64), blocks = cols * (ceil_div(a.M, 64) + (a.E - 1) / 2);
+    const int64_t cols = ceil_div(a.N, 64), full = a.M < a.E ? a.M : a.E;
+    const int64_t blocks = cols * (a.M <= 48 * (int64_t)a.E ? full : ceil_div(a.M, 64) + a.E / 2);
     if (rows && cols * a.E >= 2 * kRuleCUs && a.M <= 24 * (int64_t)a.E) {
         // many experts' weights, few rows of each: read at memory speed (E = 32,
         // 1536x2048: 256 rows 20 us, 512 rows 23, 768 rows 30; in 128x256 tiles
         // 27, 28 and 29; 57 x 1000x1008, 1368 rows: 15 against 19)
         return gated ? launch_int8_rows<true, 4, 4, 32>(a, bf16, s) : launch_int8_rows<false, 4, 4, 32>(a, bf16, s);
     }
-    if (rows && blocks <= 2 * kRuleCUs) {
-        // at most two blocks per CU: the largest blocks that leave none idle
-        // (4096x4096, one group: 1 row 8 us, 128 rows 16, 256 rows 20, 512
-        // rows 34; in 128x256 tiles 31 to 33)
-        if (blocks >= kRuleCUs)
+    if (rows && blocks <= kRuleCUs) {
+        // one block per CU at most: the smallest blocks for which that holds
+        // (one group of 4096x4096: 128 rows in blocks of 32 columns 16 us, of 64
+        // 20; 192 rows 26 and 20, since the smaller ones need a second round;
+        // 256 rows 20, in 128x128 tiles 25)
+        if (2 * blocks > kRuleCUs)
             return gated ? launch_int8_rows<true, 4, 8, 64>(a, bf16, s) : launch_int8_rows<false, 4, 8, 64>(a, bf16, s);
         if (gated) return launch_int8_rows<true, 2, 8, 64>(a, bf16, s);
-        return 2 * blocks >= kRuleCUs ? launch_int8_rows<false, 2, 8, 64>(a, bf16, s)
-                                      : launch_int8_rows<false, 1, 8, 64>(a, bf16, s);
+        return 4 * blocks > kRuleCUs ? launch_int8_rows<false, 2, 8, 64>(a, bf16, s)
+                                     : launch_int8_rows<false, 1, 8, 64>(a, bf16, s);
+    }
+    if (rows && blocks <= 2 * kRuleCUs && (a.M <= 48 * (int64_t)a.E || a.K % 128 != 0)) {
+        // two blocks per CU at most, of four waves: with about one for each
+        // group's columns (48 rows of each of 32 experts: 928x1504 14.3 us,
+        // 1024x2048 19.3, 768x768 11.1; in 128x128 tiles 18.1, 20.4, 12.1; 64
+        // rows of each, 1024x2048: 27 and 21), and where K is no multiple of 128,
+        // with which these blocks gain and tiles lose (E = 5, 955 rows, 1472
+        // columns: K = 2304 22.0 us, 2368 17.0, 2432 22.7; in 128x128 tiles 17.3,
+        // 19.7, 18.6)
+        return gated ? launch_int8_rows<true, 4, 4, 64>(a, bf16, s) : launch_int8_rows<false, 4, 4, 64>(a, bf16, s);
     }
     const int64_t cols_out = gated ? a.N / 2 : a.N, bc = gated ? 128 : 256;
     if (tile == kTileAuto)

@@ -497,12 +497,18 @@ inline int default_tile(int op, int64_t E, int64_t M, int64_t N, int64_t K, bool
 // tiles, one per CU (of 128x128 two), takes about a + b * K/64 microseconds,
 // fitted on MI355X (K from 750 to 4096):
 //   256x256  6.7 + 0.83 K/64    128x256  4.9 + 0.525 K/64    128x128  6.4 + 0.53 K/64
+// and 128x128 tiles that have a CU each to themselves 5.0 + 0.3 K/64 (E = 4,
+// 1024x2048x4096: 26 us, 128x256 32; E = 1, 400x8192x2048: 17, 21).
 // Two 128x128 tiles do the work of one of 128x256 in finer pieces, so that a
 // last round costs only about its share.  The smaller tiles move more bytes
 // per product and are taken where they promise 15 % (E = 1, 6559x2552x976 in
 // FP32: 128x128 48 us, 128x256 55, 256x256 59; E = 57, gated, 21000x544x816:
 // 29, 41, 39; E = 32, 8192x1536x2048: 128x256 53, 256x256 65; without the
-// margin E = 57, 23215x1560x2864 took 128x256: 238 against 205).
+// margin E = 57, 23215x1560x2864 took 128x256: 238 against 205).  Up to 96
+// rows a group on average, most groups are one row tile of either height 128
+// and the smaller ones only read the few rows again: they are never slower
+// (E = 24, 64 rows each, 1536x4096: 46 us, 128x256 52; E = 64, 2048x2048: 59,
+// 64; but at 128 rows each E = 40, 1536x2000: 64, 256x256 44).
 inline int int8_tile(int64_t E, int64_t M, int64_t K, int64_t nc256, int64_t nc128, bool may128) {
     const double s = (double)K / 64;
     auto tiles = [&](int64_t bm, int64_t nc) {
@@ -512,9 +518,9 @@ inline int int8_tile(int64_t E, int64_t M, int64_t K, int64_t nc256, int64_t nc1
     const double c256 = (double)ceil_div(tiles(256, nc256), kRuleCUs) * (6.7 + 0.83 * s);
     const double c128x256 = (double)ceil_div(tiles(128, nc256), kRuleCUs) * (4.9 + 0.525 * s);
     const double r = (double)tiles(128, nc128) / (2 * kRuleCUs);
-    const double c128 = (r > 1 ? r + 0.15 : 1.0) * (6.4 + 0.53 * s);
+    const double c128 = r <= 0.5 ? 5.0 + 0.3 * s : (r > 1 ? r + 0.15 : 1.0) * (6.4 + 0.53 * s);
     const double best = c256 < 1.15 * c128x256 ? c256 : 1.15 * c128x256;
-    if (may128 && 1.15 * c128 < best) return kTile128x128;
+    if (may128 && (M <= 96 * E || 1.15 * c128 < best)) return kTile128x128;
     return best == c256 ? kTile256x256 : kTile128x256;
 }
 
