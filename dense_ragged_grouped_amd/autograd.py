@@ -57,6 +57,31 @@ def saved(ctx):
     return tuple(unpack(h) for h in handles)
 
 
+_TWICE = ("the package's gradients are computed in kernels that autograd cannot differentiate: "
+          "no second derivative passes through this operation")
+
+
+class _Gradient(torch.autograd.Function):
+    """fn(*tensors), a gradient, whose own derivative raises."""
+
+    @staticmethod
+    def forward(ctx, fn, *tensors):
+        return fn(*tensors)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(_TWICE)
+
+
+def gradient(fn, *tensors):
+    """fn(*tensors) for a backward pass, `tensors` all that the gradient depends
+    on.  Under create_graph the result stays connected to them, so that a second
+    derivative raises instead of being without this part.  (once_differentiable
+    would not do: it leaves the result unconnected where the incoming gradient
+    is a constant, and connects it to no input.)"""
+    return _Gradient.apply(fn, *tensors) if torch.is_grad_enabled() else fn(*tensors)
+
+
 class GroupedLinearFunction(torch.autograd.Function):
     """Y = grouped_gemm_fwd(X, W, offsets); backward: dX = grouped_gemm_dgrad(G,
     W, offsets), dW = grouped_gemm_wgrad(X, G, offsets) in W's dtype, the
@@ -71,13 +96,16 @@ class GroupedLinearFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, G):
+        if ctx.packed is not None and torch.is_grad_enabled():   # what the hooks give back has no graph
+            raise RuntimeError(_TWICE + " (create_graph on tensors saved through hooks or a checkpoint)")
         X, W, offs = saved(ctx)
         G = G.contiguous()
         dX = dW = None
         if ctx.needs_input_grad[0]:
-            dX = grouped_gemm_dgrad(G, W, offs, out_dtype=X.dtype)
+            dX = gradient(lambda G, W: grouped_gemm_dgrad(G, W, offs, out_dtype=X.dtype), G, W)
         if ctx.needs_input_grad[1]:
-            dW = grouped_gemm_wgrad(X, G, offs, out_dtype=W.dtype, deterministic=ctx.deterministic)
+            dW = gradient(lambda X, G: grouped_gemm_wgrad(X, G, offs, out_dtype=W.dtype, deterministic=ctx.deterministic),
+                          X, G)
         return dX, dW, None, None
 
 

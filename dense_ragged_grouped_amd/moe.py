@@ -8,13 +8,14 @@ results are added with the router's weights.
                and both weights
 
 Weights are stacked per expert, W1 [E, 2I, H] (gate rows, then up rows) and
-W2 [E, H, I].
+W2 [E, H, I].  Derivatives are of first order: a second one through these
+operators raises.
 """
 import torch
 
 from . import (Routing, moe_combine, moe_combine_grad, moe_dispatch, moe_ffn_int8, moe_route, moe_route_grad,
                quantize_int8)
-from .autograd import grouped_linear
+from .autograd import gradient, grouped_linear
 
 
 def quantize_weights(W):
@@ -47,7 +48,8 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def backward(ctx, _experts, dweights, _offsets, _positions, _tokens):
         logits, experts, weights = ctx.saved_tensors
-        return moe_route_grad(dweights.contiguous(), logits, experts, weights, renormalize=ctx.renormalize), None, None
+        return gradient(lambda *a: moe_route_grad(*a, renormalize=ctx.renormalize), dweights.contiguous(), logits, experts,
+                        weights), None, None
 
 
 class _Dispatch(torch.autograd.Function):
@@ -58,7 +60,7 @@ class _Dispatch(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
-        return moe_combine(dout.contiguous(), *ctx.saved_tensors), None
+        return gradient(moe_combine, dout.contiguous(), *ctx.saved_tensors), None
 
 
 class _Combine(torch.autograd.Function):
@@ -69,7 +71,7 @@ class _Combine(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
-        drows, dweights = moe_combine_grad(dout.contiguous(), *ctx.saved_tensors)
+        drows, dweights = gradient(moe_combine_grad, dout.contiguous(), *ctx.saved_tensors)
         return drows, None, dweights
 
 
