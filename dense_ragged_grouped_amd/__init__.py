@@ -381,6 +381,21 @@ def _on_one_device(stream, *tensors):
     return torch.cuda.device(dev)
 
 
+def _new(shape, dtype, like, stream):
+    """A result of a call on `stream`, on the device of `like`.  Allocated on
+    the stream that writes it: memory that is free on the caller's stream may
+    still be in use there.  Recorded on the caller's stream, which will read
+    it: dropped, it is not handed out again before that has happened."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    torch = _torch()
+    caller = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(caller)
+    return t
+
+
 class Workspace:
     """Device workspace for the weight gradient, grown on demand.
 
@@ -464,7 +479,7 @@ def grouped_gemm_fwd(X, W, group_offsets, out_dtype=None, deterministic=True, ou
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, E={E}")
     code = _dtype_code(out_dtype if out_dtype is not None else torch.bfloat16)
     if out is None:
-        out = torch.empty((M, N), dtype=_torch_dtype(code), device=X.device)
+        out = _new((M, N), _torch_dtype(code), X, stream)
     else:
         _need(out, _torch_dtype(code), "out", 2)
         if tuple(out.shape) != (M, N):
@@ -493,7 +508,7 @@ def grouped_gemm_dgrad(G, W, group_offsets, out_dtype=None, deterministic=True, 
         raise ValueError(f"shape mismatch: G {tuple(G.shape)}, W {tuple(W.shape)}, E={E}")
     code = _dtype_code(out_dtype if out_dtype is not None else torch.bfloat16)
     if out is None:
-        out = torch.empty((M, K), dtype=_torch_dtype(code), device=G.device)
+        out = _new((M, K), _torch_dtype(code), G, stream)
     else:
         _need(out, _torch_dtype(code), "out", 2)
         if tuple(out.shape) != (M, K):
@@ -521,7 +536,7 @@ def grouped_gemm_wgrad(X, G, group_offsets, out_dtype=None, deterministic=True, 
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, G {tuple(G.shape)}")
     code = _dtype_code(out_dtype if out_dtype is not None else torch.bfloat16)
     if out is None:
-        out = torch.empty((E, N, K), dtype=_torch_dtype(code), device=X.device)
+        out = _new((E, N, K), _torch_dtype(code), X, stream)
     else:
         _need(out, _torch_dtype(code), "out", 3)
         if tuple(out.shape) != (E, N, K):
@@ -576,10 +591,9 @@ def _need_rows(t, name, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _out_rows(out, shape, code, device, name="out"):
-    torch = _torch()
+def _out_rows(out, shape, code, like, stream, name="out"):
     if out is None:
-        return torch.empty(shape, dtype=_torch_dtype(code), device=device)
+        return _new(shape, _torch_dtype(code), like, stream)
     if out.dtype != _torch_dtype(code):
         raise TypeError(f"{name} must be {_torch_dtype(code)}")
     _need_rows(out, name, shape)
@@ -601,7 +615,7 @@ def batched_gemm_fwd(X, W, out_dtype=None, out=None, stream=None):
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
     N = W.shape[1]
     code = _dtype_code(out_dtype if out_dtype is not None else torch.bfloat16)
-    out = _out_rows(out, (B, T, N), code, X.device)
+    out = _out_rows(out, (B, T, N), code, X, stream)
     b = Batched(B, T, N, K, X.stride(1), X.stride(0), 0, 0, out.stride(1), out.stride(0))
     with _on_one_device(stream, X, W, out):
         st = lib.batched_gemm_fwd(X.data_ptr(), W.data_ptr(), ctypes.byref(b), code, out.data_ptr(),
@@ -623,7 +637,7 @@ def batched_gemm_dgrad(G, W, out_dtype=None, out=None, workspace=None, stream=No
         raise ValueError(f"shape mismatch: G {tuple(G.shape)}, W {tuple(W.shape)}")
     K = W.shape[2]
     code = _dtype_code(out_dtype if out_dtype is not None else torch.bfloat16)
-    out = _out_rows(out, (B, T, K), code, G.device)
+    out = _out_rows(out, (B, T, K), code, G, stream)
     nbytes = workspace_size(OP_DGRAD, B, B * T, N, K, code, True)
     b = Batched(B, T, N, K, G.stride(1), G.stride(0), 0, 0, out.stride(1), out.stride(0))
     with _on_one_device(stream, G, W, out):
@@ -649,7 +663,7 @@ def batched_gemm_wgrad(X, G, out_dtype=None, deterministic=True, out=None, works
     N = G.shape[2]
     code = _dtype_code(out_dtype if out_dtype is not None else torch.bfloat16)
     if out is None:
-        out = torch.empty((B, N, K), dtype=_torch_dtype(code), device=X.device)
+        out = _new((B, N, K), _torch_dtype(code), X, stream)
     else:
         _need(out, _torch_dtype(code), "out", 3)
         if tuple(out.shape) != (B, N, K):
@@ -693,7 +707,7 @@ def router_gemm_fp32_bf16x3(X, Wr, out=None, stream=None, workspace=None):
     if Kw != K:
         raise ValueError("shape mismatch")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=X.device)
+        out = _new((M, N), torch.float32, X, stream)
     else:
         _need(out, torch.float32, "out", 2)
         if tuple(out.shape) != (M, N):
@@ -763,9 +777,9 @@ def _need_shape(t, dtype, shape, name):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
 
 
-def _out(out, dtype, shape, like):
+def _out(out, dtype, shape, like, stream):
     if out is None:
-        return like.new_empty(shape, dtype=dtype)
+        return _new(shape, dtype, like, stream)
     _need_shape(out, dtype, shape, "out")
     return out
 
@@ -797,9 +811,9 @@ def moe_route(logits, k, renormalize=True, workspace=None, stream=None):
     k = int(k)
     nbytes = route_workspace_size(T, E, k)
     R = T * k
-    weights = logits.new_empty((T, k))
+    weights = _new((T, k), torch.float32, logits, stream)
     # one allocation for the integers (four would cost three times as much)
-    ints = logits.new_empty((3 * R + E + 1,), dtype=torch.int32)
+    ints = _new((3 * R + E + 1,), torch.int32, logits, stream)
     experts, positions = ints.as_strided((T, k), (k, 1)), ints.as_strided((T, k), (k, 1), R)
     tokens, offsets = ints.as_strided((R,), (1,), 2 * R), ints.as_strided((E + 1,), (1,), 3 * R)
     ws_ptr, ws_bytes = None, 0
@@ -834,7 +848,7 @@ def moe_route_grad(dweights, logits, experts, weights, renormalize=True, out=Non
     _need_shape(experts, torch.int32, (T, k), "experts")
     _need_shape(weights, torch.float32, (T, k), "weights")
     _need_shape(dweights, torch.float32, (T, k), "dweights")
-    out = _out(out, torch.float32, (T, E), logits)
+    out = _out(out, torch.float32, (T, E), logits, stream)
     _call("moe_route_grad", stream, (logits, dweights, experts, weights, out), dweights.data_ptr(), logits.data_ptr(),
           experts.data_ptr(), weights.data_ptr(), T, E, k, 1 if renormalize else 0, out.data_ptr())
     return out
@@ -849,7 +863,7 @@ def moe_dispatch(X, positions, out=None, stream=None):
     _need(positions, torch.int32, "positions", 2)
     k = positions.shape[1]
     _need_shape(positions, torch.int32, (T, k), "positions")
-    out = _out(out, X.dtype, (T * k, H), X)
+    out = _out(out, X.dtype, (T * k, H), X, stream)
     _call("moe_dispatch", stream, (X, positions, out), X.data_ptr(), positions.data_ptr(), T, k, H, code,
           out.data_ptr())
     return out
@@ -874,7 +888,7 @@ def moe_combine(rows, positions, weights=None, out=None, stream=None):
     rows[positions[t, j]] (FP32 sum, one rounding to the rows' dtype).  Without
     weights this is the gradient of moe_dispatch."""
     code, T, k, H = _grouped_rows(rows, positions, weights)
-    out = _out(out, rows.dtype, (T, H), rows)
+    out = _out(out, rows.dtype, (T, H), rows, stream)
     _call("moe_combine", stream, (rows, positions, weights, out), rows.data_ptr(), positions.data_ptr(),
           weights.data_ptr() if weights is not None else None, T, k, H, code, out.data_ptr())
     return out
@@ -885,7 +899,7 @@ def moe_combine_grad(dout, rows, positions, weights, stream=None):
     dtype, dweights [T, k] FP32)."""
     code, T, k, H = _grouped_rows(rows, positions, weights)
     _need_shape(dout, rows.dtype, (T, H), "dout")
-    drows, dweights = rows.new_empty(rows.shape), weights.new_empty((T, k))
+    drows, dweights = _new(rows.shape, rows.dtype, rows, stream), _new((T, k), weights.dtype, rows, stream)
     _call("moe_combine_grad", stream, (dout, rows, positions, weights), dout.data_ptr(), rows.data_ptr(),
           positions.data_ptr(), weights.data_ptr(), T, k, H, code, drows.data_ptr(), dweights.data_ptr())
     return drows, dweights
@@ -903,13 +917,13 @@ def quantize_int8(X, positions=None, stream=None):
         _need(positions, torch.int32, "positions", 2)
         k, at = positions.shape[1], positions.data_ptr()
         _need_shape(positions, torch.int32, (T, k), "positions")
-    q = X.new_empty((T * k, K), dtype=torch.int8)
-    scale = X.new_empty((T * k,), dtype=torch.float32)
+    q = _new((T * k, K), torch.int8, X, stream)
+    scale = _new((T * k,), torch.float32, X, stream)
     _call("quantize_int8", stream, (X, positions), X.data_ptr(), code, T, K, at, k, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
-def _int8_operands(Xq, x_scale, Wq, w_scale, wdim, M, gated, out_dtype, out):
+def _int8_operands(Xq, x_scale, Wq, w_scale, wdim, M, gated, out_dtype, out, stream):
     torch = _torch_module
     _need(Xq, torch.int8, "Xq", 2)
     _need(Wq, torch.int8, "Wq", wdim)
@@ -921,7 +935,7 @@ def _int8_operands(Xq, x_scale, Wq, w_scale, wdim, M, gated, out_dtype, out):
         raise ValueError(f"shape mismatch: Xq {tuple(Xq.shape)}, x_scale {tuple(x_scale.shape)}, "
                          f"Wq {tuple(Wq.shape)}, w_scale {tuple(w_scale.shape)}")
     code = BF16 if out_dtype is None else _dtype_code(out_dtype)
-    out = _out(out, _torch_dtype(code), (T if M is None else M, N // 2 if gated else N), Xq)
+    out = _out(out, _torch_dtype(code), (T if M is None else M, N // 2 if gated else N), Xq, stream)
     return T, N, K, code, out
 
 
@@ -939,7 +953,7 @@ def grouped_gemm_int8(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, rows
     if rows is not None:
         _need(rows, torch.int32, "rows", 1)
         M, at = rows.numel(), rows.data_ptr()
-    T, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 3, M, gated, out_dtype, out)
+    T, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 3, M, gated, out_dtype, out, stream)
     if Wq.shape[0] != E:
         raise ValueError(f"shape mismatch: Wq {tuple(Wq.shape)}, E={E}")
     _call("grouped_gemm_int8", stream, (Xq, x_scale, Wq, w_scale, group_offsets, rows, out), Xq.data_ptr(),
@@ -950,7 +964,7 @@ def grouped_gemm_int8(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, rows
 
 def gemm_int8(Xq, x_scale, Wq, w_scale, gated=False, out_dtype=None, out=None, stream=None):
     """The one-group case of grouped_gemm_int8: Wq [N, K], w_scale [N]."""
-    M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 2, None, gated, out_dtype, out)
+    M, N, K, code, out = _int8_operands(Xq, x_scale, Wq, w_scale, 2, None, gated, out_dtype, out, stream)
     _call("gemm_int8", stream, (Xq, x_scale, Wq, w_scale, out), Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(),
           w_scale.data_ptr(), M, N, K, 1 if gated else 0, code, out.data_ptr())
     return out
@@ -976,7 +990,7 @@ def moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True, o
     _need_shape(w1_scale, torch.float32, (E, N), "w1_scale")
     _need_shape(W2q, torch.int8, (E, H, I), "W2q")
     _need_shape(w2_scale, torch.float32, (E, H), "w2_scale")
-    out = _out(out, torch.bfloat16, (T, H), X)
+    out = _out(out, torch.bfloat16, (T, H), X, stream)
     if workspace is None:
         workspace = _scratch(X, ffn_workspace_size(T, E, k, H, I), stream)
     _call("moe_ffn_int8", stream, (X, logits, W1q, w1_scale, W2q, w2_scale, out, workspace), X.data_ptr(),
