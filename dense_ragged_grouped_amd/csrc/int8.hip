@@ -353,7 +353,7 @@ __global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
     constexpr int NJ = GATED ? Mma::kBJ / 2 : Mma::kBJ; // blocks of 32 of them per wave
     const int64_t NO = GATED ? a.N / 2 : a.N, K2 = a.K / 2;
     const int32_t ntn = (int32_t)((NO + BC - 1) / BC);
-    build_schedule(sch, a.offs, a.E, a.M, a.M, [=](int, int32_t T) { return ((T + BM - 1) / BM) * ntn; });
+    build_schedule(sch, a.offs, a.E, a.M, a.M, [=](int, int32_t T) { return ceil_div32(T, BM) * ntn; });
     const int64_t total = uni(sch.prefix[a.E]);
     const int64_t G = gridDim.x;
     int64_t w = xcd_remap(blockIdx.x, G);

@@ -224,7 +224,7 @@ __global__ __launch_bounds__(64 * WAVES) void gg_fwd_dgrad_kernel(GemmArgs a) {
     const int64_t ncols = OP == 0 ? a.N : a.K;
     const int32_t ntn = (int32_t)((ncols + BN - 1) / BN);
     build_schedule(sch, a.offs, a.E, a.M, a.T,
-                   [=](int, int32_t T) { return ((T + BM - 1) / BM) * ntn; });
+                   [=](int, int32_t T) { return ceil_div32(T, BM) * ntn; });
     const int64_t total = uni(sch.prefix[a.E]);
     const int64_t G = gridDim.x;
     int64_t w = xcd_remap(blockIdx.x, G);
@@ -583,7 +583,7 @@ __device__ __forceinline__ int32_t unit_chunk_len(int32_t T, int64_t chunk_max) 
 }
 __device__ __forceinline__ int32_t unit_chunks(int32_t T, int64_t chunk_max) {
     const int32_t l = unit_chunk_len(T, chunk_max);
-    return l ? (T + l - 1) / l : 0;
+    return l ? ceil_div32(T, l) : 0;
 }
 
 // Test aid (DRGG_KNOB_DELAY_SEED): a bounded sleep, a different length for
@@ -819,7 +819,7 @@ __global__ __launch_bounds__(kGemmThreads) void gg_wgrad_atomic_kernel(GemmArgs 
         const int32_t oe = uni(sch.offs[e]), oe1 = uni(sch.offs[e + 1]);
         const int32_t T = oe1 - oe;
         const int32_t clen = unit_chunk_len(T, cmax);
-        const int32_t nch = (T + clen - 1) / clen;
+        const int32_t nch = ceil_div32(T, clen);
         const int32_t local = (int32_t)w - uni(sch.prefix[pos]);
         int32_t tile, chunk = 0;
         bool whole;

@@ -62,6 +62,10 @@ inline TileShape tile_shape(int id) {
 }
 
 DRGG_HD inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// ceil(t / n) in 32 bits for counts below 2^31: t + n - 1 may need the 32nd bit
+DRGG_HD inline int32_t ceil_div32(int32_t t, int32_t n) {
+    return (int32_t)(((uint32_t)t + (uint32_t)n - 1) / (uint32_t)n);
+}
 DRGG_HD inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 // Chunk rule part 2 (host mirror of the device function): an expert with T
