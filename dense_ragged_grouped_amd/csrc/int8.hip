@@ -343,8 +343,12 @@ __device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* sc
 // zeros, so a part of it is the clock under load, the rest the loads' path as
 // in BF16) and about 6.7 us its epilogue and switch: without the global stores
 // the call takes 384 us, without the epilogue 355.
+//
+// 128x128 tiles share a CU in pairs, so their four waves get at most 256 of a
+// SIMD's 512 registers per lane (unbounded, the gathered FP32 variants took 260
+// and had a CU each: E = 57, gated, 20976x544x816 gathered 43.8 instead of 31.2 us).
 template <int BM, int BN, bool OUT_BF16, bool GATED, bool GATHERED, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void int8_tile_kernel(Int8Args a) {
+__global__ __launch_bounds__(64 * WAVES, BM == 128 && BN == 128 ? 2 : 1) void int8_tile_kernel(Int8Args a) {
     DRGG_STAGES(BM, BN, true, true, stg);
     __shared__ SchedOf<16> sch;
     __shared__ __attribute__((aligned(16))) char ep[WAVES * ep_rows(BM, BN) * 128];
