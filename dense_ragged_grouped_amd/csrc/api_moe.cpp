@@ -14,6 +14,8 @@ namespace drgg {
 namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// rows of E logits are read and written four at a time where all of them start aligned
+bool aligned_logits(const void* p, int32_t E) { return E % 4 ? aligned4(p) : aligned16(p); }
 
 drgg_status check_pairs(int64_t T, int32_t k) {
     int64_t r;
@@ -124,7 +126,7 @@ drgg_status moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int 
     drgg_status st = check_route(T, E, k);
     if (st != DRGG_OK) return st;
     if (!group_offsets || (T > 0 && (!logits || !experts || !weights || !positions))) return DRGG_EINVAL;
-    if (!aligned16(logits) || !aligned4(experts) || !aligned4(weights) || !aligned4(group_offsets) ||
+    if (!aligned_logits(logits, E) || !aligned4(experts) || !aligned4(weights) || !aligned4(group_offsets) ||
         !aligned4(positions) || !aligned4(tokens))
         return DRGG_EALIGN;
     const size_t need = route_table_bytes(T, E);
@@ -141,7 +143,7 @@ drgg_status moe_route_grad(const float* dweights, const float* logits, const int
     drgg_status st = check_route(T, E, k);
     if (st != DRGG_OK) return st;
     if (T > 0 && (!dweights || !logits || !experts || !weights || !dlogits)) return DRGG_EINVAL;
-    if (!aligned16(logits) || !aligned16(dlogits) || !aligned4(dweights) || !aligned4(experts) || !aligned4(weights))
+    if (!aligned_logits(logits, E) || !aligned_logits(dlogits, E) || !aligned4(dweights) || !aligned4(experts) || !aligned4(weights))
         return DRGG_EALIGN;
     if (T == 0) return DRGG_OK;
     return launch_status(
@@ -225,7 +227,7 @@ drgg_status moe_ffn_int8(const void* X, const float* logits, const int8_t* W1q, 
     drgg_status st = ffn_layout(T, E, k, H, I, &L);
     if (st != DRGG_OK) return st;
     if (!W1q || !w1_scale || !W2q || !w2_scale || (T > 0 && (!X || !logits || !out))) return DRGG_EINVAL;
-    if (!aligned16(X) || !aligned16(logits) || !aligned16(W1q) || !aligned16(w1_scale) || !aligned16(W2q) ||
+    if (!aligned16(X) || !aligned_logits(logits, E) || !aligned16(W1q) || !aligned16(w1_scale) || !aligned16(W2q) ||
         !aligned16(w2_scale) || !aligned16(out))
         return DRGG_EALIGN;
     if (T == 0) return DRGG_OK;

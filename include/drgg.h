@@ -476,8 +476,9 @@ drgg_status drgg_tailsplit_units(int64_t tiles, int64_t workers, int64_t *out);
  * pair; rows move into the grouped order and back; and for serving the
  * products run in 8-bit integers.  The conventions at the top of this file
  * hold here too (caller-owned buffers, asynchronous on `stream`, nothing
- * enqueued on an error, capturable).  Alignment: logits, dlogits, rows, codes,
- * w_scale and the workspace 16 bytes, other arrays 4.
+ * enqueued on an error, capturable).  Alignment: rows, codes, w_scale, the
+ * workspace and, with E a multiple of 4, logits and dlogits 16 bytes, other
+ * arrays 4.
  *
  * T tokens with k experts each make R = T*k pairs, pair t*k + j being token t
  * and its j-th expert.  Limits: 1 <= E <= 1024, 1 <= k <= min(E, 64),
