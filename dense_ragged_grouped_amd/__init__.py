@@ -436,6 +436,13 @@ class Workspace:
 _default_ws = {}
 
 
+def _need_span(workspace):
+    """A workspace's size in bytes is that of its elements: an expanded tensor
+    has fewer."""
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+
+
 def _workspace(device, nbytes, workspace, deterministic, kind="wgrad", stream=None):
     torch = _torch()
     if workspace is False:   # explicitly none (the data gradient's direct program)
@@ -445,6 +452,8 @@ def _workspace(device, nbytes, workspace, deterministic, kind="wgrad", stream=No
         buf = workspace.get(nbytes, s) if isinstance(workspace, Workspace) else workspace
         if buf is not None and buf.device != device:
             raise ValueError(f"the workspace is on {buf.device}, the operands on {device}")
+        if buf is not None:
+            _need_span(buf)
     else:
         # keyed by the program that runs (`deterministic` here: whether the
         # deterministic program runs): a non-deterministic call routed to it
@@ -993,6 +1002,8 @@ def moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True, o
     out = _out(out, torch.bfloat16, (T, H), X, stream)
     if workspace is None:
         workspace = _scratch(X, ffn_workspace_size(T, E, k, H, I), stream)
+    else:
+        _need_span(workspace)
     _call("moe_ffn_int8", stream, (X, logits, W1q, w1_scale, W2q, w2_scale, out, workspace), X.data_ptr(),
           logits.data_ptr(), W1q.data_ptr(), w1_scale.data_ptr(), W2q.data_ptr(), w2_scale.data_ptr(), T, E, int(k), H,
           I, 1 if renormalize else 0, out.data_ptr(), workspace.data_ptr(),
