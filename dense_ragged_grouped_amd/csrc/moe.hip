@@ -362,6 +362,8 @@ struct RouteGradArgs {
 //   softmax over the chosen: w_j (dw_j - s) at the chosen, 0 elsewhere;
 //   softmax over all: p_e (dw_e - s), dw_e = 0 but at the chosen, where p_e
 //   is w_j; the p are recomputed from the logits.
+// An expert of probability 0 gets 0 and its dw_j is not used: a masked
+// expert's row, and so its dw_j, may hold anything.
 // The row is first written as if no expert were chosen, then lane j writes
 // the chosen ones; the fence between makes the second store the last.
 template <int V>
@@ -372,7 +374,10 @@ __global__ __launch_bounds__(256) void moe_route_grad_kernel(RouteGradArgs a) {
     const bool live = t < a.T;
     float s = 0.f;
     if (live)
-        for (int j = l; j < k; j += 16) s += a.weights[t * k + j] * a.dweights[t * k + j];
+        for (int j = l; j < k; j += 16) {
+            const float w = a.weights[t * k + j];
+            s += w != 0.f ? w * a.dweights[t * k + j] : 0.f;
+        }
     s = row_sum(s);
     float g[V];
     if (a.renormalize) {
@@ -393,7 +398,7 @@ __global__ __launch_bounds__(256) void moe_route_grad_kernel(RouteGradArgs a) {
         }
         total = row_sum(total);
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = none ? 0.f : -s * (g[i] / total);
+        for (int i = 0; i < V; ++i) g[i] = g[i] == 0.f ? 0.f : -s * (g[i] / total);
     }
     float* out = a.dlogits + t * E;
     if (live) {
@@ -413,7 +418,8 @@ __global__ __launch_bounds__(256) void moe_route_grad_kernel(RouteGradArgs a) {
     if (live)
         for (int j = l; j < k; j += 16) {
             const int32_t e = a.experts[t * k + j];
-            if (e >= 0 && e < E) out[e] = a.weights[t * k + j] * (a.dweights[t * k + j] - s);
+            const float w = a.weights[t * k + j];
+            if (e >= 0 && e < E) out[e] = w != 0.f ? w * (a.dweights[t * k + j] - s) : 0.f;
         }
 }
 

@@ -513,7 +513,8 @@ drgg_status moe_route_workspace_size(int64_t T, int32_t E, int32_t k, size_t *by
  *   renormalize != 0: w_j (dw_j - s) at the chosen experts, 0 elsewhere;
  *   else:             p_e (dw_e - s), p the softmax over all experts and dw_e
  *                     the chosen experts' dweights, 0 for the others.
- * A token with every expert masked gets zeros.
+ * An expert of weight 0 (a masked one) gets 0 and its dweights, whatever they
+ * hold, are not used; a token with every expert masked gets zeros.
  */
 drgg_status moe_route_grad(const float *dweights, const float *logits, const int32_t *experts,
                            const float *weights, int64_t T, int32_t E, int32_t k, int renormalize,
