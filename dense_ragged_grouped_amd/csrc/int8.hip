@@ -57,8 +57,8 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantArgs a) {
 //
 // Blocks of tokens are 16, 32 or 64 long by what is left of the group; U steps
 // are loaded before the first is used.  Rows and reduction positions outside
-// the operands carry an out-of-range offset and read as zero.  launch_int8
-// says which NB, W and TOK run when.
+// the operands carry an out-of-range offset and read as zero.  int8_program
+// (plan.hpp) says which NB, W and TOK run when.
 //
 // Bound by the weights' bytes on many experts (64 rows on 32 of 1536x2048, 88
 // MB: 17 us, 5.0 TB/s), by latency on one (one row through 4096x4096: 6 us).
@@ -490,54 +490,27 @@ hipError_t launch_quantize_int8(const void* X, bool bf16, int64_t T, int64_t K, 
     return hipGetLastError();
 }
 
-// Which program runs, from the sizes alone (forced_tile: the test knob; a tile
-// this product has, or none).  M rows in E groups of unknown
-// sizes make about M/64 + E/2 blocks of 64 tokens, and up to 48 rows a group
-// about one for each.
+template <bool GATED>
+hipError_t launch_int8_program(const Int8Args& a, const Int8Program& p, bool bf16, hipStream_t s) {
+    if (p.tok == 32) return launch_int8_rows<GATED, 4, 4, 32>(a, bf16, s);
+    if (p.waves == 4) return launch_int8_rows<GATED, 4, 4, 64>(a, bf16, s);
+    if (p.nb == 4) return launch_int8_rows<GATED, 4, 8, 64>(a, bf16, s);
+    if constexpr (!GATED)
+        if (p.nb == 1) return launch_int8_rows<false, 1, 8, 64>(a, bf16, s);
+    return launch_int8_rows<GATED, 2, 8, 64>(a, bf16, s);
+}
+
 hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s) {
-    const bool may128 = !(gated && bf16);
-    int tile = forced_tile;
-    if (tile != kTile256x256 && tile != kTile128x256 && !(tile == kTile128x128 && may128)) tile = kTileAuto;
-    // a launch has fewer than 2^32 threads (the tiles walk theirs)
-    const bool rows = tile == kTileAuto && (a.M / 32 + a.E) * ceil_div(a.N, 16) < int64_t(1) << 22;
-    const int64_t cols = ceil_div(a.N, 64), full = a.M < a.E ? a.M : a.E;
-    const int64_t blocks = cols * (a.M <= 48 * (int64_t)a.E ? full : ceil_div(a.M, 64) + a.E / 2);
-    if (rows && cols * a.E >= 2 * kRuleCUs && a.M <= 24 * (int64_t)a.E) {
-        // many experts' weights, few rows of each: read at memory speed (E = 32,
-        // 1536x2048: 256 rows 20 us, 512 rows 23, 768 rows 30; in 128x256 tiles
-        // 27, 28 and 29; 57 x 1000x1008, 1368 rows: 15 against 19)
-        return gated ? launch_int8_rows<true, 4, 4, 32>(a, bf16, s) : launch_int8_rows<false, 4, 4, 32>(a, bf16, s);
-    }
-    if (rows && blocks <= kRuleCUs) {
-        // one block per CU at most: the smallest blocks for which that holds
-        // (one group of 4096x4096: 128 rows in blocks of 32 columns 16 us, of 64
-        // 20; 192 rows 26 and 20, since the smaller ones need a second round;
-        // 256 rows 20, in 128x128 tiles 25)
-        if (2 * blocks > kRuleCUs)
-            return gated ? launch_int8_rows<true, 4, 8, 64>(a, bf16, s) : launch_int8_rows<false, 4, 8, 64>(a, bf16, s);
-        if (gated) return launch_int8_rows<true, 2, 8, 64>(a, bf16, s);
-        return 4 * blocks > kRuleCUs ? launch_int8_rows<false, 2, 8, 64>(a, bf16, s)
-                                     : launch_int8_rows<false, 1, 8, 64>(a, bf16, s);
-    }
-    if (rows && blocks <= 2 * kRuleCUs && (a.M <= 48 * (int64_t)a.E || a.K % 128 != 0)) {
-        // two blocks per CU at most, of four waves: with about one for each
-        // group's columns (48 rows of each of 32 experts: 928x1504 14.3 us,
-        // 1024x2048 19.3, 768x768 11.1; in 128x128 tiles 18.1, 20.4, 12.1; 64
-        // rows of each, 1024x2048: 27 and 21), and where K is no multiple of 128,
-        // with which these blocks gain and tiles lose (E = 5, 955 rows, 1472
-        // columns: K = 2304 22.0 us, 2368 17.0, 2432 22.7; in 128x128 tiles 17.3,
-        // 19.7, 18.6)
-        return gated ? launch_int8_rows<true, 4, 4, 64>(a, bf16, s) : launch_int8_rows<false, 4, 4, 64>(a, bf16, s);
-    }
+    const Int8Program p = int8_program(a.E, a.M, a.N, a.K, gated, bf16, forced_tile);
+    if (p.tile == kTileAuto)
+        return gated ? launch_int8_program<true>(a, p, bf16, s) : launch_int8_program<false>(a, p, bf16, s);
     const int64_t cols_out = gated ? a.N / 2 : a.N, bc = gated ? 128 : 256;
-    if (tile == kTileAuto)
-        tile = int8_tile(a.E, a.M, a.K, ceil_div(cols_out, bc), ceil_div(cols_out, bc / 2), may128);
     auto grid = [&](int64_t bm, int64_t bcols, int64_t per_cu) {
         const int64_t most = (a.M / bm + (a.M < a.E ? a.M : a.E)) * ceil_div(cols_out, bcols);
         return most < per_cu * cus ? most : per_cu * cus;
     };
-    if (tile == kTile256x256) return launch_int8_tile<256, 256, 8>(a, gated, bf16, grid(256, bc, 1), s);
-    if (tile == kTile128x256) return launch_int8_tile<128, 256, 4>(a, gated, bf16, grid(128, bc, 1), s);
+    if (p.tile == kTile256x256) return launch_int8_tile<256, 256, 8>(a, gated, bf16, grid(256, bc, 1), s);
+    if (p.tile == kTile128x256) return launch_int8_tile<128, 256, 4>(a, gated, bf16, grid(128, bc, 1), s);
     return launch_int8_tile<128, 128, 4>(a, gated, bf16, grid(128, bc / 2, 2), s);
 }
 

@@ -494,7 +494,7 @@ inline int default_tile(int op, int64_t E, int64_t M, int64_t N, int64_t K, bool
     return kTile256x256;
 }
 
-// The tile of the 8-bit product when it runs in tiles (launch_int8).  nc: the
+// The tile of the 8-bit product when it runs in tiles (int8_program).  nc: the
 // output's columns in tiles of 256 (gated: 128) and in tiles of 128 (gated:
 // 64).  The group sizes are not known here: M rows in E groups make about
 // M/bm + E/2 row tiles, and one for each group with rows at least.  A round of
@@ -526,6 +526,46 @@ inline int int8_tile(int64_t E, int64_t M, int64_t K, int64_t nc256, int64_t nc1
     const double best = c256 < 1.15 * c128x256 ? c256 : 1.15 * c128x256;
     if (may128 && (M <= 96 * E || 1.15 * c128 < best)) return kTile128x128;
     return best == c256 ? kTile256x256 : kTile128x256;
+}
+
+// The program of an 8-bit product (launch_int8): an output tile, or, with tile
+// kTileAuto, the few-row program in blocks of 16*nb weight rows and up to tok
+// tokens on `waves` waves.
+struct Int8Program { int tile, nb, waves, tok; };
+
+// From the sizes alone (forced_tile: the test knob; a tile this product has,
+// or none).  M rows in E groups of unknown sizes make about M/64 + E/2 blocks of
+// 64 tokens, and up to 48 rows a group about one for each.
+inline Int8Program int8_program(int64_t E, int64_t M, int64_t N, int64_t K, bool gated, bool bf16, int forced_tile) {
+    const bool may128 = !(gated && bf16);
+    const int64_t cols_out = gated ? N / 2 : N, bc = gated ? 128 : 256;
+    if (forced_tile == kTile256x256 || forced_tile == kTile128x256 || (forced_tile == kTile128x128 && may128))
+        return {forced_tile, 0, 0, 0};
+    // a launch has fewer than 2^32 threads (the tiles walk theirs)
+    const bool rows = (M / 32 + E) * ceil_div(N, 16) < int64_t(1) << 22;
+    const int64_t cols = ceil_div(N, 64), full = M < E ? M : E;
+    const int64_t blocks = cols * (M <= 48 * E ? full : ceil_div(M, 64) + E / 2);
+    // many experts' weights, few rows of each: read at memory speed (E = 32,
+    // 1536x2048: 256 rows 20 us, 512 rows 23, 768 rows 30; in 128x256 tiles
+    // 27, 28 and 29; 57 x 1000x1008, 1368 rows: 15 against 19)
+    if (rows && cols * E >= 2 * kRuleCUs && M <= 24 * E) return {kTileAuto, 4, 4, 32};
+    if (rows && blocks <= kRuleCUs) {
+        // one block per CU at most: the smallest blocks for which that holds
+        // (one group of 4096x4096: 128 rows in blocks of 32 columns 16 us, of 64
+        // 20; 192 rows 26 and 20, since the smaller ones need a second round;
+        // 256 rows 20, in 128x128 tiles 25)
+        if (2 * blocks > kRuleCUs) return {kTileAuto, 4, 8, 64};
+        return {kTileAuto, gated || 4 * blocks > kRuleCUs ? 2 : 1, 8, 64};
+    }
+    // two blocks per CU at most, of four waves: with about one for each
+    // group's columns (48 rows of each of 32 experts: 928x1504 14.3 us,
+    // 1024x2048 19.3, 768x768 11.1; in 128x128 tiles 18.1, 20.4, 12.1; 64
+    // rows of each, 1024x2048: 27 and 21), and where K is no multiple of 128,
+    // with which these blocks gain and tiles lose (E = 5, 955 rows, 1472
+    // columns: K = 2304 22.0 us, 2368 17.0, 2432 22.7; in 128x128 tiles 17.3,
+    // 19.7, 18.6)
+    if (rows && blocks <= 2 * kRuleCUs && (M <= 48 * E || K % 128 != 0)) return {kTileAuto, 4, 4, 64};
+    return {int8_tile(E, M, K, ceil_div(cols_out, bc), ceil_div(cols_out, bc / 2), may128), 0, 0, 0};
 }
 
 }  // namespace drgg
