@@ -560,11 +560,15 @@ inline Int8Program int8_program(int64_t E, int64_t M, int64_t N, int64_t K, bool
     // two blocks per CU at most, of four waves: with about one for each
     // group's columns (48 rows of each of 32 experts: 928x1504 14.3 us,
     // 1024x2048 19.3, 768x768 11.1; in 128x128 tiles 18.1, 20.4, 12.1; 64
-    // rows of each, 1024x2048: 27 and 21), and where K is no multiple of 128,
-    // with which these blocks gain and tiles lose (E = 5, 955 rows, 1472
-    // columns: K = 2304 22.0 us, 2368 17.0, 2432 22.7; in 128x128 tiles 17.3,
-    // 19.7, 18.6)
-    if (rows && blocks <= 2 * kRuleCUs && (M <= 48 * E || K % 128 != 0)) return {kTileAuto, 4, 4, 64};
+    // rows of each, 1024x2048: 27 and 21), and, up to 2048 rows a group, where K
+    // is no multiple of 128, with which these blocks gain and tiles lose (E = 5,
+    // 955 rows, 1472 columns: K = 2304 22.0 us, 2368 17.0, 2432 22.7; in 128x128
+    // tiles 17.3, 19.7, 18.6; over 9 pairs of E and N, E from 1 to 32, with K
+    // from 16 to 8208, 0.48 to 1.29 of the best tile's time, 0.90 on average;
+    // cause not known).  Longer groups share their weights better in tiles (E = 1,
+    // N = 256, 4793 rows, K = 4112: 31 us, 128x128 22).
+    if (rows && blocks <= 2 * kRuleCUs && (M <= 48 * E || (K % 128 != 0 && M <= 2048 * E)))
+        return {kTileAuto, 4, 4, 64};
     return {int8_tile(E, M, K, ceil_div(cols_out, bc), ceil_div(cols_out, bc / 2), may128), 0, 0, 0};
 }
 

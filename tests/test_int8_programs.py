@@ -66,6 +66,19 @@ def test_the_shapes_reach_every_program(tmp_path):
         assert reached == rows | {(t, 0, 0, 0) for t in (T256, T128, T128x256)}
 
 
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_long_groups_run_in_tiles(tmp_path):
+    """Two blocks of 64 tokens per CU without more than 2048 rows a group: beyond, whatever K is, in tiles."""
+    exe = str(tmp_path / "int8_programs")
+    subprocess.run(["g++", "-std=c++17", *SAN, "-I", os.path.join(ROOT, "dense_ragged_grouped_amd", "csrc"),
+                    os.path.join(HERE, "int8_programs.cpp"), "-o", exe], check=True)
+    cases = [(1, 4793, 256, 4112), (1, 7673, 256, 2000), (1, 30713, 64, 144), (1, 1785, 1040, 400), (5, 1145, 1472, 2368),
+             (16, 3321, 512, 784)]
+    text = "".join(f"{E} {M} {N} {K} 0 1\n" for E, M, N, K in cases)
+    got = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split()
+    assert [int(t) != 0 for t in got[::4]] == [M > 2048 * E for E, M, _, _ in cases]
+
+
 def product64(X, xs, W, ws, counts, gated):
     out, at = [], 0
     for e, n in enumerate(counts):
