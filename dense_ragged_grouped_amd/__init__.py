@@ -737,6 +737,7 @@ def router_gemm_fp32_bf16x3(X, Wr, out=None, stream=None, workspace=None):
 
 def workspace_init(buf, stream=None):
     """Zero a workspace tensor with the library's fill kernel."""
+    _need_span(buf)
     _check(lib.drgg_workspace_init(buf.data_ptr(), buf.numel() * buf.element_size(),
                                    _stream(buf.device, stream)), "drgg_workspace_init")
 

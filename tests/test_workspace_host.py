@@ -45,6 +45,14 @@ def calls(d):
     }
 
 
+def test_zeroed_workspace_must_be_contiguous(drgg, launched):  # noqa: F811
+    with pytest.raises(ValueError, match="contiguous"):
+        drgg.workspace_init(torch.zeros(1, dtype=torch.uint8).expand(1 << 20))
+    assert not launched
+    drgg.workspace_init(torch.zeros(64, dtype=torch.uint8))
+    assert launched
+
+
 @pytest.mark.parametrize("name", sorted(calls(None)))
 def test_workspace_must_be_contiguous(drgg, launched, name):  # noqa: F811
     call = calls(drgg)[name]
