@@ -390,6 +390,8 @@ def _new(shape, dtype, like, stream):
         return like.new_empty(shape, dtype=dtype)
     torch = _torch()
     caller = torch.cuda.current_stream(like.device)
+    if stream == caller:
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
         t = like.new_empty(shape, dtype=dtype)
     t.record_stream(caller)

@@ -99,6 +99,13 @@ def test_results_on_a_given_stream(drgg, world, name):  # noqa: F811
         assert shared.get(at) == {home}
 
 
+def test_the_given_stream_is_the_current_one(drgg, world):  # noqa: F811
+    """Nothing to record then."""
+    home, _, born, shared = world
+    got = calls(drgg)["moe_combine"](home)
+    assert born[got.untyped_storage()._cdata] is home and not shared
+
+
 @pytest.mark.parametrize("name", sorted(calls(None)))
 def test_results_on_the_current_stream(drgg, world, name, monkeypatch):  # noqa: F811
     home, _, born, shared = world
