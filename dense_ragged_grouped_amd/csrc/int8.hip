@@ -27,9 +27,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // silu(g) u = g u / (1 + exp(-g)).  The exponential and the reciprocal are the
-// hardware's (within 1 ulp each): with the library's expf and a correctly
-// rounded division the gate was the larger part of the gated product's
-// epilogue.  exp(-g) overflows to infinity below g = -88 and the result is 0.
+// hardware's, within 1 ulp each; the exponential's argument is rounded before,
+// which moves the result by |g| 2^-24 of it, a third of what the three roundings
+// of g itself (the sum, two scales) do.  Below g = -87 the sigmoid leaves FP32's
+// normal range and the result is 0, off by less than 2^-100 |g u|.  With the
+// library's expf and a correctly rounded division the gate was the larger part
+// of the gated product's epilogue.
 __device__ __forceinline__ float gate(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }
@@ -337,8 +340,8 @@ __device__ __forceinline__ void store_tile_values(Value value, int rb, lds_t* sc
 // the accumulators of neighbouring blocks.  The epilogue scales (and gates)
 // the sums as they pass to the staged whole-line stores.
 //
-// 131072x1536x2048 in 8 groups, BF16 out: 407 to 430 us (2.0 POP/s; a large
-// library product reaches 2.1 to 2.3 on this card).  Of a 256x256 tile's time
+// 131072x1536x2048 in 8 groups, BF16 out: 407 to 462 us from run to run (2.0 to
+// 1.8 POP/s; a large library product reaches 2.1 to 2.3 on this card).  Of a 256x256 tile's time
 // 0.83 us per 64 reduction values are the main loop (2.4 POP/s; 20 % faster on
 // zeros, so a part of it is the clock under load, the rest the loads' path as
 // in BF16) and about 6.7 us its epilogue and switch: without the global stores

@@ -129,9 +129,10 @@ __device__ __forceinline__ int32_t block_prefix(int32_t v, int32_t* tmp) {
 // ranks for moe_place_kernel and the counts go to the table: bytes (at most
 // 64 each) [blocks][E rounded up to 4], or with more than kRouteBytes blocks
 // words [blocks][E] for moe_scan_kernel.
-// Bound by the latency of the k dependent rounds: 12 us for 16384 tokens, k = 8
-// of 256 experts (16.8 MB of logits, 3.4 us at the rate of a large copy), 4 us
-// for 2039 tokens, k = 2 of 32; with a wave per token and shuffles through LDS
+// Bound by the k dependent rounds: 12 us for 16384 tokens, k = 8 of 256 experts
+// (16.8 MB of logits, 3.4 us at the rate of a large copy), of which the rounds'
+// 88 vector instructions take about 4.7 us to issue and the rest is waiting, part
+// of it between a compare and the select that reads its mask; 4 us for 2039 tokens, k = 2 of 32; with a wave per token and shuffles through LDS
 // 21 and 12 us.
 template <int V, int S>
 __device__ __forceinline__ void select_tokens(const RouteArgs& a) {

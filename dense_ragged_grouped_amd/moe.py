@@ -93,7 +93,9 @@ def combine(rows, positions, weights):
 
 def ffn(X, logits, W1, W2, k, renormalize=True, deterministic=True):
     """The block in BF16, differentiable in X [T, H], logits [T, E] (FP32), W1
-    and W2; the weight gradients as autograd.grouped_linear computes them."""
+    and W2; the weight gradients as autograd.grouped_linear computes them.  What
+    passes from one operator to the next is BF16: gate and up, silu(gate), its
+    product with up, and the experts' outputs are rounded once each."""
     r = route(logits, k, renormalize)
     gate, up = grouped_linear(dispatch(X, r.positions), W1, r.group_offsets, deterministic).chunk(2, dim=1)
     h = torch.nn.functional.silu(gate) * up

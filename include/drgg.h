@@ -563,7 +563,8 @@ drgg_status quantize_int8(const void *X, drgg_dtype dtype, int64_t T, int64_t K,
  * once to out_dtype.  Y [M,N]; rows outside every group (offsets that end
  * before M) are not written.
  * gated != 0: N = 2I, Y [M,I] = silu(g) * u with g and u columns i and I + i of
- * the product (in FP32), silu(g) = g / (1 + exp(-g)).
+ * the product (in FP32), silu(g) = g / (1 + exp(-g)) to within (4 |g| + 16) 2^-24
+ * of it, and 0 below g = -87, where the sigmoid leaves FP32's normal range.
  * rows (int32 [M] on the device, NULL for none; moe_route's tokens): row t of
  * the product is row rows[t] of Xq [T,K] and x_scale [T], so that tokens need
  * not be copied into the grouped order; T*K <= 2^31 - 4097 then (DRGG_ESHAPE).
