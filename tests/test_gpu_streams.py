@@ -74,3 +74,24 @@ def test_results_on_a_given_stream(drgg, name):
         assert torch.equal(a, b)
         assert home_stream(a) == torch.cuda.current_stream().cuda_stream
         assert home_stream(b) == side.cuda_stream
+
+
+@pytest.mark.parametrize("name", ["grouped_gemm_fwd", "moe_route", "moe_ffn_int8"])
+def test_captured_on_a_forked_stream(drgg, name):
+    """A call on a stream that a capture forks to: every replay gives the eager result."""
+    call = calls(drgg)[name]
+    want = call(None)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    want, got = (x if isinstance(x, tuple) else (x,) for x in (want, got))
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        call(None)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
