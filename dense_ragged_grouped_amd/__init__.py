@@ -16,7 +16,11 @@ Around them, for a whole expert layer: the router's selection (moe_route,
 moe_route_grad), the movement of rows (moe_dispatch, moe_combine,
 moe_combine_grad), and products in 8-bit integers (quantize_int8,
 grouped_gemm_int8, gemm_int8); moe_ffn_int8 runs them as one serving block, and
-`moe` holds the differentiable ones.
+`moe` holds the differentiable ones.  moe_route_scores selects by sigmoid or
+softmax scores with a bias and groups of experts; quantize_mxfp4,
+grouped_gemm_mxfp4, gemm_mxfp4 and moe_ffn_mxfp4 are the products and the serving
+block in microscaled 4-bit floating point; moe_gate_int8 is a training step's gated
+activation, which keeps its inputs in 8 bits for its gradient.
 
 ``offsets`` is an int32 CUDA tensor: offsets[0] = 0, non-decreasing,
 offsets[E] = M; expert e owns tokens offsets[e] .. offsets[e+1]-1.
@@ -48,6 +52,8 @@ EXPORTS = (
     "drgg_set_knob", "drgg_timing_count", "drgg_timing_read", "drgg_status_string", "drgg_abi_version",
     "moe_route", "moe_route_workspace_size", "moe_route_grad", "moe_dispatch", "moe_combine", "moe_combine_grad",
     "quantize_int8", "grouped_gemm_int8", "gemm_int8", "moe_ffn_int8", "moe_ffn_int8_workspace_size",
+    "moe_route_scores", "moe_route_scores_grad", "quantize_mxfp4", "dequantize_mxfp4", "grouped_gemm_mxfp4",
+    "gemm_mxfp4", "moe_ffn_mxfp4", "moe_ffn_mxfp4_workspace_size", "moe_gate_int8", "moe_gate_int8_grad",
 )
 
 
@@ -78,6 +84,14 @@ class Batched(ctypes.Structure):
         ("a_row", ctypes.c_int64), ("a_batch", ctypes.c_int64),
         ("b_row", ctypes.c_int64), ("b_batch", ctypes.c_int64),
         ("o_row", ctypes.c_int64), ("o_batch", ctypes.c_int64),
+    ]
+
+
+class ScoringStruct(ctypes.Structure):
+    """drgg_scoring."""
+    _fields_ = [
+        ("score", ctypes.c_int), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("best", ctypes.c_int32),
+        ("renormalize", ctypes.c_int), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p),
     ]
 
 
@@ -158,6 +172,19 @@ def _load(path=LIB_PATH):
     lib.gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp]
     lib.moe_ffn_int8.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, i64, c_int, vp, vp, sz, vp]
     lib.moe_ffn_int8_workspace_size.argtypes = [i64, i32, i32, i64, i64, ctypes.POINTER(sz)]
+    ps = ctypes.POINTER(ScoringStruct)
+    lib.moe_route_scores.argtypes = [vp, i64, i32, i32, ps, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_route_scores_grad.argtypes = [vp, vp, vp, vp, i64, i32, i32, ps, vp, vp]
+    lib.quantize_mxfp4.argtypes = [vp, c_int, i64, i64, vp, vp, vp]
+    lib.dequantize_mxfp4.argtypes = [vp, vp, i64, i64, c_int, vp, vp]
+    lib.grouped_gemm_mxfp4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i64, i64, i64, c_int, c_int, vp, vp]
+    lib.gemm_mxfp4.argtypes = [vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp]
+    lib.moe_ffn_mxfp4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, i64, ps, vp, vp, sz, vp]
+    lib.moe_ffn_mxfp4_workspace_size.argtypes = [i64, i32, i32, i64, i64, ctypes.POINTER(sz)]
+    lib.moe_gate_int8.argtypes = [vp, vp, vp, i64, i32, i64, vp, vp, vp, vp]
+    lib.moe_gate_int8_grad.argtypes = [vp, vp, vp, vp, vp, i64, i32, i64, vp, vp, vp, vp]
+    for name in EXPORTS[-10:]:
+        getattr(lib, name).restype = c_int
     for name in ("moe_ffn_int8", "moe_ffn_int8_workspace_size", "moe_route", "moe_route_workspace_size", "moe_route_grad", "moe_dispatch", "moe_combine",
                  "moe_combine_grad", "quantize_int8", "grouped_gemm_int8", "gemm_int8"):
         getattr(lib, name).restype = c_int
@@ -1018,6 +1045,262 @@ def ffn_workspace_size(T: int, E: int, k: int, H: int, I: int) -> int:
     n = ctypes.c_size_t()
     _check(lib.moe_ffn_int8_workspace_size(T, E, k, H, I, ctypes.byref(n)), "moe_ffn_int8_workspace_size")
     return n.value
+
+
+# ---- selection by scores ---------------------------------------------------------
+
+class Scoring(NamedTuple):
+    """How moe_route_scores chooses and weighs: `score` "sigmoid" or "softmax";
+    `bias` FP32 [E] (added to the score for the choice alone) or None; the E
+    experts in `groups` groups of neighbours, of which the top_groups take part
+    whose largest value (best=1), or the sum of their two largest (best=2), is
+    largest; weights renormalised over the chosen or not, times `scale`."""
+    score: str = "sigmoid"
+    bias: "torch.Tensor | None" = None
+    groups: int = 1
+    top_groups: int = 1
+    best: int = 2
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _scoring(c, E):
+    """The C structure of a Scoring (its bias is not kept alive by it)."""
+    if c.score not in _SCORES:
+        raise ValueError(f"unknown score {c.score!r}: sigmoid or softmax")
+    at = None
+    if c.bias is not None:
+        _need_shape(c.bias, _torch_module.float32, (E,), "bias")
+        at = c.bias.data_ptr()
+    return ScoringStruct(_SCORES[c.score], c.groups, c.top_groups, c.best, 1 if c.renormalize else 0, c.scale, at)
+
+
+def moe_route_scores(logits, k, scoring=Scoring(), workspace=None, stream=None):
+    """moe_route on scores of the logits [T, E] (FP32), chosen and weighted as
+    the Scoring says: a Routing.  Choices are those of 64-bit values, ties to
+    the lowest index.  A masked (-inf) logit, or a bias of -inf, is chosen last
+    and gets weight 0."""
+    torch = _torch_module
+    _need(logits, torch.float32, "logits", 2)
+    T, E = logits.shape
+    k = int(k)
+    c = _scoring(scoring, E)
+    nbytes = route_workspace_size(T, E, k)
+    R = T * k
+    weights = _new((T, k), torch.float32, logits, stream)
+    ints = _new((3 * R + E + 1,), torch.int32, logits, stream)   # one allocation, as in moe_route
+    experts, positions = ints.as_strided((T, k), (k, 1)), ints.as_strided((T, k), (k, 1), R)
+    tokens, offsets = ints.as_strided((R,), (1,), 2 * R), ints.as_strided((E + 1,), (1,), 3 * R)
+    ws_ptr, ws_bytes = None, 0
+    if nbytes and workspace is None:
+        scratch = _scratch(logits, nbytes, stream)
+        ws_ptr, ws_bytes = scratch.data_ptr(), nbytes
+    elif nbytes:
+        ws_ptr, ws_bytes = _workspace(logits.device, nbytes, workspace, True, stream=stream)
+    at = ints.data_ptr()
+    _call("moe_route_scores", stream, (logits, scoring.bias), logits.data_ptr(), T, E, k, c, at, weights.data_ptr(),
+          at + 12 * R, at + 4 * R, at + 8 * R, ws_ptr, ws_bytes)
+    return Routing(experts, weights, offsets, positions, tokens)
+
+
+def moe_route_scores_grad(dweights, logits, experts, weights, scoring=Scoring(), out=None, stream=None):
+    """dlogits [T, E] from the gradient of moe_route_scores' weights."""
+    torch = _torch_module
+    _need(logits, torch.float32, "logits", 2)
+    T, E = logits.shape
+    _need(experts, torch.int32, "experts", 2)
+    k = experts.shape[1]
+    _need_shape(experts, torch.int32, (T, k), "experts")
+    _need_shape(weights, torch.float32, (T, k), "weights")
+    _need_shape(dweights, torch.float32, (T, k), "dweights")
+    c = _scoring(scoring._replace(bias=None), E)
+    out = _out(out, torch.float32, (T, E), logits, stream)
+    _call("moe_route_scores_grad", stream, (logits, dweights, experts, weights, out), dweights.data_ptr(),
+          logits.data_ptr(), experts.data_ptr(), weights.data_ptr(), T, E, k, c, out.data_ptr())
+    return out
+
+
+# ---- microscaled 4-bit floating point ---------------------------------------------
+
+def mxfp4_scales(scales):
+    """Scale bytes [.., rows, K/32], one after another in each row as other
+    programs store them, in the layout that the 4-bit products read:
+    [ceil(K/256), .., rows, 8]."""
+    torch = _torch_module
+    if scales.dtype != torch.uint8 or scales.dim() < 2:
+        raise TypeError("scales must be uint8 with at least two dimensions")
+    blocks = -(-scales.shape[-1] // 8)
+    padded = torch.nn.functional.pad(scales, (0, 8 * blocks - scales.shape[-1]))
+    return padded.unflatten(-1, (blocks, 8)).movedim(-2, 0).contiguous()
+
+
+def quantize_mxfp4(X, stream=None):
+    """Codes and scales of the rows of X [T, K] (BF16 or FP32, K a multiple of
+    32): (codes uint8 [T, K/2], scales uint8 [ceil(K/256), T, 8])."""
+    torch = _torch_module
+    code = _row_code(X, "X")
+    T, K = X.shape
+    codes = _new((T, K // 2), torch.uint8, X, stream)
+    scales = _new((-(-K // 256), T, 8), torch.uint8, X, stream)
+    _call("quantize_mxfp4", stream, (X,), X.data_ptr(), code, T, K, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def _mx_operand(codes, scales, dims, what):
+    """K of codes [.., K/2] whose scales have their shape."""
+    torch = _torch_module
+    _need(codes, torch.uint8, what, dims)
+    _need(scales, torch.uint8, f"{what}'s scales", dims + 1)
+    K = 2 * codes.shape[-1]
+    if scales.shape != (-(-K // 256), *codes.shape[:-1], 8):
+        raise ValueError(f"{what} is {tuple(codes.shape)}, its scales {tuple(scales.shape)}")
+    return K
+
+
+def dequantize_mxfp4(codes, scales, dtype=None, out=None, stream=None):
+    """The values [T, K] that quantize_mxfp4's codes and scales stand for, BF16
+    (default) or FP32."""
+    K = _mx_operand(codes, scales, 2, "codes")
+    code = BF16 if dtype is None else _dtype_code(dtype)
+    T = codes.shape[0]
+    out = _out(out, _torch_dtype(code), (T, K), codes, stream)
+    _call("dequantize_mxfp4", stream, (codes, scales, out), codes.data_ptr(), scales.data_ptr(), T, K, code, out.data_ptr())
+    return out
+
+
+def _mx_operands(Xq, x_scale, Wq, w_scale, wdim, M, gated, out_dtype, out, stream):
+    K, Kw = _mx_operand(Xq, x_scale, 2, "Xq"), _mx_operand(Wq, w_scale, wdim, "Wq")
+    if K != Kw:
+        raise ValueError(f"shape mismatch: Xq {tuple(Xq.shape)}, Wq {tuple(Wq.shape)}")
+    T, N = Xq.shape[0], Wq.shape[-2]
+    code = BF16 if out_dtype is None else _dtype_code(out_dtype)
+    out = _out(out, _torch_dtype(code), (T if M is None else M, N // 2 if gated else N), Xq, stream)
+    return T, N, K, code, out
+
+
+def grouped_gemm_mxfp4(Xq, x_scale, Wq, w_scale, group_offsets, gated=False, rows=None, out_dtype=None, out=None,
+                       stream=None):
+    """Y[t] = x[t] w[e(t)]^T for 4-bit codes Xq [M, K/2], Wq [E, N, K/2] with
+    scales [ceil(K/256), M, 8], [ceil(K/256), E, N, 8]: FP32 accumulation of
+    exact products, rounded once to out_dtype (bf16 by default).  gated and
+    rows as for grouped_gemm_int8; with rows, Xq [T, K/2], T*K/2 < 2^31 - 4096."""
+    torch = _torch_module
+    E = _offsets(group_offsets)
+    M = at = None
+    if rows is not None:
+        _need(rows, torch.int32, "rows", 1)
+        M, at = rows.numel(), rows.data_ptr()
+    T, N, K, code, out = _mx_operands(Xq, x_scale, Wq, w_scale, 3, M, gated, out_dtype, out, stream)
+    if Wq.shape[0] != E:
+        raise ValueError(f"shape mismatch: Wq {tuple(Wq.shape)}, E={E}")
+    _call("grouped_gemm_mxfp4", stream, (Xq, x_scale, Wq, w_scale, group_offsets, rows, out), Xq.data_ptr(),
+          x_scale.data_ptr(), Wq.data_ptr(), w_scale.data_ptr(), group_offsets.data_ptr(), at, T, E,
+          T if M is None else M, N, K, 1 if gated else 0, code, out.data_ptr())
+    return out
+
+
+def gemm_mxfp4(Xq, x_scale, Wq, w_scale, gated=False, out_dtype=None, out=None, stream=None):
+    """The one-group case of grouped_gemm_mxfp4: Wq [N, K/2], w_scale
+    [ceil(K/256), N, 8]."""
+    M, N, K, code, out = _mx_operands(Xq, x_scale, Wq, w_scale, 2, None, gated, out_dtype, out, stream)
+    _call("gemm_mxfp4", stream, (Xq, x_scale, Wq, w_scale, out), Xq.data_ptr(), x_scale.data_ptr(), Wq.data_ptr(),
+          w_scale.data_ptr(), M, N, K, 1 if gated else 0, code, out.data_ptr())
+    return out
+
+
+def moe_ffn_mxfp4(X, logits, W1q, w1_scale, W2q, w2_scale, k, scoring=None, out=None, workspace=None, stream=None):
+    """moe_ffn_int8's block on 4-bit weights in one call: the selection (by
+    `scoring`, or moe_route's with renormalised weights), quantize_mxfp4 of X
+    [T, H] (BF16), the gated product with W1q [E, 2I, H/2] (FP32 result),
+    quantize_mxfp4 of it, the product with W2q [E, H, I/2] (BF16) and
+    moe_combine: [T, H] BF16.  `workspace`: a device tensor of at least
+    ffn_mxfp4_workspace_size bytes, or None for one allocated for this call."""
+    torch = _torch_module
+    _need(X, torch.bfloat16, "X", 2)
+    T, H = X.shape
+    _need(logits, torch.float32, "logits", 2)
+    E = logits.shape[1]
+    _need_shape(logits, torch.float32, (T, E), "logits")
+    K1, I = _mx_operand(W1q, w1_scale, 3, "W1q"), _mx_operand(W2q, w2_scale, 3, "W2q")
+    if K1 != H or W1q.shape[:2] != (E, 2 * I) or W2q.shape[:2] != (E, H):
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W1q {tuple(W1q.shape)}, W2q {tuple(W2q.shape)}, E={E}")
+    c = None if scoring is None else _scoring(scoring, E)
+    out = _out(out, torch.bfloat16, (T, H), X, stream)
+    if workspace is None:
+        workspace = _scratch(X, ffn_mxfp4_workspace_size(T, E, k, H, I), stream)
+    else:
+        _need_span(workspace)
+    _call("moe_ffn_mxfp4", stream, (X, logits, W1q, w1_scale, W2q, w2_scale, out, workspace,
+                                    None if scoring is None else scoring.bias), X.data_ptr(), logits.data_ptr(),
+          W1q.data_ptr(), w1_scale.data_ptr(), W2q.data_ptr(), w2_scale.data_ptr(), T, E, int(k), H, I, c, out.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+def ffn_mxfp4_workspace_size(T: int, E: int, k: int, H: int, I: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.moe_ffn_mxfp4_workspace_size(T, E, k, H, I, ctypes.byref(n)), "moe_ffn_mxfp4_workspace_size")
+    return n.value
+
+
+# ---- the gated activation kept in 8 bits -------------------------------------------
+
+KEPT_BLOCK = 128   # columns of a half that share a scale
+
+
+def _gate_rows(positions, weights, R):
+    torch = _torch_module
+    _need(positions, torch.int32, "positions", 2)
+    T, k = positions.shape
+    if R != T * k:
+        raise ValueError(f"{R} rows, positions {T} x {k}")
+    _need_shape(weights, torch.float32, (T, k), "weights")
+    return T, k
+
+
+def moe_gate_int8(GU, positions, weights, stream=None):
+    """The gated activation of grouped rows with their weights, and what its
+    gradient needs: GU [T*k, 2I] BF16 (gate, then up) to (h [T*k, I] BF16 =
+    weight * silu(gate) * up, codes int8 [T*k, 2I], scale FP32 [T*k,
+    2*ceil(I/128)], one for each 128 columns of a half).  positions and weights
+    [T, k] as moe_route gives them; a row of weight 0 gives zeros whatever it
+    holds.  The rows that the next product makes of h are added by moe_combine
+    without weights."""
+    torch = _torch_module
+    _need(GU, torch.bfloat16, "GU", 2)
+    R, N = GU.shape
+    if N % 2:
+        raise ValueError("GU needs a gate and an up half")
+    T, k = _gate_rows(positions, weights, R)
+    I = N // 2
+    h = _new((R, I), torch.bfloat16, GU, stream)
+    codes = _new((R, N), torch.int8, GU, stream)
+    scale = _new((R, 2 * -(-I // KEPT_BLOCK)), torch.float32, GU, stream)
+    _call("moe_gate_int8", stream, (GU, positions, weights), GU.data_ptr(), positions.data_ptr(), weights.data_ptr(), T, k, I,
+          h.data_ptr(), codes.data_ptr(), scale.data_ptr())
+    return h, codes, scale
+
+
+def moe_gate_int8_grad(dh, codes, scale, positions, weights, stream=None):
+    """From dh [T*k, I] BF16 and what moe_gate_int8 kept: (dGU [T*k, 2I] BF16,
+    h [T*k, I] BF16 again, dweights [T, k] FP32), the gradients at the values
+    that the codes stand for."""
+    torch = _torch_module
+    _need(dh, torch.bfloat16, "dh", 2)
+    R, I = dh.shape
+    T, k = _gate_rows(positions, weights, R)
+    _need_shape(codes, torch.int8, (R, 2 * I), "codes")
+    _need_shape(scale, torch.float32, (R, 2 * -(-I // KEPT_BLOCK)), "scale")
+    dGU = _new((R, 2 * I), torch.bfloat16, dh, stream)
+    h = _new((R, I), torch.bfloat16, dh, stream)
+    dweights = _new((T, k), torch.float32, dh, stream)
+    _call("moe_gate_int8_grad", stream, (dh, codes, scale, positions, weights), dh.data_ptr(), codes.data_ptr(),
+          scale.data_ptr(), positions.data_ptr(), weights.data_ptr(), T, k, I, dGU.data_ptr(), h.data_ptr(),
+          dweights.data_ptr())
+    return dGU, h, dweights
 
 
 if os.environ.get("DRGG_NO_ROUTES", "0") in ("", "0"):

@@ -1,5 +1,5 @@
-// internal.hpp -- declarations shared by the C ABI (api.cpp, api_moe.cpp) and
-// the kernel launchers (kernels.hip, moe.hip, int8.hip).  Not part of the
+// internal.hpp -- declarations shared by the C ABI (api.cpp, api_moe.cpp,
+// api_experts.cpp) and the kernel launchers (the .hip files).  Not part of the
 // public interface.
 #pragma once
 
@@ -134,6 +134,43 @@ struct Int8Args {
 // the longest reduction whose sum fits 32 bits for any codes: 131056 * 128^2 < 2^31
 constexpr int64_t kInt8MaxK = 131056;
 hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s);
+
+// ---- selection by scores (moe.hip), 4-bit products (mxfp4.hip), kept activations (gate.hip)
+
+// the scored selection; its workspace is moe_route's
+hipError_t launch_moe_route_scores(const float* logits, int64_t T, int32_t E, int32_t k, const drgg_scoring& scoring,
+                                   int32_t* experts, float* weights, int32_t* offsets, int32_t* positions,
+                                   int32_t* tokens, void* table, hipStream_t s);
+hipError_t launch_moe_route_scores_grad(const float* dweights, const float* logits, const int32_t* experts,
+                                        const float* weights, int64_t T, int32_t E, int32_t k,
+                                        const drgg_scoring& scoring, float* dlogits, hipStream_t s);
+
+hipError_t launch_quantize_mxfp4(const void* X, bool bf16, int64_t T, int64_t K, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t s);
+hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t T, int64_t K, bool bf16,
+                                   void* X, hipStream_t s);
+
+// Arguments of the 4-bit products: X [M,K/2], W [E,N,K/2] codes, xs, ws scale
+// bytes [ceil(K/256)][M], [E*N] rows of 8; the rest as in Int8Args.
+struct MxArgs {
+    const uint8_t* X;
+    const uint8_t* W;
+    const uint8_t* xs;
+    const uint8_t* ws;
+    const int32_t* offs;
+    void* out;
+    int64_t M, N, K;
+    int32_t E;
+    const int32_t* rows = nullptr;   // row r of the product is row rows[r] of X and xs, T rows (null: row r)
+    int64_t T = 0;
+};
+hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, hipStream_t s);
+
+hipError_t launch_moe_gate_int8(const void* GU, const int32_t* positions, const float* weights, int64_t T, int32_t k,
+                                int64_t I, void* h, int8_t* codes, float* scale, hipStream_t s);
+hipError_t launch_moe_gate_int8_grad(const void* dh, const int8_t* codes, const float* scale, const int32_t* positions,
+                                     const float* weights, int64_t T, int32_t k, int64_t I, void* dGU, void* h,
+                                     float* dweights, hipStream_t s);
 
 // Per-launch timing marks (a measurement knob, off by default): when on, an
 // event is recorded on the stream before every kernel launch of a call and

@@ -259,6 +259,395 @@ __global__ __launch_bounds__(kRouteThreads) void moe_select_quantize_kernel(Rout
                                   blockIdx.x - a.blocks, gridDim.x - a.blocks);
 }
 
+// ---------------------------------------------------------------------------
+// selection by scores
+//
+// The same rounds on keys of v = s + bias, s the sigmoid or softmax score.  A
+// choice is that of 64-bit values: FP32 values are off by at most `off` (see
+// below), so where two that decide something -- neighbours among the chosen,
+// the last chosen and the best left, the last kept group and the best left --
+// are no further apart than both errors, the token is chosen again from values
+// in 64 bits, by its whole wave.
+
+struct ScoreArgs {
+    const float* bias;
+    int32_t groups, top_groups, best;
+    int32_t by_logits;   // no bias, one group: the order is that of the logits
+    float scale;
+};
+
+// The largest key of the row of lanes.  Four running values (a wave alone on
+// its SIMD waits for every dependent result; a tree would hold V/2 more).
+template <int V>
+__device__ __forceinline__ uint32_t best_key(const uint32_t (&key)[V]) {
+    uint32_t m[4] = {key[0], key[1], key[2], key[3]};
+#pragma unroll
+    for (int i = 4; i < V; ++i) m[i & 3] = max(m[i & 3], key[i]);
+    return row_max(max(max(m[0], m[1]), max(m[2], m[3])));
+}
+// the lowest expert with it, whose key becomes 0
+template <int V>
+__device__ __forceinline__ uint32_t take_best(uint32_t (&key)[V], int l, uint32_t* best) {
+    *best = best_key<V>(key);
+    uint32_t is[4] = {0xFFFFu, 0xFFFFu, 0xFFFFu, 0xFFFFu};
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) is[i & 3] = key[i] == *best ? (uint32_t)(64 * (i >> 2) + (i & 3)) : is[i & 3];
+    const uint32_t e = row_min(min(min(is[0], is[1]), min(is[2], is[3])) + 4 * l);   // above every index where there is none
+    const uint32_t mine_at = e - 4 * l;          // the taken key's place, if it is this lane's
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = mine_at == (uint32_t)(64 * (i >> 2) + (i & 3)) ? 0u : key[i];
+    return e;
+}
+
+constexpr float kUnit = 0x1p-24f;   // half a step of FP32, relative
+
+// the score of a logit; most and total: the softmax's (most finite)
+template <bool SIGMOID, class F>
+__device__ __forceinline__ F score(float x, F most, F total) {
+    if constexpr (SIGMOID) {
+        const F e = exp(-fabs((F)x)), q = 1 / (1 + e);
+        return x < 0 ? e * q : q;   // NaN: q
+    } else {
+        return exp((F)x - most) / total;
+    }
+}
+// v; every part is computed and then chosen from (a branch per expert costs
+// more than the exponential)
+template <bool SIGMOID, class F>
+__device__ __forceinline__ F score_value(float x, float bias, F most, F total) {
+    const F v = score<SIGMOID, F>(x, most, total) + (F)bias;
+    return ((x == -INFINITY) | (bias == -INFINITY)) ? (F)-INFINITY : v;
+}
+
+__device__ __forceinline__ uint64_t order_key64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0), key = u >> 63 ? ~u : u | 1ull << 63;
+    return v != v ? ~0ull : key;
+}
+__device__ __forceinline__ double key_value64(uint64_t k) {
+    return __builtin_bit_cast(double, k >> 63 ? k & ~(1ull << 63) : ~k);   // NaN: all ones, a NaN
+}
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const uint64_t o = __shfl_xor((unsigned long long)v, m, 64);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// The largest of a wave's N*64 keys (lane l's i-th is expert 64 i + l), which
+// becomes 0, and its lowest expert.
+template <int N>
+__device__ __forceinline__ uint64_t take_best64(uint64_t (&key)[N], int* expert) {
+    uint64_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = key[i] > m ? key[i] : m;
+    m = wave_max64(m);
+    int at = -1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const unsigned long long has = __ballot(key[i] == m);
+        if (at < 0 && has) at = 64 * i + __ffsll((long long)has) - 1;
+    }
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (at == 64 * i + lane) key[i] = 0;
+    *expert = at;
+    return m;
+}
+
+// Token t's choice from values in 64 bits, by one wave; chosen(j, e) for each round.
+template <int N, bool SIGMOID, class Chosen>
+__device__ __forceinline__ void choose64(const RouteArgs& a, const ScoreArgs& c, const float* bias, int64_t t, Chosen chosen) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    float x[N], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = 64 * i + lane < a.E ? a.logits[t * a.E + 64 * i + lane] : -INFINITY;
+        top = fmaxf(top, x[i]);
+    }
+    double most = 0, total = 1;
+    if constexpr (!SIGMOID) {
+        for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+        most = top == -INFINITY ? 0.0 : (double)top;
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            total += exp((double)x[i] - most);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m, 64);
+    }
+    uint64_t key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = 64 * i + lane;
+        const float b = bias[e < a.E ? e : 0];
+        key[i] = e >= a.E ? 0 : order_key64(score_value<SIGMOID, double>(x[i], b, most, total));
+        __builtin_amdgcn_sched_barrier(0);   // one at a time: sixteen exponentials side by side do not fit the registers
+    }
+    if (c.groups > 1) {
+        const int size = a.E / c.groups;
+        uint64_t rank = 0;   // lane g: the value of group g
+        for (int g = 0; g < c.groups; ++g) {
+            uint64_t in[N];
+            int at;
+#pragma unroll
+            for (int i = 0; i < N; ++i) in[i] = (unsigned)(64 * i + lane - g * size) < (unsigned)size ? key[i] : 0;
+            uint64_t v = take_best64<N>(in, &at);
+            if (c.best == 2 && size > 1) {
+                const double one = key_value64(v), two = key_value64(take_best64<N>(in, &at));
+                if (two != -INFINITY) v = order_key64(one + two);
+            }
+            if (lane == g) rank = v;
+        }
+        int ahead = 0;   // groups before this lane's
+        for (int g = 0; g < c.groups; ++g) {
+            const uint64_t v = __shfl((unsigned long long)rank, g, 64);
+            ahead += v > rank || (v == rank && g < lane);
+        }
+        const unsigned long long open = __ballot(lane < c.groups && ahead < c.top_groups);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = 64 * i + lane;
+            if (e < a.E && !(open >> (e / size) & 1)) key[i] = 0;
+        }
+    }
+    for (int j = 0; j < a.k; ++j) {
+        int e;
+        take_best64<N>(key, &e);
+        chosen(j, e);
+    }
+}
+
+// One token of the block (number tl of its 64) per row of lanes.  `far`: the
+// largest finite |bias|.
+template <int V, int S, bool SIGMOID>
+__device__ __forceinline__ void select_by_scores(const RouteArgs& a, const ScoreArgs& c, const float* bias, float far,
+                                                 unsigned long long* mask, int tl) {
+    // opaque: what depends on the lane alone would otherwise be hoisted out of
+    // the loop over the block's tokens and held in registers
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int l = lane & 15;
+    const int E = a.E, k = a.k;
+    const int64_t t = (int64_t)blockIdx.x * kRouteTokens + tl;
+    const bool live = t < a.T;
+    const float* row = a.logits + t * E;
+    uint32_t key[V];
+    load_keys<V>(key, row, E, l, live);
+    // the softmax's maximum and sum
+    float most = 0.f, total = 1.f;
+    if constexpr (!SIGMOID) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = max(m, key[i]);
+        most = key_value(row_max(m));   // NaN if there is one
+        if (most == -INFINITY) most = 0.f;
+        total = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) total += key[i] ? expf(key_value(key[i]) - most) : 0.f;
+        total = row_sum(total);
+    }
+    // An FP32 value's error, with half steps u: a sigmoid's exponential is
+    // within 2 u of itself and two roundings follow, 2.5 u in all; a softmax
+    // score p has u |x - most| p <= 0.37 u from its exponent and at most
+    // (V + 16) u p from the exponential, the sum and the division; the bias adds
+    // a rounding, u |v|.
+    const float off = SIGMOID ? 2.5f * kUnit : (1.f + (V + 16) / total) * kUnit;
+    bool close = false;
+    auto near = [&](uint32_t hi, uint32_t lo, float within) {
+        const float h = key_value(hi), d = h - key_value(lo);   // infinity or NaN unless both are finite
+        return fabsf(h) < INFINITY && d <= within;
+    };
+    unsigned long long open = ~0ull;
+    if (c.groups > 1) {
+        // sixteen lanes take the groups in turn
+        const int size = E / c.groups;
+        uint32_t rank[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int g = 16 * q + l;
+            rank[q] = 0;
+            if (live && g < c.groups) {
+                uint32_t one = 0, two = 0;
+                for (int e = g * size; e < (g + 1) * size; ++e) {
+                    const float x = row[e], b = bias[e];
+                    const uint32_t v = order_key(score_value<SIGMOID, float>(x, b, most, total));
+                    two = max(two, min(one, v));
+                    one = max(one, v);
+                }
+                rank[q] = c.best == 2 && two != 0 && key_value(two) != -INFINITY ? order_key(key_value(one) + key_value(two)) : one;
+            }
+        }
+        const float within = (4.f * off + 8.f * kUnit * (1.f + far)) * 1.01f;
+        open = 0;
+        uint32_t last = 0;
+        for (int j = 0; j < c.top_groups; ++j) {
+            last = row_max(max(max(rank[0], rank[1]), max(rank[2], rank[3])));
+            uint32_t at = 64;
+#pragma unroll
+            for (int q = 3; q >= 0; --q) at = rank[q] == last ? (uint32_t)(16 * q + l) : at;
+            at = row_min(at);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) rank[q] = at == (uint32_t)(16 * q + l) ? 0u : rank[q];
+            open |= 1ull << (at & 63);
+        }
+        const uint32_t left = row_max(max(max(rank[0], rank[1]), max(rank[2], rank[3])));
+        close = left != 0 && near(last, left, within);
+    }
+    // e / size for e < 1024 by a multiplication
+    const uint32_t by_size = c.groups > 1 ? ((1u << 20) + E / c.groups - 1) / (E / c.groups) : 0u;
+    if (!c.by_logits) {   // in place, four experts at a time
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+            const f32x4 b = *reinterpret_cast<const f32x4*>(&bias[64 * q + 4 * l]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t e = 64 * q + 4 * l + i;
+                const float x = key_value(key[4 * q + i]);
+                const uint32_t v = order_key(score_value<SIGMOID, float>(x, b[i], most, total));
+                const bool in = key[4 * q + i] != 0 && (c.groups == 1 || (open >> ((e * by_size) >> 20 & 63) & 1));
+                key[4 * q + i] = in ? v : 0u;
+            }
+            if constexpr (V > 16) __builtin_amdgcn_sched_barrier(0);   // side by side they do not fit the registers
+        }
+    }
+    int32_t mine[S];
+    // a wave without tokens does not compete with the others
+    const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens + __builtin_amdgcn_readfirstlane(tl);   // the wave's first
+    const int rounds = t0 < a.T ? k : 0;
+    uint32_t last = 0;
+    for (int j = 0; j <= rounds; ++j) {
+        if (j == rounds && (rounds == 0 || c.by_logits)) break;
+        uint32_t best, e = 0;
+        if (j < rounds) e = take_best<V>(key, l, &best);
+        else best = best_key<V>(key);
+        if (!c.by_logits && j > 0 && best != 0) close |= near(last, best, (2.f * off + 2.f * kUnit * fabsf(key_value(last))) * 1.01f);
+        last = best;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (j == 16 * s + l && j < rounds) mine[s] = (int32_t)e;
+    }
+    // the tokens of this wave that FP32 does not decide
+    unsigned long long undecided = __ballot(close && live);
+    while (undecided) {
+        const int at = __ffsll((long long)undecided) - 1;   // a lane of the token's row
+        undecided &= ~(0xFFFFull << (at & ~15));
+        choose64<V / 4, SIGMOID>(a, c, bias, t0 + (at >> 4), [&](int j, int e) {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (lane >> 4 == at >> 4 && j == 16 * s + l) mine[s] = e;
+        });
+    }
+    // Weights.  Renormalised sigmoids are taken relative to the largest
+    // exp(min(x, 0)) among the chosen: the same ratio, also where every score is
+    // below FP32's range.
+    float x[S], p[S], m = -INFINITY, sum = 0.f;
+    bool in[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const bool has = live && 16 * s + l < k;
+        x[s] = has ? row[mine[s]] : -INFINITY;
+        in[s] = has && x[s] != -INFINITY && bias[has ? mine[s] : 0] != -INFINITY;
+        if (in[s]) m = fmaxf(m, SIGMOID ? fminf(x[s], 0.f) : x[s]);   // a NaN is passed over here and comes back below
+    }
+    if (a.renormalize) {
+        m = key_value(row_max(order_key(m)));
+        if (m == -INFINITY) m = 0.f;   // none but masked experts (or NaN)
+    } else {
+        m = SIGMOID ? 0.f : most;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const float shared = expf(fminf(x[s], 0.f) - m) / (1.f + expf(-fabsf(x[s])));
+        const float e = !SIGMOID ? expf(x[s] - m) : x[s] != x[s] ? x[s] : shared;
+        p[s] = in[s] ? e : 0.f;
+        sum += p[s];
+    }
+    sum = a.renormalize ? row_sum(sum) : SIGMOID ? 1.f : total;
+    if (!SIGMOID && total != total) sum = total;
+    if (live) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int j = 16 * s + l;
+            if (j < k) {
+                a.experts[t * k + j] = mine[s];
+                a.weights[t * k + j] = in[s] ? c.scale * (p[s] / sum) : 0.f;
+                atomicOr(&mask[mine[s]], 1ull << tl);
+            }
+        }
+    }
+}
+
+// The block of 64 tokens, THREADS / 16 at a time, then their pairs' ranks and the
+// counts as moe_select_kernel leaves them.  More than 256 experts take 512 or
+// 256 threads: with 1024 a lane has 128 registers, which 32 or 64 keys do not
+// fit beside the rest.
+template <int V, int S, int THREADS, bool SIGMOID>
+__global__ __launch_bounds__(THREADS) void moe_select_scores_kernel(RouteArgs a, ScoreArgs c) {
+    __shared__ unsigned long long mask[16 * V];
+    __shared__ int32_t start[16 * V], tmp[THREADS / 64];
+    __shared__ __attribute__((aligned(16))) float bias[16 * V];
+    __shared__ float widest[THREADS / 64];
+    const int E = a.E, k = a.k, tid = threadIdx.x, l = tid & 15;
+    float far = 0.f;
+    for (int e = tid; e < 16 * V; e += THREADS) {
+        const float b = c.bias && e < E ? c.bias[e] : 0.f;
+        bias[e] = b;
+        if (fabsf(b) < INFINITY) far = fmaxf(far, fabsf(b));
+        mask[e] = 0;
+    }
+    for (int m = 1; m < 64; m <<= 1) far = fmaxf(far, __shfl_xor(far, m, 64));
+    if ((tid & 63) == 0) widest[tid >> 6] = far;
+    __syncthreads();
+    for (int w = 0; w < THREADS / 64; ++w) far = fmaxf(far, widest[w]);
+    for (int tl = tid >> 4; tl < kRouteTokens; tl += THREADS / 16) select_by_scores<V, S, SIGMOID>(a, c, bias, far, mask, tl);
+    __syncthreads();
+    const bool single = a.blocks == 1;
+    if (single) {
+        // threads hold neighbouring experts, so that their sums are in order
+        constexpr int kPer = 16 * V > THREADS ? 16 * V / THREADS : 1;
+        int32_t n[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            n[i] = kPer * tid + i < E ? __popcll(mask[kPer * tid + i]) : 0;
+            sum += n[i];
+        }
+        int32_t at = block_prefix(sum, tmp);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = kPer * tid + i;
+            if (e < E) start[e] = a.offsets[e] = at;
+            at += n[i];
+            if (e == E - 1) a.offsets[E] = at;
+        }
+        __syncthreads();
+    } else if (a.blocks <= kRouteBytes) {
+        const int stride = table_stride(E);
+        for (int e = tid; e < stride; e += THREADS)
+            static_cast<uint8_t*>(a.table)[(int64_t)blockIdx.x * stride + e] = e < E ? (uint8_t)__popcll(mask[e]) : 0;
+    } else {
+        for (int e = tid; e < E; e += THREADS)
+            static_cast<int32_t*>(a.table)[(int64_t)blockIdx.x * E + e] = __popcll(mask[e]);
+    }
+    for (int tl = tid >> 4; tl < kRouteTokens; tl += THREADS / 16) {
+        const int64_t t = (int64_t)blockIdx.x * kRouteTokens + tl;
+        if (t >= a.T) break;
+        for (int j = l; j < k; j += 16) {
+            const int32_t e = a.experts[t * k + j];   // this thread's own store
+            int32_t r = __popcll(mask[e] & ((1ull << tl) - 1));
+            if (single) {
+                r += start[e];
+                if (a.tokens) a.tokens[r] = (int32_t)t;
+            }
+            a.positions[t * k + j] = r;
+        }
+    }
+}
+
 // More than kRouteBytes blocks: the table's columns to exclusive prefixes over
 // the blocks, and each expert's total after them.  One lane per expert; the
 // 16 waves of a workgroup each take a run of blocks, sum it, and write its
@@ -421,6 +810,71 @@ __global__ __launch_bounds__(256) void moe_route_grad_kernel(RouteGradArgs a) {
             const int32_t e = a.experts[t * k + j];
             const float w = a.weights[t * k + j];
             if (e >= 0 && e < E) out[e] = w != 0.f ? w * (a.dweights[t * k + j] - s) : 0.f;
+        }
+}
+
+// The same for weights from scores: with r = sum_j w_j dw_j / scale,
+//   sigmoid:  w_j (1 - s_j) (dw_j - r), without the r where the weights are not
+//             renormalised;  1 - s = sigmoid(-x)
+//   softmax:  as above, with r for s
+template <int V>
+__global__ __launch_bounds__(256) void moe_route_scores_grad_kernel(RouteGradArgs a, int sigmoid, float scale) {
+    const int l = threadIdx.x & 15;
+    const int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int E = a.E, k = a.k;
+    const bool live = t < a.T;
+    float r = 0.f;
+    if (live && !(sigmoid && !a.renormalize))
+        for (int j = l; j < k; j += 16) {
+            const float w = a.weights[t * k + j];
+            r += w != 0.f ? w * a.dweights[t * k + j] : 0.f;
+        }
+    r = row_sum(r);
+    float g[V];
+    if (a.renormalize || sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = 0.f;
+    } else {
+        uint32_t key[V], m = 0;
+        load_keys<V>(key, a.logits + t * E, E, l, live);
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = max(m, key[i]);
+        const float most = key_value(row_max(m));
+        const bool none = most == -INFINITY;
+        float total = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            g[i] = key[i] && !none ? expf(key_value(key[i]) - most) : 0.f;
+            total += g[i];
+        }
+        total = row_sum(total);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = g[i] == 0.f ? 0.f : -r * (g[i] / total);
+    }
+    r /= scale;
+    float* out = a.dlogits + t * E;
+    if (live) {
+#pragma unroll
+        for (int c = 0; c < V / 4; ++c) {
+            const int e = 64 * c + 4 * l;
+            if ((E & 3) == 0) {
+                if (e < E) *reinterpret_cast<f32x4*>(out + e) = f32x4{g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (e + i < E) out[e + i] = g[4 * c + i];
+            }
+        }
+    }
+    __syncthreads();   // the row's stores are performed before the ones below
+    if (live)
+        for (int j = l; j < k; j += 16) {
+            const int32_t e = a.experts[t * k + j];
+            const float w = a.weights[t * k + j];
+            if (e >= 0 && e < E && w != 0.f) {   // of weight 0: as if not chosen
+                const float by = sigmoid ? score<true, float>(-a.logits[t * E + e], 0.f, 1.f) : 1.f;
+                out[e] = w * by * (a.dweights[t * k + j] - r);
+            }
         }
 }
 
@@ -638,6 +1092,22 @@ size_t route_table_bytes(int64_t T, int32_t E) {
     return (size_t)(n <= kRouteBytes ? n * round_up(E, 4) : (n + 1) * E * 4);
 }
 
+// the places of the pairs, where the selection took more than one block
+static hipError_t finish_route(const RouteArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)a.blocks), block(kRouteThreads);
+    if (a.blocks > kRouteBytes) {
+        timing_mark("moe_scan_kernel", s);
+        hipLaunchKernelGGL(moe_scan_kernel, dim3((unsigned)ceil_div(a.E, 64)), block, 0, s, a);
+    }
+    if (a.blocks > 1) {
+        timing_mark("moe_place_kernel", s);
+        if (a.blocks > kRouteBytes) hipLaunchKernelGGL(moe_place_kernel<false>, grid, block, 0, s, a);
+        else hipLaunchKernelGGL(moe_place_kernel<true>, grid, block, 0, s, a);
+    }
+    timing_end(s);
+    return hipGetLastError();
+}
+
 hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k, int renormalize, int32_t* experts,
                             float* weights, int32_t* offsets, int32_t* positions, int32_t* tokens, void* table,
                             hipStream_t s, const QuantArgs* quantize) {
@@ -661,15 +1131,40 @@ hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k
             else hipLaunchKernelGGL((moe_select_kernel<V, 4>), grid, block, 0, s, a);
         });
     }
-    if (a.blocks > kRouteBytes) {
-        timing_mark("moe_scan_kernel", s);
-        hipLaunchKernelGGL(moe_scan_kernel, dim3((unsigned)ceil_div(E, 64)), block, 0, s, a);
-    }
-    if (a.blocks > 1) {
-        timing_mark("moe_place_kernel", s);
-        if (a.blocks > kRouteBytes) hipLaunchKernelGGL(moe_place_kernel<false>, grid, block, 0, s, a);
-        else hipLaunchKernelGGL(moe_place_kernel<true>, grid, block, 0, s, a);
-    }
+    return finish_route(a, s);
+}
+
+hipError_t launch_moe_route_scores(const float* logits, int64_t T, int32_t E, int32_t k, const drgg_scoring& c,
+                                   int32_t* experts, float* weights, int32_t* offsets, int32_t* positions,
+                                   int32_t* tokens, void* table, hipStream_t s) {
+    RouteArgs a{logits, experts, weights, offsets, positions, tokens, table, T, route_blocks(T), E, k, c.renormalize != 0};
+    const ScoreArgs sc{c.bias, c.groups, c.top_groups, c.best, !c.bias && c.groups == 1, c.scale};
+    timing_mark("moe_select_scores_kernel", s);
+    for_experts(E, [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        constexpr int kThreads = V <= 16 ? 1024 : V == 32 ? 512 : 256;
+        const dim3 grid((unsigned)a.blocks), block(kThreads);
+        if (c.score == DRGG_SCORE_SIGMOID) {
+            if (k <= 16) hipLaunchKernelGGL((moe_select_scores_kernel<V, 1, kThreads, true>), grid, block, 0, s, a, sc);
+            else hipLaunchKernelGGL((moe_select_scores_kernel<V, 4, kThreads, true>), grid, block, 0, s, a, sc);
+        } else {
+            if (k <= 16) hipLaunchKernelGGL((moe_select_scores_kernel<V, 1, kThreads, false>), grid, block, 0, s, a, sc);
+            else hipLaunchKernelGGL((moe_select_scores_kernel<V, 4, kThreads, false>), grid, block, 0, s, a, sc);
+        }
+    });
+    return finish_route(a, s);
+}
+
+hipError_t launch_moe_route_scores_grad(const float* dweights, const float* logits, const int32_t* experts,
+                                        const float* weights, int64_t T, int32_t E, int32_t k, const drgg_scoring& c,
+                                        float* dlogits, hipStream_t s) {
+    RouteGradArgs a{dweights, logits, experts, weights, dlogits, T, E, k, c.renormalize != 0};
+    const dim3 grid((unsigned)ceil_div(T, 16)), block(256);
+    timing_mark("moe_route_scores_grad_kernel", s);
+    for_experts(E, [&](auto v) {
+        hipLaunchKernelGGL(moe_route_scores_grad_kernel<decltype(v)::value>, grid, block, 0, s, a,
+                           (int)(c.score == DRGG_SCORE_SIGMOID), c.scale);
+    });
     timing_end(s);
     return hipGetLastError();
 }

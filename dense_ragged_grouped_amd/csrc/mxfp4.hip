@@ -1,0 +1,342 @@
+// mxfp4.hip -- gfx950 (CDNA4) kernels of microscaled 4-bit floating point:
+// blocks of 32 values along a row with a scale 2^(b - 127), elements of two
+// exponent bits and one mantissa bit.
+//
+//   quantisation   b = floor(log2 max|x|) + 125,  code = nearest(x / 2^(b - 127))
+//   product        Y[t,n] = sum over blocks of 2^(bx + bw - 254) <x, w>
+//   gated product  Y[t,i] = silu(g) u,  g, u = columns i and N/2 + i of the product
+//
+// Codes are rows of K/2 bytes; the scale bytes of 256 columns (one line of 128
+// code bytes) stand side by side, [ceil(K/256)][rows][8], so that the scales a
+// tile needs are runs of memory and no row's scales are unaligned.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "engine.hpp"
+#include "internal.hpp"
+#include "plan.hpp"
+#include "products.hpp"
+
+namespace drgg {
+
+namespace {
+
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------------------------
+// quantisation
+//
+// Half a wave per row and 256 columns: lane l has columns 8l .. 8l+7, four
+// lanes a block of 32.  The maxima are two rotations within quads; the codes
+// leave as one dword per lane, the scales of 128 columns as one dword of the
+// row of 16 lanes that holds them.
+
+// v of lane l ^ 1, l ^ 2
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+}
+// or over the row of 16 of values that agree within each quad
+__device__ __forceinline__ uint32_t or_quads(uint32_t v) {
+    v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false);
+    return v | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false);
+}
+
+// The scale byte for a largest magnitude given as bits: its exponent field
+// less 2 (the largest code is 1.5 * 2^2), 255 for infinity and NaN.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t most) {
+    const int e = (int)(most >> 23);
+    return e == 255 ? 255u : e > 2 ? (uint32_t)(e - 2) : 0u;
+}
+// 2^(127 - b), by which the values are multiplied, for a finite block (b is at
+// most 252).  Exact; a result below FP32's normal range is far below half the
+// smallest code.
+__device__ __forceinline__ float scale_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+// eight codes, the first in the lowest bits.  The conversion rounds to the
+// nearest code, ties to even, and limits to 6.
+__device__ __forceinline__ uint32_t codes8(const float (&y)[8]) {
+    uint32_t q = 0;
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, y[0], y[1], 1.f, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, y[2], y[3], 1.f, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, y[4], y[5], 1.f, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, y[6], y[7], 1.f, 3);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(float (&f)[8], const void* X, int64_t i) {
+    if constexpr (BF16) {
+        const u32x4 v = reinterpret_cast<const u32x4*>(X)[i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            f[2 * r] = __uint_as_float(v[r] << 16);
+            f[2 * r + 1] = __uint_as_float(v[r] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 v = reinterpret_cast<const f32x4*>(X)[2 * i + h];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[4 * h + r] = v[r];
+        }
+    }
+}
+
+struct MxRowArgs {
+    const void* X;      // quantisation: values; dequantisation: codes
+    const uint8_t* in_scales;
+    void* out;          // codes; values
+    uint8_t* scales;
+    int64_t T, K;
+};
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(MxRowArgs a) {
+    const int l = threadIdx.x & 31;
+    const int64_t kb = blockIdx.y, c = 256 * kb + 8 * l;
+    // every lane of a wave takes part in the exchanges
+    for (int64_t t0 = (int64_t)blockIdx.x * 8; t0 < a.T; t0 += (int64_t)gridDim.x * 8) {
+        const int64_t t = t0 + (threadIdx.x >> 5);
+        const bool live = t < a.T && c < a.K;
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live) load8<BF16>(f, a.X, (t * a.K + c) / 8);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+        const uint32_t b = scale_byte(quad_max(m));
+        const float by = scale_inverse(b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = b == 255 ? 0.f : f[i] * by;
+        if (live) static_cast<uint32_t*>(a.out)[(t * a.K + c) / 8] = codes8(f);
+        const uint32_t four = or_quads(live ? b << (8 * ((l >> 2) & 3)) : 0u);
+        if ((l & 15) == 0 && t < a.T) reinterpret_cast<uint32_t*>(a.scales)[(kb * a.T + t) * 2 + (l >> 4)] = four;
+    }
+}
+
+// The values of eight codes: converted with scale 1 and moved by the block's
+// exponent, so that 2^-127, which is below FP32's normal range, needs no care.
+template <bool BF16>
+__global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(MxRowArgs a) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const int l = threadIdx.x & 31;
+    const int64_t kb = blockIdx.y, c = 256 * kb + 8 * l;
+    if (c >= a.K) return;
+    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * 8) {
+        const uint32_t q = static_cast<const uint32_t*>(a.X)[(t * a.K + c) / 8];
+        const int b = a.in_scales[(kb * a.T + t) * 8 + (l >> 2)];
+        const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0);
+        const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
+        const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2);
+        const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
+        float f[8] = {p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = b == 255 ? __uint_as_float(0x7FC00000u) : ldexpf(f[i], b - 127);
+        if constexpr (BF16) {
+            static_cast<u32x4*>(a.out)[(t * a.K + c) / 8] =
+                u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+        } else {
+            f32x4* out = static_cast<f32x4*>(a.out) + (t * a.K + c) / 4;
+            out[0] = f32x4{f[0], f[1], f[2], f[3]};
+            out[1] = f32x4{f[4], f[5], f[6], f[7]};
+        }
+    }
+}
+
+dim3 mx_row_grid(int64_t T, int64_t K) {
+    // a launch has fewer than 2^32 threads: blocks walk the rows beyond
+    const int64_t kb = ceil_div(K, 256), n = ceil_div(T, 8), most = (int64_t(1) << 23) / kb;
+    return dim3((unsigned)(n < most ? n : most), (unsigned)kb);
+}
+
+// ---------------------------------------------------------------------------
+// product, few rows per group
+//
+// The work items of the 8-bit few-row program (products.hpp): a workgroup
+// computes a block of 16*NB weight rows (gated: 8*NB gate rows and their up
+// rows) and up to TOK tokens of one group; its W waves split K in pieces of 256
+// columns (one line of a row's codes, eight scale bytes), each computing the
+// whole block, and add their sums through LDS in the waves' order.  Fragments
+// go from memory to registers directly: lane l of a
+// v_mfma_scale_f32_16x16x128_f8f6f4 holds the block of 32 columns 32*(l/16) ..
+// +31 of row l%16, one 16-byte load, and that block's scale byte; the result
+// has token l%16 and weight rows 4*(l/16) .. +3 in lane l.  The lane's byte
+// of a dword of four scales is shifted down (one vector instruction beside a
+// 16-byte load).  Rows and columns outside the operands carry an out-of-range
+// offset and read as zero, and so do their scales (a scale byte of 255 would
+// make the zeros NaN).
+
+__device__ __forceinline__ i32x8 fragment(u32x4 v) {   // 4-bit elements fill half of the operand's registers
+    const i32x4 a = __builtin_bit_cast(i32x4, v);
+    return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+
+template <bool OUT_BF16, bool GATED, bool GATHERED, int NB, int MB, int W, int U>
+__device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& it, f32x4 (&sums)[W][NB][64]) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int64_t NO = GATED ? a.N / 2 : a.N;
+    constexpr int NC = GATED ? NB / 2 : NB;          // blocks of 16 output columns
+    const int64_t n0 = (int64_t)it.nt * 16 * NC;
+    const int B = (int)(a.K / 2);                    // bytes per row
+    const auto rx = make_rsrc(GATHERED ? a.X : a.X + it.m0 * B);
+    const uint8_t* w0 = a.W + ((int64_t)it.e * a.N + n0) * B;
+    const auto rw = make_rsrc(w0);
+    const auto rw2 = make_rsrc(GATED ? w0 + NO * B : w0);
+    // a row's byte offset, bytes it has from this lane's 16 on, and its scales' offset
+    int off[4], xoff[MB], xk[MB], wk[NC], xs[MB];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) off[b] = (16 * b + r) * B + 16 * g;
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        const bool ok = it.m0 + 16 * b + r < it.hi;
+        xoff[b] = off[b];
+        xk[b] = ok ? B - 16 * g : 0;
+        xs[b] = (16 * b + r) * 8;
+        if constexpr (GATHERED) {   // T * B < 2^31
+            const int32_t from = ok ? a.rows[it.m0 + 16 * b + r] : -1;
+            if ((uint32_t)from < (uint32_t)a.T) {
+                xoff[b] = from * B + 16 * g;
+                xs[b] = from * 8;
+            } else {
+                xk[b] = 0;
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < NC; ++b) wk[b] = n0 + 16 * b + r < NO ? B - 16 * g : 0;
+    const int64_t xrows = GATHERED ? a.T : a.M, wrows = (int64_t)a.E * a.N;
+    const uint8_t* xs0 = a.xs + (GATHERED ? 0 : it.m0 * 8);
+    const uint8_t* ws0 = a.ws + ((int64_t)it.e * a.N + n0) * 8;
+    f32x4 acc[NB][MB] = {};
+    for (int k0 = wave * 128; k0 < B; k0 += 128 * W * U) {
+        u32x4 fx[U][2][MB], fw[U][2][NB];
+        uint32_t sx[U][2][MB], sw[U][2][NB];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + 128 * W * u;
+            const auto rxs = make_rsrc(xs0 + (int64_t)(k >> 7) * xrows * 8);
+            const uint8_t* wsk = ws0 + (int64_t)(k >> 7) * wrows * 8;
+            const auto rws = make_rsrc(wsk), rws2 = make_rsrc(GATED ? wsk + NO * 8 : wsk);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const bool in = k + 64 * s < wk[b % NC];
+                    fw[u][s][b] = __builtin_amdgcn_raw_buffer_load_b128(b < NC ? rw : rw2,
+                                                                        in ? (uint32_t)(off[b % NC] + k + 64 * s) : kOOB, 0, 0);
+                    sw[u][s][b] = __builtin_amdgcn_raw_buffer_load_b32(
+                        b < NC ? rws : rws2, in ? (uint32_t)((16 * (b % NC) + r) * 8 + 4 * s) : kOOB, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const bool in = k + 64 * s < xk[b];
+                    fx[u][s][b] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? (uint32_t)(xoff[b] + k + 64 * s) : kOOB, 0, 0);
+                    sx[u][s][b] = __builtin_amdgcn_raw_buffer_load_b32(rxs, in ? (uint32_t)(xs[b] + 4 * s) : kOOB, 0, 0);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        acc[b][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            fragment(fw[u][s][b]), fragment(fx[u][s][m]), acc[b][m], 4, 4, 0, sw[u][s][b] >> (8 * g), 0,
+                            sx[u][s][m] >> (8 * g));
+    }
+    // the waves' sums, one block of 16 tokens at a time
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+        if (m > 0) __syncthreads();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[b][m];
+        __syncthreads();
+        if (wave >= NC) continue;
+        f32x4 c0 = sums[0][wave][lane], c1 = c0;
+        if constexpr (GATED) c1 = sums[0][NC + wave][lane];
+#pragma unroll
+        for (int v = 1; v < W; ++v) {
+            c0 += sums[v][wave][lane];
+            if constexpr (GATED) c1 += sums[v][NC + wave][lane];
+        }
+        const int64_t t = it.m0 + 16 * m + r, n = n0 + 16 * wave + 4 * g;
+        if (t < it.hi && n < NO) {   // NO is a multiple of 4
+            f32x4 y = c0;
+            if constexpr (GATED) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = gate(c0[i], c1[i]);
+            }
+            if constexpr (OUT_BF16)
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + t * NO + n) =
+                    u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+            else
+                *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + t * NO + n) = y;
+        }
+    }
+}
+
+template <bool OUT_BF16, bool GATED, bool GATHERED, int NB, int W, int TOK>
+__global__ __launch_bounds__(64 * W, 2) void mx_rows_kernel(MxArgs a) {
+    __shared__ f32x4 sums[W][NB][64];
+    RowsItem it;
+    const int64_t NO = GATED ? a.N / 2 : a.N;
+    constexpr int kCols = 16 * (GATED ? NB / 2 : NB);
+    if (!find_rows_item<TOK>(a.offs, a.E, a.M, (int32_t)((NO + kCols - 1) / kCols), &it)) return;
+    const int64_t left = it.hi - it.m0;
+    if (left <= 16) mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 1, W, 2>(a, it, sums);
+    else if (left <= 32) mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 2, W, 1>(a, it, sums);
+    else mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 4, W, 1>(a, it, sums);
+}
+
+template <bool GATED, int NB, int W, int TOK>
+hipError_t launch_mx_rows(const MxArgs& a, bool bf16, hipStream_t s) {
+    const int64_t ntn = ceil_div(GATED ? a.N / 2 : a.N, 16 * (GATED ? NB / 2 : NB));
+    // ceil(T_e / TOK) over the groups is at most M / TOK and one for each group with rows
+    const int64_t most = (a.M / TOK + (a.M < a.E ? a.M : a.E)) * ntn;
+    const dim3 grid((unsigned)most), block(64 * W);
+    timing_mark("mx_rows_kernel", s);
+    if (a.rows) {
+        if (bf16) hipLaunchKernelGGL((mx_rows_kernel<true, GATED, true, NB, W, TOK>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((mx_rows_kernel<false, GATED, true, NB, W, TOK>), grid, block, 0, s, a);
+    } else {
+        if (bf16) hipLaunchKernelGGL((mx_rows_kernel<true, GATED, false, NB, W, TOK>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((mx_rows_kernel<false, GATED, false, NB, W, TOK>), grid, block, 0, s, a);
+    }
+    timing_end(s);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_mxfp4(const void* X, bool bf16, int64_t T, int64_t K, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t s) {
+    const MxRowArgs a{X, nullptr, codes, scales, T, K};
+    timing_mark("quantize_mxfp4_kernel", s);
+    if (bf16) hipLaunchKernelGGL(quantize_mxfp4_kernel<true>, mx_row_grid(T, K), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(quantize_mxfp4_kernel<false>, mx_row_grid(T, K), dim3(256), 0, s, a);
+    timing_end(s);
+    return hipGetLastError();
+}
+
+hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t T, int64_t K, bool bf16,
+                                   void* X, hipStream_t s) {
+    const MxRowArgs a{codes, scales, X, nullptr, T, K};
+    timing_mark("dequantize_mxfp4_kernel", s);
+    if (bf16) hipLaunchKernelGGL(dequantize_mxfp4_kernel<true>, mx_row_grid(T, K), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(dequantize_mxfp4_kernel<false>, mx_row_grid(T, K), dim3(256), 0, s, a);
+    timing_end(s);
+    return hipGetLastError();
+}
+
+hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, hipStream_t s) {
+    // a launch has fewer than 2^32 threads
+    if ((a.M / 64 + a.E) * ceil_div(a.N, 32) >= int64_t(1) << 23) return hipErrorInvalidConfiguration;
+    return gated ? launch_mx_rows<true, 4, 4, 64>(a, bf16, s) : launch_mx_rows<false, 4, 4, 64>(a, bf16, s);
+}
+
+}  // namespace drgg

@@ -599,6 +599,162 @@ drgg_status moe_ffn_int8(const void *X, const float *logits, const int8_t *W1q,
 drgg_status moe_ffn_int8_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
                                         size_t *bytes);
 
+/*
+ * ---- Selection by scores ----------------------------------------------------
+ *
+ * moe_route with scores s_e = sigmoid(logit_e), or the softmax over all E
+ * logits, in the logits' place:
+ *   * An expert is chosen by its value v_e = s_e + bias_e (bias [E] FP32 on the
+ *     device, NULL for none); the bias takes no part in the weights.
+ *   * The E experts are `groups` groups of E / groups neighbours.  A group's
+ *     value is the largest v_e in it (best = 1), or the sum of the two largest
+ *     (best = 2; the one, where there is one).  Only the top_groups groups of
+ *     the largest values take part (ties to the lowest index).
+ *   * experts [T, k]: the k largest values of those groups, in decreasing order,
+ *     the lowest index first among equals.  Values are compared as those of
+ *     64-bit arithmetic on the FP32 logits and biases: in FP32 wherever its
+ *     error cannot change a choice, else again in 64 bits.  Without bias and
+ *     with one group the order is that of the logits, as in moe_route.
+ *   * weights [T, k]: scale * s_j / (sum of the k chosen s) with renormalize != 0
+ *     (taken as a ratio: also where every s_j itself is below FP32's range),
+ *     else scale * s_j.
+ *   * An expert whose logit or bias is -infinity is masked: chosen only where
+ *     the groups that take part have fewer than k others, then by index, with
+ *     weight 0; a group with none but masked experts comes after the others.  A
+ *     NaN value counts as larger than +infinity, and its weight is NaN.  A
+ *     softmax over logits with NaN or +infinity is NaN at every expert that is
+ *     not masked.
+ * group_offsets, positions, tokens, workspace (moe_route_workspace_size) and
+ * limits as for moe_route; besides 1 <= groups <= 64, a divisor of E,
+ * 1 <= top_groups <= groups, k <= top_groups * E / groups, best 1 or 2, and scale
+ * positive and finite (DRGG_EINVAL).  `scoring` is a HOST pointer, read before
+ * the call returns.
+ */
+typedef enum {
+    DRGG_SCORE_SOFTMAX = 0,
+    DRGG_SCORE_SIGMOID = 1
+} drgg_score;
+
+typedef struct {
+    drgg_score score;
+    int32_t groups, top_groups, best;
+    int renormalize;
+    float scale;
+    const float *bias;
+} drgg_scoring;
+
+drgg_status moe_route_scores(const float *logits, int64_t T, int32_t E, int32_t k,
+                             const drgg_scoring *scoring, int32_t *experts, float *weights,
+                             int32_t *group_offsets, int32_t *positions, int32_t *tokens,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradient of its weights in the logits (the choice, and so the bias, has
+ * none): dlogits [T, E] from dweights [T, k], with r = sum_j w_j dw_j / scale,
+ *   sigmoid, renormalize != 0:  w_j (1 - s_j) (dw_j - r)  at the chosen, else 0
+ *   sigmoid:                    w_j (1 - s_j) dw_j        at the chosen, else 0
+ *   softmax, renormalize != 0:  w_j (dw_j - r)            at the chosen, else 0
+ *   softmax:                    s_e (scale dw_e - scale r), dw_e = 0 but at the chosen
+ * Only score, renormalize and scale of `scoring` are used.  A chosen expert of
+ * weight 0 counts as not chosen, and its dweights are not used.
+ */
+drgg_status moe_route_scores_grad(const float *dweights, const float *logits, const int32_t *experts,
+                                  const float *weights, int64_t T, int32_t E, int32_t k,
+                                  const drgg_scoring *scoring, float *dlogits, hipStream_t stream);
+
+/*
+ * ---- Products in microscaled 4-bit floating point ---------------------------
+ *
+ * A row of K values (K a multiple of 32) is K/32 blocks of 32, each with a
+ * scale 2^(b - 127), b a byte, and 32 elements of two exponent bits and one
+ * mantissa bit: codes 0 .. 7 are 0, 0.5, 1, 1.5, 2, 3, 4 and 6, codes 8 .. 15
+ * their negatives.  b = 255 is NaN.
+ *   codes   [rows, K/2] bytes, the even column in the low half
+ *   scales  [ceil(K/256), rows, 8] bytes: the scales of 256 columns side by
+ *           side, row after row.  The bytes past column K may hold anything
+ *           (the quantisation writes 0).
+ * Rows stacked in more dimensions ([E, N]) are E*N rows.
+ *
+ * Quantisation of X [T, K] (BF16 or FP32): with m = max|x| of a block,
+ * b = floor(log2 m) - 2 + 127 limited to 0 .. 254, and the elements are the
+ * codes nearest to x / 2^(b - 127), the even code among two as near, beyond 6
+ * limited to it (m / 2^(b - 127) is below 8).  A block of zeros has b = 0; one
+ * that holds an infinity or NaN has b = 255 and codes 0.  Dequantisation gives
+ * the values (exact in FP32 and in BF16, where they are in its range).
+ * 32 <= K <= 2^22, T < 2^31.  Codes and X 16-byte aligned, scales 8.
+ */
+drgg_status quantize_mxfp4(const void *X, drgg_dtype dtype, int64_t T, int64_t K, uint8_t *codes,
+                           uint8_t *scales, hipStream_t stream);
+drgg_status dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t T, int64_t K,
+                             drgg_dtype dtype, void *X, hipStream_t stream);
+
+/*
+ * Y[t,n] = sum_k x[t,k] * w[e(t),n,k], FP32 accumulation in one fixed order,
+ * rounded once to out_dtype.  Xq [M, K/2] with scales x_scale, Wq [E, N, K/2]
+ * with w_scale (E*N rows).  Every product of two elements is exact.  gated,
+ * rows and group_offsets as for grouped_gemm_int8 (gated: silu(g) to within
+ * (4 |g| + 16) 2^-24 of it); with rows, Xq [T, K/2] and T*K/2 <= 2^31 - 4097.
+ * N a multiple of 8 (gated: 16), K of 32, N and K at most 2^22, M < 2^31.
+ * gemm_mxfp4 is the one-group case without offsets.  No workspace.
+ */
+drgg_status grouped_gemm_mxfp4(const uint8_t *Xq, const uint8_t *x_scale, const uint8_t *Wq,
+                               const uint8_t *w_scale, const int32_t *group_offsets,
+                               const int32_t *rows, int64_t T, int32_t E, int64_t M, int64_t N,
+                               int64_t K, int gated, drgg_dtype out_dtype, void *Y,
+                               hipStream_t stream);
+drgg_status gemm_mxfp4(const uint8_t *Xq, const uint8_t *x_scale, const uint8_t *Wq,
+                       const uint8_t *w_scale, int64_t M, int64_t N, int64_t K, int gated,
+                       drgg_dtype out_dtype, void *Y, hipStream_t stream);
+
+/*
+ * moe_ffn_int8's block on 4-bit weights, in one call: moe_route_scores (or, with
+ * scoring NULL, moe_route with renormalize = 1), quantize_mxfp4 of X [T,H] BF16,
+ * the gated product of its rows in the grouped order with W1 (E*2I rows of H,
+ * gate rows then up rows), quantize_mxfp4 of its FP32 result, the product with
+ * W2 (E*H rows of I; BF16), and moe_combine into out [T,H] BF16.  The same
+ * results as the single calls.  H and I multiples of 32, T*H/2 <= 2^31 - 4097.
+ * Workspace: moe_ffn_mxfp4_workspace_size bytes, 16-byte aligned, no
+ * initialisation; calls in flight at once must not share it.
+ */
+drgg_status moe_ffn_mxfp4(const void *X, const float *logits, const uint8_t *W1q,
+                          const uint8_t *w1_scale, const uint8_t *W2q, const uint8_t *w2_scale,
+                          int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
+                          const drgg_scoring *scoring, void *out, void *workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+drgg_status moe_ffn_mxfp4_workspace_size(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
+                                         size_t *bytes);
+
+/*
+ * ---- The gated activation of a training step, kept in 8 bits ----------------
+ *
+ * GU [T*k, 2I] BF16 holds gate and up halves g, u of the experts' rows in the
+ * grouped order, positions [T, k] the place of every (token, expert) pair and
+ * weights [T, k] FP32 its weight (as moe_route gives them).
+ *   forward   h[p] = weights[t,j] * silu(g[p]) * u[p], p = positions[t,j]: [T*k, I]
+ *             BF16, FP32 until then; and what the backward pass needs of GU:
+ *             codes [T*k, 2I] int8 = round(127 x / m) and scale [T*k, 2B] FP32 =
+ *             m / 127, m = max|x| over each 128 columns of a half (B =
+ *             ceil(I / 128) blocks of gate, then B of up).  A block of zeros has
+ *             scale 0, one with an infinity or NaN scale NaN and codes 0.
+ *   backward  from dh [T*k, I] BF16, with g, u the values that the codes stand
+ *             for and s = 1 / (1 + exp(-g)):
+ *               dGU[p] = weights[t,j] * dh[p] * (u s (1 + g (1 - s)), g s)   BF16
+ *               h[p] = weights[t,j] * g s u                                 BF16
+ *               dweights[t,j] = sum over I of dh[p] * g s u                 FP32
+ *             (h again, for the gradient of the product that takes it).
+ * With the weights here, the rows that the following product makes are added
+ * without weights (moe_combine, weights NULL) and need not be kept for the
+ * weights' gradient.  A position outside [0, T*k) is skipped (its dweights are
+ * 0), so that no access leaves the buffers; a row that no entry names is not
+ * written.  I a multiple of 8, 8 <= I <= 2^21; k and T as for moe_route.
+ */
+drgg_status moe_gate_int8(const void *GU, const int32_t *positions, const float *weights, int64_t T,
+                          int32_t k, int64_t I, void *h, int8_t *codes, float *scale,
+                          hipStream_t stream);
+drgg_status moe_gate_int8_grad(const void *dh, const int8_t *codes, const float *scale,
+                               const int32_t *positions, const float *weights, int64_t T, int32_t k,
+                               int64_t I, void *dGU, void *h, float *dweights, hipStream_t stream);
+
 /* Text of a status code, with the HIP error name and text appended for
  * DRGG_EDEVICE (the fail-closed precedent of PR #7516, #7632 commit body:
  * an error names what failed and why). */
