@@ -71,7 +71,11 @@ drgg_status run_mxfp4(const uint8_t* Xq, const uint8_t* xs, const uint8_t* Wq, c
         if (st != DRGG_OK) return st;
     }
     if (M == 0) return DRGG_OK;
-    return launch_status(launch_mxfp4(MxArgs{Xq, Wq, xs, ws, offs, Y, M, N, K, E, rows, T}, gated != 0, dt == DRGG_BF16, s));
+    int cus = 0;
+    drgg_status st = current_cu_count(&cus);
+    if (st != DRGG_OK) return st;
+    return launch_status(launch_mxfp4(MxArgs{Xq, Wq, xs, ws, offs, Y, M, N, K, E, rows, T}, gated != 0, dt == DRGG_BF16, cus,
+                                      knob_tile(), s));
 }
 
 // The parts of moe_ffn_mxfp4's workspace (byte offsets, multiples of 256).  The
@@ -222,6 +226,9 @@ drgg_status moe_ffn_mxfp4(const void* X, const float* logits, const uint8_t* W1q
     auto* xs = reinterpret_cast<uint8_t*>(ws + L.xs);
     auto* hq = reinterpret_cast<uint8_t*>(ws + L.hq);
     auto* hs = reinterpret_cast<uint8_t*>(ws + L.hs);
+    int cus = 0;
+    st = current_cu_count(&cus);
+    if (st != DRGG_OK) return st;
     const int64_t R = T * k;
     hipError_t e = scoring ? launch_moe_route_scores(logits, T, E, k, *scoring, experts, weights, offsets, positions, tokens,
                                                      ws + L.table, stream)
@@ -229,10 +236,10 @@ drgg_status moe_ffn_mxfp4(const void* X, const float* logits, const uint8_t* W1q
                                               ws + L.table, stream);
     if (e == hipSuccess) e = launch_quantize_mxfp4(X, true, T, H, x, xs, stream);
     if (e == hipSuccess)
-        e = launch_mxfp4(MxArgs{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E, tokens, T}, true, false, stream);
+        e = launch_mxfp4(MxArgs{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E, tokens, T}, true, false, cus, knob_tile(), stream);
     if (e == hipSuccess) e = launch_quantize_mxfp4(ws + L.h, false, R, I, hq, hs, stream);
     if (e == hipSuccess)
-        e = launch_mxfp4(MxArgs{hq, W2q, hs, w2_scale, offsets, ws + L.y, R, H, I, E}, false, true, stream);
+        e = launch_mxfp4(MxArgs{hq, W2q, hs, w2_scale, offsets, ws + L.y, R, H, I, E}, false, true, cus, knob_tile(), stream);
     if (e == hipSuccess) e = launch_moe_combine(ws + L.y, positions, weights, T, k, H, true, out, stream);
     return launch_status(e);
 }

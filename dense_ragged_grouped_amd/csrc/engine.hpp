@@ -76,10 +76,11 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) char lds_t;
 
 // SCAN: words of scratch; the schedule alone needs one per wave and one more.
-template <int SCAN>
+// MOST: the experts it has room for.
+template <int SCAN, int MOST = kMaxExperts>
 struct SchedOf {
-    int32_t offs[kMaxExperts + 1];    // clamped, non-decreasing offsets
-    int32_t prefix[kMaxExperts + 1];  // exclusive prefix of work per expert
+    int32_t offs[MOST + 1];    // clamped, non-decreasing offsets
+    int32_t prefix[MOST + 1];  // exclusive prefix of work per expert
     int32_t scan[SCAN];
 };
 using Sched = SchedOf<kMaxGemmThreads>;
@@ -160,8 +161,8 @@ __device__ __forceinline__ int32_t wave_incl_sum(int32_t x) {
 // uniform: offs[e] = e * T.  With fewer than kWaveExperts experts wave 0
 // does it all (offsets on lanes 0..E, shuffle scans).  Must be called by all
 // threads; ends with a barrier.
-template <int SCAN, class WorkFn>
-__device__ void build_schedule(SchedOf<SCAN>& s, const int32_t* __restrict__ offs, int E, int64_t M, int64_t T,
+template <int SCAN, int MOST, class WorkFn>
+__device__ void build_schedule(SchedOf<SCAN, MOST>& s, const int32_t* __restrict__ offs, int E, int64_t M, int64_t T,
                                WorkFn work) {
     const int tid = threadIdx.x, nthr = blockDim.x;
     if (E < kWaveExperts) {
@@ -331,8 +332,8 @@ __device__ __forceinline__ int32_t uni(int32_t v) { return __builtin_amdgcn_read
 // Largest e < n with prefix[e] <= w (so that prefix[e] <= w < prefix[e+1]
 // when w < prefix[n]); n is the number of experts, or of positions of a
 // plan's walk.
-template <int SCAN>
-__device__ __forceinline__ int find_expert(const SchedOf<SCAN>& s, int n, int32_t w) {
+template <int SCAN, int MOST>
+__device__ __forceinline__ int find_expert(const SchedOf<SCAN, MOST>& s, int n, int32_t w) {
     int lo = 0, hi = n;   // answer in [0, n)
     while (lo < hi) {
         int mid = (lo + hi + 1) >> 1;
@@ -907,6 +908,16 @@ __device__ __forceinline__ void store_tile_lines(const Mma& mma, lds_t* scr, voi
     }
 }
 
+// What a runner is made of, by element type: loads and products of whole
+// values here; block-scaled elements have their own (mxfp4.hip).
+template <class El>
+struct EngineParts {
+    template <int BM, int BN, bool AK, bool BK, int WAVES>
+    using Mma = TileMma<BM, BN, AK, BK, WAVES, El>;
+    template <int ROWS, bool KMAJ, int WAVES, bool PAIRED, bool GATHERED>
+    using Loader = StageLoader<ROWS, KMAJ, WAVES, PAIRED, GATHERED>;
+};
+
 // Issue schedule of the stage loads of a 4-wave runner (steps t of the
 // global step sequence; the prologue acts as steps -4 .. -1).  A K-major operand loads stages t+3
 // and t+4 at odd steps (into the pair buffer whose two stages t-1 and t were
@@ -960,9 +971,9 @@ struct NoLoads {
 template <int BM, int BN, bool AK, bool BK, int WAVES = kGemmWaves, class El = Bf16, bool PAIRED_B = false,
           bool GATHERED_A = false>
 struct TileRunner {
-    using Mma = TileMma<BM, BN, AK, BK, WAVES, El>;
-    using LA = StageLoader<BM, AK, WAVES, false, GATHERED_A>;
-    using LB = StageLoader<BN, BK, WAVES, PAIRED_B>;
+    using Mma = typename EngineParts<El>::template Mma<BM, BN, AK, BK, WAVES>;
+    using LA = typename EngineParts<El>::template Loader<BM, AK, WAVES, false, GATHERED_A>;
+    using LB = typename EngineParts<El>::template Loader<BN, BK, WAVES, PAIRED_B, false>;
     using Plan = IssuePlan<AK, BK, LA::kPerWave, LB::kPerWave>;
     Mma mma;
     LA la;

@@ -164,7 +164,7 @@ struct MxArgs {
     const int32_t* rows = nullptr;   // row r of the product is row rows[r] of X and xs, T rows (null: row r)
     int64_t T = 0;
 };
-hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, hipStream_t s);
+hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s);
 
 hipError_t launch_moe_gate_int8(const void* GU, const int32_t* positions, const float* weights, int64_t T, int32_t k,
                                 int64_t I, void* h, int8_t* codes, float* scale, hipStream_t s);

@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * W, 2) void mx_rows_kernel(MxArgs a) {
     const int64_t left = it.hi - it.m0;
     if (left <= 16) mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 1, W, 2>(a, it, sums);
     else if (left <= 32) mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 2, W, 1>(a, it, sums);
-    else mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 4, W, 1>(a, it, sums);
+    else if constexpr (TOK > 32) mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 4, W, 1>(a, it, sums);
 }
 
 template <bool GATED, int NB, int W, int TOK>
@@ -309,6 +309,283 @@ hipError_t launch_mx_rows(const MxArgs& a, bool bf16, hipStream_t s) {
     }
     timing_end(s);
     return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// product, many rows per group
+//
+// The tile engine (engine.hpp) on 4-bit elements: a stage of 64 bytes a row is
+// 128 values, a fragment (16 bytes a lane) one block of 32, so that a lane needs
+// one scale byte per fragment and MFMA: the lower half of the lanes the blocks
+// 0 and 2 of a stage, the upper half 1 and 3.  The scales of a pair of stages
+// (eight bytes a row) are loaded beside the pair's codes and land behind them
+// in its buffer.  A lane reads the four bytes of a stage for two of its row
+// blocks and permutes its half's bytes into one register: byte 0 and 1 are the
+// two blocks' scales of sub-step 0, byte 2 and 3 those of sub-step 1, and the
+// MFMAs select the byte (a register and a shift for each block would be twice
+// the instructions, and the gated 256x256 tile would spill).
+
+struct Mxfp4 {};
+
+constexpr int mx_buffer_bytes(int rows) { return rows * (4 * kStageK + 8); }   // codes of a pair of stages, then scales
+
+#define DRGG_MX_BUFFERS(ROWS, name)                                                       \
+    __shared__ __attribute__((aligned(256))) char name##0[mx_buffer_bytes(ROWS)];         \
+    __shared__ __attribute__((aligned(256))) char name##1[mx_buffer_bytes(ROWS)]
+#define DRGG_MX_STAGES(BM, BN, name)                                                      \
+    DRGG_MX_BUFFERS(BM, name##_a);                                                        \
+    DRGG_MX_BUFFERS(BN, name##_b);                                                        \
+    const Stages name{{(lds_t*)name##_a0, (lds_t*)name##_a0, (lds_t*)name##_a1, (lds_t*)name##_a1}, \
+                      {(lds_t*)name##_b0, (lds_t*)name##_b0, (lds_t*)name##_b1, (lds_t*)name##_b1}}
+
+// The codes as StageLoader brings them, then ROWS/32 wave instructions of 4 bytes
+// a lane: lane l of instruction g has the scales of stage l%2 of row 32 g + l/2.
+// An operand that is not gathered says in `of` which row of its scales is its
+// first.
+template <int ROWS, int WAVES, bool PAIRED, bool GATHERED>
+struct MxLoader : StageLoader<ROWS, true, WAVES, PAIRED, GATHERED> {
+    using Codes = StageLoader<ROWS, true, WAVES, PAIRED, GATHERED>;
+    static constexpr int kCodes = Codes::kPerWave, kScales = ROWS / 32 / WAVES;
+    static constexpr int kPerWave = kCodes + kScales;
+    static_assert(kScales >= 1, "every wave loads scales");
+    uint32_t soff[kScales];
+    const uint8_t* scales;      // of the operand's first row
+    // set once by the kernel: the scales of row 0, the bytes from the scales of
+    // 256 columns to the next, and (paired) the rows to the second run
+    const uint8_t* all_scales;
+    int64_t scale_step;
+    int32_t pair_rows;
+
+    __device__ __forceinline__ void init(const Operand& op) {
+        Codes::init(op);
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        scales = all_scales + (GATHERED ? 0 : op.of * 8);
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) {
+            const int row = (wave * kScales + i) * 32 + (lane >> 1);
+            int from = PAIRED ? (row & 31) + 32 * (row >> 6) : row;
+            bool ok = from < op.nvalid;
+            if constexpr (GATHERED) {
+                from = ok ? op.index[from] : 0;
+                ok = ok && (uint32_t)from < (uint32_t)op.of;
+            }
+            if (PAIRED && (row & 32)) from += pair_rows;
+            soff[i] = ok ? (uint32_t)(from * 8 + 4 * (lane & 1)) : kOOB;
+        }
+    }
+    __device__ __forceinline__ void issue(lds_t* buf, int L, bool valid) const { issue_part<0, kPerWave>(buf, L, valid); }
+    template <int J0, int J1>
+    __device__ __forceinline__ void issue_part(lds_t* buf, int L, bool valid) const {
+        constexpr int c1 = J1 < kCodes ? J1 : kCodes, s0 = J0 > kCodes ? J0 - kCodes : 0, s1 = J1 - kCodes;
+        if constexpr (J0 < c1) Codes::template issue_part<J0, c1>(buf, L, valid);
+        if constexpr (s0 < s1) {
+            const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            const __amdgpu_buffer_rsrc_t r = make_rsrc(scales + (L >> 1) * scale_step);
+            const int lane = threadIdx.x & 63;
+            const bool in = valid && (L + (lane & 1)) * kStageK < this->klen;
+#pragma unroll
+            for (int i = s0; i < s1; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(buf + ROWS * 4 * kStageK + (wave * kScales + i) * 256),
+                                                         4, in ? soff[i] : kOOB, 0, 0, 0);
+        }
+    }
+};
+
+// The products of a tile (TileMma's wave grid and accumulator layout).
+template <int BM, int BN, int WAVES>
+struct MxMma {
+    using Grid = TileMma<BM, BN, true, true, WAVES, Bf16>;
+    __device__ static __forceinline__ int wave_row(int wave) { return Grid::wave_row(wave); }
+    __device__ static __forceinline__ int wave_col(int wave) { return Grid::wave_col(wave); }
+    static constexpr int kBI = Grid::kBI, kBJ = Grid::kBJ;
+    static constexpr int kReads = kBI + kBJ, kMfmas = kBI * kBJ;
+    f32x16 acc[kBI][kBJ];
+    i32x4 fa[2][kBI], fb[2][kBJ];
+    static_assert(kBI % 2 == 0 && kBJ % 2 == 0, "scales are held for two blocks of rows");
+    uint32_t sa[2][kBI / 2], sb[2][kBJ / 2];
+    // Stage of the tile that is read next, stages a tile runs, blocks of a row.
+    // The bytes of a stage past the row's last block may hold anything: they
+    // are cleared, since a scale of 255 would make the zeros there NaN.
+    int at, stages, blocks;
+
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kBI; ++i)
+#pragma unroll
+            for (int j = 0; j < kBJ; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    }
+
+    template <int F, int ST>
+    __device__ __forceinline__ void read(const Stages& st, int s) {
+        const int l = threadIdx.x & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int ra = wave_row(wave), rb = wave_col(wave);
+        fa[F][0] = __builtin_bit_cast(i32x4, read_frag<BM, true>(st.a[ST], ST & 1, ra, s, l));
+#pragma unroll
+        for (int j = 0; j < kBJ; ++j)
+            fb[F][j] = __builtin_bit_cast(i32x4, read_frag<BN, true>(st.b[ST], ST & 1, rb + 32 * j, s, l));
+#pragma unroll
+        for (int i = 1; i < kBI; ++i)
+            fa[F][i] = __builtin_bit_cast(i32x4, read_frag<BM, true>(st.a[ST], ST & 1, ra + 32 * i, s, l));
+        if constexpr (F == 1) {
+#pragma unroll
+            for (int i = 0; i < kBI / 2; ++i) sa[1][i] = sa[0][i];
+#pragma unroll
+            for (int j = 0; j < kBJ / 2; ++j) sb[1][j] = sb[0][j];
+        } else {
+            const int half = l >> 5, left = blocks - 4 * at;
+            at = at + 1 == stages ? 0 : at + 1;
+            // byte selectors: 0 to 3 of the first block's dword, 4 to 7 of the second's; 0x0c is zero
+            const uint32_t sel = (half < left ? 0x0400u + 0x0101u * half : 0x0c0cu) |
+                                 (2 + half < left ? 0x06020000u + 0x01010000u * half : 0x0c0c0000u);
+            typedef const __attribute__((address_space(3))) uint32_t lds_u32;
+            auto two = [&](const lds_t* scales, int row) {
+                const lds_u32* p = reinterpret_cast<lds_u32*>(scales + (row + (l & 31)) * 8 + 4 * (ST & 1));
+                return __builtin_amdgcn_perm(p[64], p[0], sel);   // 32 rows on: 64 dwords
+            };
+#pragma unroll
+            for (int i = 0; i < kBI / 2; ++i) sa[0][i] = two(st.a[ST] + BM * 4 * kStageK, ra + 64 * i);
+#pragma unroll
+            for (int j = 0; j < kBJ / 2; ++j) sb[0][j] = two(st.b[ST] + BN * 4 * kStageK, rb + 64 * j);
+        }
+    }
+
+    // the byte selections are immediates
+    template <int F, bool FIRST, int BA, int BB>
+    __device__ __forceinline__ void product(f32x16& c, i32x4 b, i32x4 a, uint32_t scale_b, uint32_t scale_a) {
+        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fragment(__builtin_bit_cast(u32x4, b)),
+                                                            fragment(__builtin_bit_cast(u32x4, a)), FIRST ? f32x16{} : c, 4, 4,
+                                                            2 * F + BB, scale_b, 2 * F + BA, scale_a);
+    }
+    template <int F, bool FIRST = false>
+    __device__ __forceinline__ void mfma() {
+#pragma unroll
+        for (int i = 0; i < kBI; i += 2) {
+#pragma unroll
+            for (int j = 0; j < kBJ; j += 2) {
+                product<F, FIRST, 0, 0>(acc[i][j], fb[F][j], fa[F][i], sb[F][j / 2], sa[F][i / 2]);
+                product<F, FIRST, 0, 1>(acc[i][j + 1], fb[F][j + 1], fa[F][i], sb[F][j / 2], sa[F][i / 2]);
+            }
+#pragma unroll
+            for (int j = 0; j < kBJ; j += 2) {
+                product<F, FIRST, 1, 0>(acc[i + 1][j], fb[F][j], fa[F][i + 1], sb[F][j / 2], sa[F][i / 2]);
+                product<F, FIRST, 1, 1>(acc[i + 1][j + 1], fb[F][j + 1], fa[F][i + 1], sb[F][j / 2], sa[F][i / 2]);
+            }
+        }
+    }
+};
+
+}  // namespace
+
+template <>
+struct EngineParts<Mxfp4> {
+    template <int BM, int BN, bool AK, bool BK, int WAVES>
+    using Mma = MxMma<BM, BN, WAVES>;
+    template <int ROWS, bool KMAJ, int WAVES, bool PAIRED, bool GATHERED>
+    using Loader = MxLoader<ROWS, WAVES, PAIRED, GATHERED>;
+};
+
+namespace {
+
+constexpr int mx_ep_rows(int bm, int bn) { return bm == 128 && bn == 256 ? 16 : 8; }   // what the scales leave room for
+
+// The 8-bit product's walk and epilogue without scales of whole rows.
+template <int BM, int BN, bool OUT_BF16, bool GATED, bool GATHERED, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, BM == 128 && BN == 128 ? 2 : 1) void mx_tile_kernel(MxArgs a) {
+    DRGG_MX_STAGES(BM, BN, stg);
+    __shared__ SchedOf<16, BM == 128 && BN == 128 ? kMx128MaxExperts : kMaxExperts> sch;
+    __shared__ __attribute__((aligned(16))) char ep[WAVES * mx_ep_rows(BM, BN) * 128];
+    using Runner = TileRunner<BM, BN, true, true, WAVES, Mxfp4, GATED, GATHERED>;
+    using Mma = typename Runner::Mma;
+    constexpr int BC = GATED ? BN / 2 : BN;             // output columns per tile
+    constexpr int NJ = GATED ? Mma::kBJ / 2 : Mma::kBJ; // blocks of 32 of them per wave
+    const int64_t NO = GATED ? a.N / 2 : a.N, K2 = a.K / 4;   // K2: a row in the engine's units of 2 bytes
+    const int32_t ntn = (int32_t)((NO + BC - 1) / BC);
+    build_schedule(sch, a.offs, a.E, a.M, a.M, [=](int, int32_t T) { return ceil_div32(T, BM) * ntn; });
+    const int64_t total = uni(sch.prefix[a.E]);
+    const int64_t G = gridDim.x;
+    int64_t w = xcd_remap(blockIdx.x, G);
+    auto more = [&]() { return w < total; };
+    auto next = [&](TileInfo& t) {
+        const int e = uni(find_expert(sch, a.E, (int32_t)w));
+        const int32_t oe = uni(sch.offs[e]), oe1 = uni(sch.offs[e + 1]);
+        const int32_t local = (int32_t)w - uni(sch.prefix[e]);
+        const int32_t mt = local / ntn, nt = local % ntn;
+        t.o0 = oe + (int64_t)mt * BM;
+        t.o1 = (int64_t)nt * BC;
+        t.rows = (int32_t)min<int64_t>(BM, oe1 - t.o0);
+        t.cols = (int32_t)min<int64_t>(BC, NO - t.o1);
+        t.e = e;
+        const int64_t row = (int64_t)e * a.N + t.o1;
+        t.A = GATHERED ? Operand{reinterpret_cast<const uint16_t*>(a.X), K2, t.rows, (int32_t)K2, 0, a.rows + t.o0, a.T}
+                       : Operand{reinterpret_cast<const uint16_t*>(a.X) + t.o0 * K2, K2, t.rows, (int32_t)K2, 0, nullptr, t.o0};
+        t.B = Operand{reinterpret_cast<const uint16_t*>(a.W) + row * K2, K2, t.cols, (int32_t)K2, NO * K2 * 2, nullptr, row};
+        w += G;
+    };
+    auto finish = [&](const TileInfo& t, const Mma& mma) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int rb = GATED ? Mma::wave_col(wave) / 2 : Mma::wave_col(wave);
+        auto value = [&](int i, int j, int q) {
+            f32x4 y;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                y[r] = GATED ? gate(mma.acc[i][2 * j % Mma::kBJ][4 * q + r], mma.acc[i][(2 * j + 1) % Mma::kBJ][4 * q + r])
+                             : mma.acc[i][j][4 * q + r];
+            return y;
+        };
+        const int64_t o = t.o0 * NO + t.o1;
+        void* base = OUT_BF16 ? (void*)(static_cast<uint16_t*>(a.out) + o) : (void*)(static_cast<float*>(a.out) + o);
+        store_tile_values<OUT_BF16, mx_ep_rows(BM, BN), Mma, NJ>(value, rb, (lds_t*)ep, base, NO, t.rows, t.cols);
+    };
+    Runner runner;
+    runner.st = stg;
+    runner.mma.at = 0;
+    runner.mma.stages = Runner::round4((int)((K2 + kStageK - 1) / kStageK));
+    runner.mma.blocks = (int)(a.K / 32);
+    runner.la.all_scales = a.xs;
+    runner.la.scale_step = 8 * (GATHERED ? a.T : a.M);
+    runner.lb.all_scales = a.ws;
+    runner.lb.scale_step = 8 * (int64_t)a.E * a.N;
+    runner.lb.pair_rows = (int32_t)NO;
+    runner.run(more, next, finish);
+}
+
+template <int BM, int BN, int WAVES, bool GATED, bool GATHERED>
+void launch_mx_tile_t(const MxArgs& a, bool bf16, dim3 grid, hipStream_t s) {
+    const dim3 block(64 * WAVES);
+    constexpr bool kBf16 = !GATED || BN >= 256;   // a gated 128x128 tile has 32 columns per wave, half a BF16 line
+    if constexpr (kBf16)
+        if (bf16) {
+            hipLaunchKernelGGL((mx_tile_kernel<BM, BN, true, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+            return;
+        }
+    hipLaunchKernelGGL((mx_tile_kernel<BM, BN, false, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+}
+
+template <int BM, int BN, int WAVES>
+hipError_t launch_mx_tile(const MxArgs& a, bool gated, bool bf16, int64_t grid_n, hipStream_t s) {
+    const dim3 grid((unsigned)grid_n);
+    timing_mark("mx_tile_kernel", s);
+    if (gated && a.rows) launch_mx_tile_t<BM, BN, WAVES, true, true>(a, bf16, grid, s);
+    else if (gated) launch_mx_tile_t<BM, BN, WAVES, true, false>(a, bf16, grid, s);
+    else if (a.rows) launch_mx_tile_t<BM, BN, WAVES, false, true>(a, bf16, grid, s);
+    else launch_mx_tile_t<BM, BN, WAVES, false, false>(a, bf16, grid, s);
+    timing_end(s);
+    return hipGetLastError();
+}
+
+template <bool GATED>
+hipError_t launch_mx_program(const MxArgs& a, const Int8Program& p, bool bf16, hipStream_t s) {
+    if (p.tok == 32) return launch_mx_rows<GATED, 4, 4, 32>(a, bf16, s);
+    if (p.waves == 4) return launch_mx_rows<GATED, 4, 4, 64>(a, bf16, s);
+    if (p.nb == 4) return launch_mx_rows<GATED, 4, 8, 64>(a, bf16, s);
+    if constexpr (!GATED)
+        if (p.nb == 1) return launch_mx_rows<false, 1, 8, 64>(a, bf16, s);
+    return launch_mx_rows<GATED, 2, 8, 64>(a, bf16, s);
 }
 
 }  // namespace
@@ -333,10 +610,18 @@ hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, 
     return hipGetLastError();
 }
 
-hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, hipStream_t s) {
-    // a launch has fewer than 2^32 threads
-    if ((a.M / 64 + a.E) * ceil_div(a.N, 32) >= int64_t(1) << 23) return hipErrorInvalidConfiguration;
-    return gated ? launch_mx_rows<true, 4, 4, 64>(a, bf16, s) : launch_mx_rows<false, 4, 4, 64>(a, bf16, s);
+hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s) {
+    const Int8Program p = mxfp4_program(a.E, a.M, a.N, a.K, gated, bf16, forced_tile);
+    if (p.tile == kTileAuto)
+        return gated ? launch_mx_program<true>(a, p, bf16, s) : launch_mx_program<false>(a, p, bf16, s);
+    const int64_t cols_out = gated ? a.N / 2 : a.N, bc = gated ? 128 : 256;
+    auto grid = [&](int64_t bm, int64_t bcols, int64_t per_cu) {
+        const int64_t most = (a.M / bm + (a.M < a.E ? a.M : a.E)) * ceil_div(cols_out, bcols);
+        return most < per_cu * cus ? most : per_cu * cus;
+    };
+    if (p.tile == kTile256x256) return launch_mx_tile<256, 256, 8>(a, gated, bf16, grid(256, bc, 1), s);
+    if (p.tile == kTile128x256) return launch_mx_tile<128, 256, 4>(a, gated, bf16, grid(128, bc, 1), s);
+    return launch_mx_tile<128, 128, 4>(a, gated, bf16, grid(128, bc / 2, 2), s);
 }
 
 }  // namespace drgg

@@ -572,4 +572,14 @@ inline Int8Program int8_program(int64_t E, int64_t M, int64_t N, int64_t K, bool
     return {int8_tile(E, M, K, ceil_div(cols_out, bc), ceil_div(cols_out, bc / 2), may128), 0, 0, 0};
 }
 
+// The same for a 4-bit product: its rows are K/2 bytes, and a step of 64 bytes
+// takes as long whatever the elements.  128x128 tiles have room for
+// kMx128MaxExperts groups beside the scales, two of them on a CU.
+constexpr int kMx128MaxExperts = 992;
+inline Int8Program mxfp4_program(int64_t E, int64_t M, int64_t N, int64_t K, bool gated, bool bf16, int forced_tile) {
+    Int8Program p = int8_program(E, M, N, K / 2, gated, bf16, forced_tile);
+    if (p.tile == kTile128x128 && E > kMx128MaxExperts) p.tile = kTile128x256;
+    return p;
+}
+
 }  // namespace drgg

@@ -101,7 +101,7 @@ hipError_t launch_quantize_mxfp4(const void* X, bool bf16, int64_t T, int64_t K,
 hipError_t launch_dequantize_mxfp4(const uint8_t*, const uint8_t*, int64_t, int64_t, bool, void*, hipStream_t) {
     return hipSuccess;
 }
-hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, hipStream_t) {
+hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, int, int, hipStream_t) {
     if (gated) {
         EXPECT(step++ == 2 && !bf16 && a.rows);
         EXPECT((const char*)a.X == x.lo && (const char*)a.xs == xs.lo);

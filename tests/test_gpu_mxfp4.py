@@ -253,6 +253,49 @@ def test_gathered(drgg, counts, T, N, K, gated):
             assert torch.equal(got, dev(y).to(torch.float32).to(dtype))
 
 
+TILES = [1, 2, 4]   # 256x256, 128x128, 128x256
+
+
+@pytest.fixture
+def forced(drgg):
+    def force(tile):
+        drgg.set_knob(drgg.KNOB_TILE, tile)
+    yield force
+    drgg.set_knob(drgg.KNOB_TILE, 0)
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("counts,N,K", [([1], 8, 32), ([3, 0, 300], 136, 96), ([17, 1, 33, 0, 64, 265], 264, 288),
+                                        ([513, 255, 0, 130], 520, 1056), ([700], 1000, 736), ([40] * 30, 72, 128),
+                                        ([5] * 1000, 32, 64), ([2100, 900], 776, 160), ([256], 256, 4096)])
+@pytest.mark.parametrize("gated,gathered", [(False, False), (True, False), (False, True), (True, True)])
+def test_every_tile(drgg, forced, tile, counts, N, K, gated, gathered):
+    """The tiles, whatever the rule would take: several per workgroup, cut at every edge, K within one stage and past
+    whole ones, the bytes past a row's last scale 255."""
+    rng = np.random.default_rng(N + K)
+    N = 2 * N if gated else N
+    E, M = len(counts), sum(counts)
+    T = M // 2 + 3 if gathered else M
+    x, xs, xv = operand(rng, T, K, fill=255)
+    w, ws, wv = operand(rng, E, N, K, fill=255)
+    offsets = counts_to_offsets(counts)
+    rows = None
+    if gathered:
+        rows = rng.integers(0, T, M).astype(np.int32)
+        rows[::11] = T
+        xv = np.where((rows < T)[:, None], xv[np.minimum(rows, T - 1)], 0)
+        rows = dev(rows)
+    y, mag = grouped64(xv, wv, offsets, N)
+    assert mag.max() * 64 < 2 ** 24
+    forced(tile)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = drgg.grouped_gemm_mxfp4(x, xs, w, ws, dev(offsets), gated=gated, rows=rows, out_dtype=dtype)
+        if gated:
+            check(got, *gate64(y))
+        else:
+            assert torch.equal(got, dev(y).to(torch.float32).to(dtype))
+
+
 @pytest.mark.parametrize("M,N", [(20, 72), (700, 264)])
 def test_nan_scales_stay_in_their_row_and_column(drgg, M, N):
     rng = np.random.default_rng(2)
