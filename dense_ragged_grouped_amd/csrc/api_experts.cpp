@@ -79,10 +79,10 @@ drgg_status run_mxfp4(const uint8_t* Xq, const uint8_t* xs, const uint8_t* Wq, c
 }
 
 // The parts of moe_ffn_mxfp4's workspace (byte offsets, multiples of 256).  The
-// experts' outputs y take the place of the codes of X and the activation,
-// which are no longer needed by then.
+// experts' outputs y take the place of the codes of X, which are no longer
+// needed by then.
 struct MxFfnLayout {
-    int64_t experts, weights, offsets, positions, tokens, table, hq, hs, x, xs, h, y, bytes;
+    int64_t experts, weights, offsets, positions, tokens, table, hq, hs, x, xs, y, bytes;
 };
 drgg_status mx_ffn_layout(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I, const drgg_scoring* c, MxFfnLayout* L) {
     drgg_status st = check_scores(T, E, k, c);
@@ -108,7 +108,6 @@ drgg_status mx_ffn_layout(int64_t T, int32_t E, int32_t k, int64_t H, int64_t I,
     L->y = at;
     L->x = part(T * (H / 2));
     L->xs = part(mx_scale_bytes(T, H));
-    L->h = part(R * I * 4);
     const int64_t y = L->y + round_up(R * H * 2, 256);
     L->bytes = at > y ? at : y;
     return DRGG_OK;
@@ -236,8 +235,8 @@ drgg_status moe_ffn_mxfp4(const void* X, const float* logits, const uint8_t* W1q
                                               ws + L.table, stream);
     if (e == hipSuccess) e = launch_quantize_mxfp4(X, true, T, H, x, xs, stream);
     if (e == hipSuccess)
-        e = launch_mxfp4(MxArgs{x, W1q, xs, w1_scale, offsets, ws + L.h, R, 2 * I, H, E, tokens, T}, true, false, cus, knob_tile(), stream);
-    if (e == hipSuccess) e = launch_quantize_mxfp4(ws + L.h, false, R, I, hq, hs, stream);
+        e = launch_mxfp4(MxArgs{x, W1q, xs, w1_scale, offsets, hq, R, 2 * I, H, E, tokens, T, hs}, true, false, cus,
+                         knob_tile(), stream);
     if (e == hipSuccess)
         e = launch_mxfp4(MxArgs{hq, W2q, hs, w2_scale, offsets, ws + L.y, R, H, I, E}, false, true, cus, knob_tile(), stream);
     if (e == hipSuccess) e = launch_moe_combine(ws + L.y, positions, weights, T, k, H, true, out, stream);

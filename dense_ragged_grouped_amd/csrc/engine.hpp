@@ -761,9 +761,9 @@ struct TileMma {
             fa[F][i] = __builtin_bit_cast(Frag, read_frag<BM, AK>(st.a[ST], ST & 1, ra + 32 * i, s, l));
     }
 
-    // FIRST: the tile's first products, accumulated onto zero (this is what
+    // products of sub-step F of stage ST (% 4).  FIRST: the tile's first products, accumulated onto zero (this is what
     // clears the accumulators between tiles)
-    template <int F, bool FIRST = false>
+    template <int F, int ST, bool FIRST = false>
     __device__ __forceinline__ void mfma() {
 #pragma unroll
         for (int i = 0; i < kBI; ++i)
@@ -1083,7 +1083,7 @@ struct TileRunner {
     __device__ __forceinline__ void odd_substep1(int kt) {
         issue_odd<ST, 0, N>(kt);
         mma.template read<0, (ST + 1) % kStages>(st, 0);
-        mma.template mfma<1>();
+        mma.template mfma<1, ST>();
         if constexpr (AK && BK) sched_interleave<Mma::kMfmas, Mma::kReads, N>();
     }
 
@@ -1110,7 +1110,7 @@ struct TileRunner {
         // sub-step 0: its MFMAs; the sub-step 1 fragments
         mma.template read<1, ST>(st, 1);
         if constexpr (DEF) issue_odd<STO, kS1, kS2>(kt - 1);
-        mma.template mfma<0, FIRST>();
+        mma.template mfma<0, ST, FIRST>();
         if constexpr (AK && BK) sched_interleave<Mma::kMfmas, Mma::kReads, DEF ? kS2 - kS1 : 0>();
         __builtin_amdgcn_sched_barrier(0);
         // stage kt+1 has landed for every wave, and every wave is done
@@ -1130,13 +1130,13 @@ struct TileRunner {
         } else if constexpr (kBar2) {
             if constexpr (DEF) issue_odd<STO, kS2, kNLT>(kt - 1);
             mma.template read<0, NX>(st, 0);
-            mma.template mfma<1>();
+            mma.template mfma<1, ST>();
             if constexpr (AK && BK) sched_interleave<Mma::kMfmas, Mma::kReads, DEF ? kNLT - kS2 : 0>();
         } else {
             issue<ST, AK>(la, st.a, kt);
             issue<ST, BK>(lb, st.b, kt);
             mma.template read<0, NX>(st, 0);
-            mma.template mfma<1>();
+            mma.template mfma<1, ST>();
             if constexpr (AK && BK) sched_interleave<Mma::kMfmas, Mma::kReads, NL>();
         }
         __builtin_amdgcn_sched_barrier(0);

@@ -158,18 +158,22 @@ dim3 mx_row_grid(int64_t T, int64_t K) {
 // go from memory to registers directly: lane l of a
 // v_mfma_scale_f32_16x16x128_f8f6f4 holds the block of 32 columns 32*(l/16) ..
 // +31 of row l%16, one 16-byte load, and that block's scale byte; the result
-// has token l%16 and weight rows 4*(l/16) .. +3 in lane l.  The lane's byte
-// of a dword of four scales is shifted down (one vector instruction beside a
-// 16-byte load).  Rows and columns outside the operands carry an out-of-range
-// offset and read as zero, and so do their scales (a scale byte of 255 would
-// make the zeros NaN).
+// has token l%16 and weight rows 4*(l/16) .. +3 in lane l.  A row's eight scale
+// bytes of a piece are one load; the lane's two of them are permuted into bytes
+// 0 and 1, which the two steps' MFMAs select.  Rows and columns outside the
+// operands carry an out-of-range offset and read as zero.
+
+// What a product leaves: FP32 or BF16 values, or (gated) codes and scales, those
+// of quantize_mxfp4 on the FP32 values, so that the next product's operand is made
+// here: 131072 rows of 768 save 403 MB of writes and as much reading.
+enum MxOut { kOutFp32, kOutBf16, kOutMx };
 
 __device__ __forceinline__ i32x8 fragment(u32x4 v) {   // 4-bit elements fill half of the operand's registers
     const i32x4 a = __builtin_bit_cast(i32x4, v);
     return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
-template <bool OUT_BF16, bool GATED, bool GATHERED, int NB, int MB, int W, int U>
+template <MxOut OUT, bool GATED, bool GATHERED, int NB, int MB, int W, int U>
 __device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& it, f32x4 (&sums)[W][NB][64]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -206,10 +210,11 @@ __device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& i
     const int64_t xrows = GATHERED ? a.T : a.M, wrows = (int64_t)a.E * a.N;
     const uint8_t* xs0 = a.xs + (GATHERED ? 0 : it.m0 * 8);
     const uint8_t* ws0 = a.ws + ((int64_t)it.e * a.N + n0) * 8;
+    const uint32_t pick = 0x0c0c0400u + 0x0101u * g;   // byte g of either dword
     f32x4 acc[NB][MB] = {};
     for (int k0 = wave * 128; k0 < B; k0 += 128 * W * U) {
         u32x4 fx[U][2][MB], fw[U][2][NB];
-        uint32_t sx[U][2][MB], sw[U][2][NB];
+        u32x2 sx[U][MB], sw[U][NB];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = k0 + 128 * W * u;
@@ -219,35 +224,38 @@ __device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& i
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const bool in = k + 64 * s < wk[b % NC];
-                    fw[u][s][b] = __builtin_amdgcn_raw_buffer_load_b128(b < NC ? rw : rw2,
-                                                                        in ? (uint32_t)(off[b % NC] + k + 64 * s) : kOOB, 0, 0);
-                    sw[u][s][b] = __builtin_amdgcn_raw_buffer_load_b32(
-                        b < NC ? rws : rws2, in ? (uint32_t)((16 * (b % NC) + r) * 8 + 4 * s) : kOOB, 0, 0);
-                }
+                for (int s = 0; s < 2; ++s)
+                    fw[u][s][b] = __builtin_amdgcn_raw_buffer_load_b128(
+                        b < NC ? rw : rw2, k + 64 * s < wk[b % NC] ? (uint32_t)(off[b % NC] + k + 64 * s) : kOOB, 0, 0);
+                sw[u][b] = __builtin_amdgcn_raw_buffer_load_b64(
+                    b < NC ? rws : rws2, k < wk[b % NC] ? (uint32_t)(16 * (b % NC) + r) * 8 : kOOB, 0, 0);
             }
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const bool in = k + 64 * s < xk[b];
-                    fx[u][s][b] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? (uint32_t)(xoff[b] + k + 64 * s) : kOOB, 0, 0);
-                    sx[u][s][b] = __builtin_amdgcn_raw_buffer_load_b32(rxs, in ? (uint32_t)(xs[b] + 4 * s) : kOOB, 0, 0);
-                }
+                for (int s = 0; s < 2; ++s)
+                    fx[u][s][b] = __builtin_amdgcn_raw_buffer_load_b128(
+                        rx, k + 64 * s < xk[b] ? (uint32_t)(xoff[b] + k + 64 * s) : kOOB, 0, 0);
+                sx[u][b] = __builtin_amdgcn_raw_buffer_load_b64(rxs, k < xk[b] ? (uint32_t)xs[b] : kOOB, 0, 0);
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            uint32_t px[MB], pw[NB];   // the lane's blocks of the two steps in bytes 0 and 1
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int b = 0; b < NB; ++b) pw[b] = __builtin_amdgcn_perm(sw[u][b][1], sw[u][b][0], pick);
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+            for (int m = 0; m < MB; ++m) px[m] = __builtin_amdgcn_perm(sx[u][m][1], sx[u][m][0], pick);
 #pragma unroll
-                    for (int m = 0; m < MB; ++m)
-                        acc[b][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            fragment(fw[u][s][b]), fragment(fx[u][s][m]), acc[b][m], 4, 4, 0, sw[u][s][b] >> (8 * g), 0,
-                            sx[u][s][m] >> (8 * g));
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    acc[b][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        fragment(fw[u][0][b]), fragment(fx[u][0][m]), acc[b][m], 4, 4, 0, pw[b], 0, px[m]);
+                    acc[b][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        fragment(fw[u][1][b]), fragment(fx[u][1][m]), acc[b][m], 4, 4, 1, pw[b], 1, px[m]);
+                }
+        }
     }
     // the waves' sums, one block of 16 tokens at a time
 #pragma unroll
@@ -256,6 +264,50 @@ __device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& i
 #pragma unroll
         for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[b][m];
         __syncthreads();
+        if constexpr (OUT == kOutMx) {
+            // wave 0 finishes the block's 32 columns: lane l has columns 4*(l/16) .. +3 of
+            // either half for token l%16
+            static_assert(GATED && NC == 2, "a block of 32 columns per workgroup");
+            if (wave > 0) continue;
+            f32x4 y[2];
+            uint32_t most = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                f32x4 v0 = sums[0][c][lane], v1 = sums[0][2 + c][lane];
+#pragma unroll
+                for (int v = 1; v < W; ++v) {
+                    v0 += sums[v][c][lane];
+                    v1 += sums[v][2 + c][lane];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[c][i] = gate(v0[i], v1[i]);
+                    most = max(most, __float_as_uint(y[c][i]) & 0x7FFFFFFFu);
+                }
+            }
+            most = max(most, (uint32_t)__shfl_xor((int)most, 16, 64));
+            most = max(most, (uint32_t)__shfl_xor((int)most, 32, 64));
+            const uint32_t byte = scale_byte(most);
+            const float by = scale_inverse(byte);
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = byte == 255 ? 0.f : y[i >> 2][i & 3] * by;
+            const uint32_t q = codes8(f);
+            const int64_t t = it.m0 + 16 * m + r;
+            if (t < it.hi) {
+                uint16_t* codes = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + t * (NO / 2) + n0 / 2);
+                codes[g] = (uint16_t)q;
+                codes[4 + g] = (uint16_t)(q >> 16);
+                if (g == 0) {
+                    uint8_t* scales = a.out_scales + ((n0 >> 8) * a.M + t) * 8;
+                    const int at = (int)(n0 >> 5) & 7;
+                    scales[at] = (uint8_t)byte;
+                    if (n0 + 32 >= NO)
+                        for (int i = at + 1; i < 8; ++i) scales[i] = 0;
+                }
+            }
+            continue;
+        }
         if (wave >= NC) continue;
         f32x4 c0 = sums[0][wave][lane], c1 = c0;
         if constexpr (GATED) c1 = sums[0][NC + wave][lane];
@@ -271,7 +323,7 @@ __device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& i
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = gate(c0[i], c1[i]);
             }
-            if constexpr (OUT_BF16)
+            if constexpr (OUT == kOutBf16)
                 *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + t * NO + n) =
                     u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
             else
@@ -280,7 +332,7 @@ __device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& i
     }
 }
 
-template <bool OUT_BF16, bool GATED, bool GATHERED, int NB, int W, int TOK>
+template <MxOut OUT, bool GATED, bool GATHERED, int NB, int W, int TOK>
 __global__ __launch_bounds__(64 * W, 2) void mx_rows_kernel(MxArgs a) {
     __shared__ f32x4 sums[W][NB][64];
     RowsItem it;
@@ -288,9 +340,9 @@ __global__ __launch_bounds__(64 * W, 2) void mx_rows_kernel(MxArgs a) {
     constexpr int kCols = 16 * (GATED ? NB / 2 : NB);
     if (!find_rows_item<TOK>(a.offs, a.E, a.M, (int32_t)((NO + kCols - 1) / kCols), &it)) return;
     const int64_t left = it.hi - it.m0;
-    if (left <= 16) mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 1, W, 2>(a, it, sums);
-    else if (left <= 32) mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 2, W, 1>(a, it, sums);
-    else if constexpr (TOK > 32) mx_rows_block<OUT_BF16, GATED, GATHERED, NB, 4, W, 1>(a, it, sums);
+    if (left <= 16) mx_rows_block<OUT, GATED, GATHERED, NB, 1, W, 2>(a, it, sums);
+    else if (left <= 32) mx_rows_block<OUT, GATED, GATHERED, NB, 2, W, 1>(a, it, sums);
+    else if constexpr (TOK > 32) mx_rows_block<OUT, GATED, GATHERED, NB, 4, W, 1>(a, it, sums);
 }
 
 template <bool GATED, int NB, int W, int TOK>
@@ -300,13 +352,18 @@ hipError_t launch_mx_rows(const MxArgs& a, bool bf16, hipStream_t s) {
     const int64_t most = (a.M / TOK + (a.M < a.E ? a.M : a.E)) * ntn;
     const dim3 grid((unsigned)most), block(64 * W);
     timing_mark("mx_rows_kernel", s);
-    if (a.rows) {
-        if (bf16) hipLaunchKernelGGL((mx_rows_kernel<true, GATED, true, NB, W, TOK>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((mx_rows_kernel<false, GATED, true, NB, W, TOK>), grid, block, 0, s, a);
-    } else {
-        if (bf16) hipLaunchKernelGGL((mx_rows_kernel<true, GATED, false, NB, W, TOK>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((mx_rows_kernel<false, GATED, false, NB, W, TOK>), grid, block, 0, s, a);
-    }
+    auto launch = [&](auto gathered) {
+        constexpr bool G = decltype(gathered)::value;
+        if constexpr (GATED && NB == 4)
+            if (a.out_scales) {
+                hipLaunchKernelGGL((mx_rows_kernel<kOutMx, GATED, G, NB, W, TOK>), grid, block, 0, s, a);
+                return;
+            }
+        if (bf16) hipLaunchKernelGGL((mx_rows_kernel<kOutBf16, GATED, G, NB, W, TOK>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((mx_rows_kernel<kOutFp32, GATED, G, NB, W, TOK>), grid, block, 0, s, a);
+    };
+    if (a.rows) launch(std::true_type{});
+    else launch(std::false_type{});
     timing_end(s);
     return hipGetLastError();
 }
@@ -314,16 +371,18 @@ hipError_t launch_mx_rows(const MxArgs& a, bool bf16, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // product, many rows per group
 //
-// The tile engine (engine.hpp) on 4-bit elements: a stage of 64 bytes a row is
-// 128 values, a fragment (16 bytes a lane) one block of 32, so that a lane needs
-// one scale byte per fragment and MFMA: the lower half of the lanes the blocks
-// 0 and 2 of a stage, the upper half 1 and 3.  The scales of a pair of stages
-// (eight bytes a row) are loaded beside the pair's codes and land behind them
-// in its buffer.  A lane reads the four bytes of a stage for two of its row
-// blocks and permutes its half's bytes into one register: byte 0 and 1 are the
-// two blocks' scales of sub-step 0, byte 2 and 3 those of sub-step 1, and the
-// MFMAs select the byte (a register and a shift for each block would be twice
-// the instructions, and the gated 256x256 tile would spill).
+// The tile engine (engine.hpp) on 4-bit elements: a pair of stages is 256 values
+// (128 bytes, eight blocks) of a row and has four sub-steps, in each of which the
+// MFMA takes one block from either half of the lanes.  Which one is free, as long
+// as both operands agree: sub-step q takes block q and, in the upper half, block
+// 4 + q.  The blocks a lane sees in a pair are then neighbours, and their four
+// scale bytes one aligned dword, which the four sub-steps' MFMAs select from by an
+// immediate: no instruction handles a scale but the LDS read.  (In the order of
+// the 8-bit product the scales of a stage had to be permuted into place, and the
+// wait for them stood among the MFMAs: 8192x8192x8192 259 to 273 us.)  The scales
+// of a pair (eight bytes a row) are loaded beside its codes and land behind them
+// in its buffer.  A pair of stages lands as one, so that the upper half may read
+// ahead of the stage.
 
 struct Mxfp4 {};
 
@@ -339,7 +398,7 @@ constexpr int mx_buffer_bytes(int rows) { return rows * (4 * kStageK + 8); }   /
                       {(lds_t*)name##_b0, (lds_t*)name##_b0, (lds_t*)name##_b1, (lds_t*)name##_b1}}
 
 // The codes as StageLoader brings them, then ROWS/32 wave instructions of 4 bytes
-// a lane: lane l of instruction g has the scales of stage l%2 of row 32 g + l/2.
+// a lane: lane l of instruction g has dword l%2 of row 32 g + l/2.
 // An operand that is not gathered says in `of` which row of its scales is its
 // first.
 template <int ROWS, int WAVES, bool PAIRED, bool GATHERED>
@@ -393,22 +452,24 @@ struct MxLoader : StageLoader<ROWS, true, WAVES, PAIRED, GATHERED> {
     }
 };
 
+// the fragment of block 2 (ST % 2) + s, in the upper half of the lanes 4 + that
+template <int ST>
+__device__ __forceinline__ i32x4 mx_read_frag(const lds_t* buf, int rb, int s, int l) {
+    const int row = rb + (l & 31), c = 4 * (l >> 5) + 2 * (ST & 1) + s;
+    return *reinterpret_cast<const __attribute__((address_space(3))) i32x4*>(buf + row * (4 * kStageK) + ((c ^ swzK(row)) << 4));
+}
+
 // The products of a tile (TileMma's wave grid and accumulator layout).
 template <int BM, int BN, int WAVES>
 struct MxMma {
     using Grid = TileMma<BM, BN, true, true, WAVES, Bf16>;
     __device__ static __forceinline__ int wave_row(int wave) { return Grid::wave_row(wave); }
     __device__ static __forceinline__ int wave_col(int wave) { return Grid::wave_col(wave); }
-    static constexpr int kBI = Grid::kBI, kBJ = Grid::kBJ;
+    static constexpr int kBI = Grid::kBI, kBJ = Grid::kBJ, kBN = BN;
     static constexpr int kReads = kBI + kBJ, kMfmas = kBI * kBJ;
     f32x16 acc[kBI][kBJ];
     i32x4 fa[2][kBI], fb[2][kBJ];
-    static_assert(kBI % 2 == 0 && kBJ % 2 == 0, "scales are held for two blocks of rows");
-    uint32_t sa[2][kBI / 2], sb[2][kBJ / 2];
-    // Stage of the tile that is read next, stages a tile runs, blocks of a row.
-    // The bytes of a stage past the row's last block may hold anything: they
-    // are cleared, since a scale of 255 would make the zeros there NaN.
-    int at, stages, blocks;
+    uint32_t sa[2][kBI], sb[2][kBJ];   // of the pair of stages in buffer 0 and 1
 
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -424,58 +485,33 @@ struct MxMma {
         const int l = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int ra = wave_row(wave), rb = wave_col(wave);
-        fa[F][0] = __builtin_bit_cast(i32x4, read_frag<BM, true>(st.a[ST], ST & 1, ra, s, l));
-#pragma unroll
-        for (int j = 0; j < kBJ; ++j)
-            fb[F][j] = __builtin_bit_cast(i32x4, read_frag<BN, true>(st.b[ST], ST & 1, rb + 32 * j, s, l));
-#pragma unroll
-        for (int i = 1; i < kBI; ++i)
-            fa[F][i] = __builtin_bit_cast(i32x4, read_frag<BM, true>(st.a[ST], ST & 1, ra + 32 * i, s, l));
-        if constexpr (F == 1) {
-#pragma unroll
-            for (int i = 0; i < kBI / 2; ++i) sa[1][i] = sa[0][i];
-#pragma unroll
-            for (int j = 0; j < kBJ / 2; ++j) sb[1][j] = sb[0][j];
-        } else {
-            const int half = l >> 5, left = blocks - 4 * at;
-            at = at + 1 == stages ? 0 : at + 1;
-            // byte selectors: 0 to 3 of the first block's dword, 4 to 7 of the second's; 0x0c is zero
-            const uint32_t sel = (half < left ? 0x0400u + 0x0101u * half : 0x0c0cu) |
-                                 (2 + half < left ? 0x06020000u + 0x01010000u * half : 0x0c0c0000u);
+        if constexpr (F == 0 && !(ST & 1)) {
             typedef const __attribute__((address_space(3))) uint32_t lds_u32;
-            auto two = [&](const lds_t* scales, int row) {
-                const lds_u32* p = reinterpret_cast<lds_u32*>(scales + (row + (l & 31)) * 8 + 4 * (ST & 1));
-                return __builtin_amdgcn_perm(p[64], p[0], sel);   // 32 rows on: 64 dwords
-            };
+            const int o = (l & 31) * 8 + 4 * (l >> 5);   // consecutive dwords over the lanes: no bank conflict
 #pragma unroll
-            for (int i = 0; i < kBI / 2; ++i) sa[0][i] = two(st.a[ST] + BM * 4 * kStageK, ra + 64 * i);
+            for (int i = 0; i < kBI; ++i)
+                sa[ST >> 1][i] = *reinterpret_cast<lds_u32*>(st.a[ST] + BM * 4 * kStageK + (ra + 32 * i) * 8 + o);
 #pragma unroll
-            for (int j = 0; j < kBJ / 2; ++j) sb[0][j] = two(st.b[ST] + BN * 4 * kStageK, rb + 64 * j);
+            for (int j = 0; j < kBJ; ++j)
+                sb[ST >> 1][j] = *reinterpret_cast<lds_u32*>(st.b[ST] + BN * 4 * kStageK + (rb + 32 * j) * 8 + o);
         }
+        fa[F][0] = mx_read_frag<ST>(st.a[ST], ra, s, l);
+#pragma unroll
+        for (int j = 0; j < kBJ; ++j) fb[F][j] = mx_read_frag<ST>(st.b[ST], rb + 32 * j, s, l);
+#pragma unroll
+        for (int i = 1; i < kBI; ++i) fa[F][i] = mx_read_frag<ST>(st.a[ST], ra + 32 * i, s, l);
     }
 
-    // the byte selections are immediates
-    template <int F, bool FIRST, int BA, int BB>
-    __device__ __forceinline__ void product(f32x16& c, i32x4 b, i32x4 a, uint32_t scale_b, uint32_t scale_a) {
-        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fragment(__builtin_bit_cast(u32x4, b)),
-                                                            fragment(__builtin_bit_cast(u32x4, a)), FIRST ? f32x16{} : c, 4, 4,
-                                                            2 * F + BB, scale_b, 2 * F + BA, scale_a);
-    }
-    template <int F, bool FIRST = false>
+    template <int F, int ST, bool FIRST = false>
     __device__ __forceinline__ void mfma() {
+        constexpr int kByte = 2 * (ST & 1) + F;
 #pragma unroll
-        for (int i = 0; i < kBI; i += 2) {
+        for (int i = 0; i < kBI; ++i)
 #pragma unroll
-            for (int j = 0; j < kBJ; j += 2) {
-                product<F, FIRST, 0, 0>(acc[i][j], fb[F][j], fa[F][i], sb[F][j / 2], sa[F][i / 2]);
-                product<F, FIRST, 0, 1>(acc[i][j + 1], fb[F][j + 1], fa[F][i], sb[F][j / 2], sa[F][i / 2]);
-            }
-#pragma unroll
-            for (int j = 0; j < kBJ; j += 2) {
-                product<F, FIRST, 1, 0>(acc[i + 1][j], fb[F][j], fa[F][i + 1], sb[F][j / 2], sa[F][i / 2]);
-                product<F, FIRST, 1, 1>(acc[i + 1][j + 1], fb[F][j + 1], fa[F][i + 1], sb[F][j / 2], sa[F][i / 2]);
-            }
-        }
+            for (int j = 0; j < kBJ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fragment(__builtin_bit_cast(u32x4, fb[F][j])), fragment(__builtin_bit_cast(u32x4, fa[F][i])),
+                    FIRST ? f32x16{} : acc[i][j], 4, 4, kByte, sb[ST >> 1][j], kByte, sa[ST >> 1][i]);
     }
 };
 
@@ -493,12 +529,71 @@ namespace {
 
 constexpr int mx_ep_rows(int bm, int bn) { return bm == 128 && bn == 256 ? 16 : 8; }   // what the scales leave room for
 
+// Write a gated tile as codes and scales: value(i, j, q) as store_tile_values
+// takes it.  A row's 32 columns are held by two lanes, 16 values each, in runs of
+// four that alternate; after their halves are exchanged each lane has eight
+// neighbouring bytes of codes.  Columns past the tile's are zeros (their operands
+// are), so their scales are 0; behind the last tile's the rest of the scales'
+// eight bytes is cleared too.
+template <class Mma, int NJ, class Value>
+__device__ __forceinline__ void store_tile_mx(Value value, int rb, const MxArgs& a, int64_t o0, int64_t o1, int rows, int cols) {
+    static_assert(NJ == 2 || NJ == 1, "one or two blocks per wave and row");
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ra = Mma::wave_row(wave), r = lane & 31, h = lane >> 5;
+    const int64_t I = a.N / 2;
+#pragma unroll
+    for (int i = 0; i < Mma::kBI; ++i) {
+        const int row = ra + 32 * i + r;
+        const bool live = row < rows;
+        uint8_t* codes = static_cast<uint8_t*>(a.out) + (o0 + row) * (I / 2) + (o1 + rb) / 2 + 8 * h;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            float f[16];
+            uint32_t most = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4 y = value(i, j, q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[4 * q + e] = y[e];
+                    most = max(most, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+                }
+            }
+            most = max(most, (uint32_t)__shfl_xor((int)most, 32, 64));
+            const uint32_t b = scale_byte(most);
+            const float by = scale_inverse(b);
+            bytes |= b << (8 * j);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] = b == 255 ? 0.f : f[e] * by;
+            // runs of four values, two bytes each: 0 and 1, then 2 and 3
+            const uint32_t lo = codes8({f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]});
+            const uint32_t hi = codes8({f[8], f[9], f[10], f[11], f[12], f[13], f[14], f[15]});
+            // lower lanes: their own runs 0, 1 and the upper lane's; upper lanes: the lower lane's runs 2, 3 and their own
+            const auto x = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
+            const u32x2 d = {__builtin_amdgcn_perm(x[1], x[0], 0x05040100u), __builtin_amdgcn_perm(x[1], x[0], 0x07060302u)};
+            if (live && rb + 32 * j < cols) *reinterpret_cast<u32x2*>(codes + 16 * j) = d;
+        }
+        if (live && h == 0) {
+            const int64_t c = o1 + rb;
+            uint8_t* scales = a.out_scales + ((c >> 8) * a.M + o0 + row) * 8;
+            const int at = (int)(c >> 5) & 7;
+            if constexpr (NJ == 2) *reinterpret_cast<uint16_t*>(scales + at) = (uint16_t)bytes;
+            else scales[at] = (uint8_t)bytes;
+            if (o1 + cols == I && rb + 32 * NJ >= Mma::kBN / 2)   // the last columns' wave of the last tile
+                for (int e = at + NJ; e < 8; e += 2) *reinterpret_cast<uint16_t*>(scales + e) = 0;
+        }
+    }
+}
+
 // The 8-bit product's walk and epilogue without scales of whole rows.
-template <int BM, int BN, bool OUT_BF16, bool GATED, bool GATHERED, int WAVES>
+template <int BM, int BN, MxOut OUT, bool GATED, bool GATHERED, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, BM == 128 && BN == 128 ? 2 : 1) void mx_tile_kernel(MxArgs a) {
     DRGG_MX_STAGES(BM, BN, stg);
     __shared__ SchedOf<16, BM == 128 && BN == 128 ? kMx128MaxExperts : kMaxExperts> sch;
-    __shared__ __attribute__((aligned(16))) char ep[WAVES * mx_ep_rows(BM, BN) * 128];
+    __shared__ __attribute__((aligned(16))) char ep[OUT == kOutMx ? 16 : WAVES * mx_ep_rows(BM, BN) * 128];
     using Runner = TileRunner<BM, BN, true, true, WAVES, Mxfp4, GATED, GATHERED>;
     using Mma = typename Runner::Mma;
     constexpr int BC = GATED ? BN / 2 : BN;             // output columns per tile
@@ -537,15 +632,17 @@ __global__ __launch_bounds__(64 * WAVES, BM == 128 && BN == 128 ? 2 : 1) void mx
                              : mma.acc[i][j][4 * q + r];
             return y;
         };
-        const int64_t o = t.o0 * NO + t.o1;
-        void* base = OUT_BF16 ? (void*)(static_cast<uint16_t*>(a.out) + o) : (void*)(static_cast<float*>(a.out) + o);
-        store_tile_values<OUT_BF16, mx_ep_rows(BM, BN), Mma, NJ>(value, rb, (lds_t*)ep, base, NO, t.rows, t.cols);
+        if constexpr (OUT == kOutMx) {
+            store_tile_mx<Mma, NJ>(value, rb, a, t.o0, t.o1, t.rows, t.cols);
+        } else {
+            constexpr bool kBf16 = OUT == kOutBf16;
+            const int64_t o = t.o0 * NO + t.o1;
+            void* base = kBf16 ? (void*)(static_cast<uint16_t*>(a.out) + o) : (void*)(static_cast<float*>(a.out) + o);
+            store_tile_values<kBf16, mx_ep_rows(BM, BN), Mma, NJ>(value, rb, (lds_t*)ep, base, NO, t.rows, t.cols);
+        }
     };
     Runner runner;
     runner.st = stg;
-    runner.mma.at = 0;
-    runner.mma.stages = Runner::round4((int)((K2 + kStageK - 1) / kStageK));
-    runner.mma.blocks = (int)(a.K / 32);
     runner.la.all_scales = a.xs;
     runner.la.scale_step = 8 * (GATHERED ? a.T : a.M);
     runner.lb.all_scales = a.ws;
@@ -558,12 +655,17 @@ template <int BM, int BN, int WAVES, bool GATED, bool GATHERED>
 void launch_mx_tile_t(const MxArgs& a, bool bf16, dim3 grid, hipStream_t s) {
     const dim3 block(64 * WAVES);
     constexpr bool kBf16 = !GATED || BN >= 256;   // a gated 128x128 tile has 32 columns per wave, half a BF16 line
-    if constexpr (kBf16)
-        if (bf16) {
-            hipLaunchKernelGGL((mx_tile_kernel<BM, BN, true, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+    if constexpr (GATED)
+        if (a.out_scales) {
+            hipLaunchKernelGGL((mx_tile_kernel<BM, BN, kOutMx, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
             return;
         }
-    hipLaunchKernelGGL((mx_tile_kernel<BM, BN, false, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+    if constexpr (kBf16)
+        if (bf16) {
+            hipLaunchKernelGGL((mx_tile_kernel<BM, BN, kOutBf16, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
+            return;
+        }
+    hipLaunchKernelGGL((mx_tile_kernel<BM, BN, kOutFp32, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
 }
 
 template <int BM, int BN, int WAVES>
@@ -611,7 +713,7 @@ hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, 
 }
 
 hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s) {
-    const Int8Program p = mxfp4_program(a.E, a.M, a.N, a.K, gated, bf16, forced_tile);
+    const Int8Program p = mxfp4_program(a.E, a.M, a.N, a.K, gated, bf16, a.out_scales != nullptr, forced_tile);
     if (p.tile == kTileAuto)
         return gated ? launch_mx_program<true>(a, p, bf16, s) : launch_mx_program<false>(a, p, bf16, s);
     const int64_t cols_out = gated ? a.N / 2 : a.N, bc = gated ? 128 : 256;

@@ -574,11 +574,14 @@ inline Int8Program int8_program(int64_t E, int64_t M, int64_t N, int64_t K, bool
 
 // The same for a 4-bit product: its rows are K/2 bytes, and a step of 64 bytes
 // takes as long whatever the elements.  128x128 tiles have room for
-// kMx128MaxExperts groups beside the scales, two of them on a CU.
+// kMx128MaxExperts groups beside the scales, two of them on a CU.  codes: the
+// result is quantised, in blocks of 32 columns of one workgroup.
 constexpr int kMx128MaxExperts = 992;
-inline Int8Program mxfp4_program(int64_t E, int64_t M, int64_t N, int64_t K, bool gated, bool bf16, int forced_tile) {
+inline Int8Program mxfp4_program(int64_t E, int64_t M, int64_t N, int64_t K, bool gated, bool bf16, bool codes,
+                                 int forced_tile) {
     Int8Program p = int8_program(E, M, N, K / 2, gated, bf16, forced_tile);
     if (p.tile == kTile128x128 && E > kMx128MaxExperts) p.tile = kTile128x256;
+    if (codes && p.tile == kTileAuto && p.nb < 4) p.nb = 4;
     return p;
 }
 

@@ -671,8 +671,8 @@ drgg_status moe_route_scores_grad(const float *dweights, const float *logits, co
  * their negatives.  b = 255 is NaN.
  *   codes   [rows, K/2] bytes, the even column in the low half
  *   scales  [ceil(K/256), rows, 8] bytes: the scales of 256 columns side by
- *           side, row after row.  The bytes past column K may hold anything
- *           (the quantisation writes 0).
+ *           side, row after row.  The bytes past column K must not be 255
+ *           (the quantisation writes 0): they scale zeros.
  * Rows stacked in more dimensions ([E, N]) are E*N rows.
  *
  * Quantisation of X [T, K] (BF16 or FP32): with m = max|x| of a block,
@@ -710,9 +710,9 @@ drgg_status gemm_mxfp4(const uint8_t *Xq, const uint8_t *x_scale, const uint8_t 
  * moe_ffn_int8's block on 4-bit weights, in one call: moe_route_scores (or, with
  * scoring NULL, moe_route with renormalize = 1), quantize_mxfp4 of X [T,H] BF16,
  * the gated product of its rows in the grouped order with W1 (E*2I rows of H,
- * gate rows then up rows), quantize_mxfp4 of its FP32 result, the product with
- * W2 (E*H rows of I; BF16), and moe_combine into out [T,H] BF16.  The same
- * results as the single calls.  H and I multiples of 32, T*H/2 <= 2^31 - 4097.
+ * gate rows then up rows), quantize_mxfp4 of its FP32 result (in the product's
+ * kernel), the product with W2 (E*H rows of I; BF16), and moe_combine into out
+ * [T,H] BF16.  The same results as the single calls.  H and I multiples of 32, T*H/2 <= 2^31 - 4097.
  * Workspace: moe_ffn_mxfp4_workspace_size bytes, 16-byte aligned, no
  * initialisation; calls in flight at once must not share it.
  */

@@ -32,7 +32,7 @@ static const char* ws_lo;
 static const char* ws_hi;
 static std::vector<Span> routed;   // written by the selection, read to the end
 static std::vector<Span> alive;    // the block's rows that a later step still reads
-static Span x, xs, h, hq, hs, y;
+static Span x, xs, hq, hs, y;
 static int step;
 static bool scored;
 static void fresh(const Span& s) {
@@ -85,17 +85,10 @@ hipError_t launch_quantize_mxfp4(const void* X, bool bf16, int64_t T, int64_t K,
     fresh(c);
     EXPECT(c.apart(s));
     fresh(s);
-    if (bf16) {
-        EXPECT(step++ == 1);
-        x = c;
-        xs = s;
-        alive = {x, xs};
-    } else {
-        EXPECT(step++ == 3 && X == h.lo);
-        hq = c;
-        hs = s;
-        alive = {hq, hs};
-    }
+    EXPECT(step++ == 1 && bf16);
+    x = c;
+    xs = s;
+    alive = {x, xs};
     return hipSuccess;
 }
 hipError_t launch_dequantize_mxfp4(const uint8_t*, const uint8_t*, int64_t, int64_t, bool, void*, hipStream_t) {
@@ -103,13 +96,16 @@ hipError_t launch_dequantize_mxfp4(const uint8_t*, const uint8_t*, int64_t, int6
 }
 hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, int, int, hipStream_t) {
     if (gated) {
-        EXPECT(step++ == 2 && !bf16 && a.rows);
+        EXPECT(step++ == 2 && !bf16 && a.rows && a.out_scales);
         EXPECT((const char*)a.X == x.lo && (const char*)a.xs == xs.lo);
-        h = Span(a.out, a.M * (a.N / 2) * 4);
-        fresh(h);
-        alive = {h};
+        hq = Span(a.out, a.M * (a.N / 4));
+        fresh(hq);
+        hs = Span(a.out_scales, scale_bytes(a.M, a.N / 2));
+        fresh(hs);
+        EXPECT(hq.apart(hs));
+        alive = {hq, hs};
     } else {
-        EXPECT(step++ == 4 && bf16 && !a.rows);
+        EXPECT(step++ == 3 && bf16 && !a.rows && !a.out_scales);
         EXPECT((const char*)a.X == hq.lo && (const char*)a.xs == hs.lo);
         y = Span(a.out, a.M * a.N * 2);
         fresh(y);
@@ -119,7 +115,7 @@ hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, int, int, hipStr
 }
 hipError_t launch_moe_combine(const void* rows, const int32_t*, const float*, int64_t, int32_t, int64_t, bool bf16, void*,
                               hipStream_t) {
-    EXPECT(step++ == 5 && bf16 && rows == y.lo);
+    EXPECT(step++ == 4 && bf16 && rows == y.lo);
     return hipSuccess;
 }
 hipError_t launch_moe_gate_int8(const void*, const int32_t*, const float*, int64_t, int32_t, int64_t, void*, int8_t*, float*,
@@ -146,7 +142,7 @@ int main() {
             scored = by;
             EXPECT(moe_ffn_mxfp4(A, f, b, b, b, b, v[0], (int32_t)v[1], (int32_t)v[2], v[3], v[4], by ? &c : nullptr, A,
                                  const_cast<char*>(ws_lo), need, nullptr) == DRGG_OK);
-            EXPECT(step == 6);
+            EXPECT(step == 5);
             EXPECT(moe_ffn_mxfp4(A, f, b, b, b, b, v[0], (int32_t)v[1], (int32_t)v[2], v[3], v[4], by ? &c : nullptr, A,
                                  const_cast<char*>(ws_lo), need - 1, nullptr) == DRGG_EWORKSPACE);
         }

@@ -185,12 +185,12 @@ GROUPED = [([1], 8, 32), ([3], 16, 64), ([0, 5, 0], 24, 96), ([17, 1, 33, 0, 64,
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("gated", [False, True])
 def test_grouped_exact(drgg, counts, N, K, dtype, gated):
-    """Sums that fit 24 bits are exact; the bytes past a row's last scale hold 255."""
+    """Sums that fit 24 bits are exact; the bytes past a row's last scale hold anything but 255."""
     rng = np.random.default_rng(N + K)
     N = 2 * N if gated else N
     E, M = len(counts), sum(counts)
-    x, xs, xv = operand(rng, M, K, fill=255)
-    w, ws, wv = operand(rng, E, N, K, fill=255)
+    x, xs, xv = operand(rng, M, K, fill=254)
+    w, ws, wv = operand(rng, E, N, K, fill=254)
     offsets = counts_to_offsets(counts)
     y, mag = grouped64(xv, wv, offsets, N)
     assert mag.max() * 64 < 2 ** 24   # multiples of (2^-2 * 0.5)^2
@@ -271,13 +271,13 @@ def forced(drgg):
 @pytest.mark.parametrize("gated,gathered", [(False, False), (True, False), (False, True), (True, True)])
 def test_every_tile(drgg, forced, tile, counts, N, K, gated, gathered):
     """The tiles, whatever the rule would take: several per workgroup, cut at every edge, K within one stage and past
-    whole ones, the bytes past a row's last scale 255."""
+    whole ones, the bytes past a row's last scale not 0."""
     rng = np.random.default_rng(N + K)
     N = 2 * N if gated else N
     E, M = len(counts), sum(counts)
     T = M // 2 + 3 if gathered else M
-    x, xs, xv = operand(rng, T, K, fill=255)
-    w, ws, wv = operand(rng, E, N, K, fill=255)
+    x, xs, xv = operand(rng, T, K, fill=254)
+    w, ws, wv = operand(rng, E, N, K, fill=254)
     offsets = counts_to_offsets(counts)
     rows = None
     if gathered:
@@ -354,12 +354,27 @@ def block(drgg, T, E, H, I, seed=0):
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 64, 32), (8, 32, 4, 2048, 768), (130, 5, 3, 288, 160), (1500, 8, 3, 544, 416)])
 @pytest.mark.parametrize("scored", [False, True])
 def test_ffn_is_its_parts(drgg, T, E, k, H, I, scored):
+    ffn_is_its_parts(drgg, T, E, k, H, I, scored)
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("T,E,k,H,I", [(40, 3, 2, 96, 32), (300, 5, 3, 288, 160), (900, 2, 2, 544, 416), (700, 40, 1, 64, 352)])
+def test_ffn_is_its_parts_in_every_tile(drgg, forced, tile, T, E, k, H, I):
+    """The activation's codes and scales are made in the first product's epilogue: their bytes past a row's end have to
+    be written too, whatever the workspace held."""
+    forced(tile)
+    ffn_is_its_parts(drgg, T, E, k, H, I, True)
+
+
+def ffn_is_its_parts(drgg, T, E, k, H, I, scored):
     from dense_ragged_grouped_amd import moe
     X, logits, bias, W1, W2 = block(drgg, T, E, H, I)
     w1, s1 = moe.quantize_weights_mxfp4(W1)
     w2, s2 = moe.quantize_weights_mxfp4(W2)
     sc = drgg.Scoring(bias=bias, scale=2.5) if scored else None
-    got = moe.ffn_mxfp4(X, logits, w1, s1, w2, s2, k, scoring=sc)
+    dirty = torch.full((drgg.ffn_mxfp4_workspace_size(T, E, k, H, I),), 255, dtype=torch.uint8, device="cuda")
+    got = drgg.moe_ffn_mxfp4(X, logits, w1, s1, w2, s2, k, scoring=sc, workspace=dirty)
+    assert torch.equal(got, moe.ffn_mxfp4(X, logits, w1, s1, w2, s2, k, scoring=sc))
     r = drgg.moe_route_scores(logits, k, sc) if scored else drgg.moe_route(logits, k)
     x, xs = drgg.quantize_mxfp4(X)
     h = drgg.grouped_gemm_mxfp4(x, xs, w1, s1, r.group_offsets, gated=True, rows=r.tokens, out_dtype=torch.float32)
