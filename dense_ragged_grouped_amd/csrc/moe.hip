@@ -319,6 +319,36 @@ __device__ __forceinline__ F score_value(float x, float bias, F most, F total) {
     return ((x == -INFINITY) | (bias == -INFINITY)) ? (F)-INFINITY : v;
 }
 
+// The same in FP32 with the hardware's exponential and reciprocal, within
+// `off` (select_by_scores) of it; inverse = 1 / total.
+template <bool SIGMOID>
+__device__ __forceinline__ float score_value32(float x, float bias, float most, float inverse) {
+    float v;
+    if constexpr (SIGMOID) {
+        const float e = __builtin_amdgcn_exp2f(fabsf(x) * -1.44269504f), q = __builtin_amdgcn_rcpf(1.f + e);
+        v = (x < 0 ? e * q : q) + bias;
+    } else {
+        v = __builtin_amdgcn_exp2f((x - most) * 1.44269504f) * inverse + bias;
+    }
+    return ((x == -INFINITY) | (bias == -INFINITY)) ? -INFINITY : v;
+}
+
+// the two largest of two pairs' four keys
+__device__ __forceinline__ void merge_two(uint32_t& one, uint32_t& two, uint32_t o1, uint32_t o2) {
+    two = max(min(one, o1), max(two, o2));
+    one = max(one, o1);
+}
+template <int CTRL>
+__device__ __forceinline__ void merge_lanes(uint32_t& one, uint32_t& two) {
+    merge_two(one, two, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)one, CTRL, 0xF, 0xF, false),
+              (uint32_t)__builtin_amdgcn_update_dpp(0, (int)two, CTRL, 0xF, 0xF, false));
+}
+// a group's value from its two largest keys (0: none)
+__device__ __forceinline__ uint32_t group_key(uint32_t one, uint32_t two, int best) {
+    const uint32_t sum = order_key(key_value(one) + key_value(two));
+    return best == 2 && two != 0 && key_value(two) != -INFINITY ? sum : one;
+}
+
 __device__ __forceinline__ uint64_t order_key64(double v) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0), key = u >> 63 ? ~u : u | 1ull << 63;
     return v != v ? ~0ull : key;
@@ -326,13 +356,32 @@ __device__ __forceinline__ uint64_t order_key64(double v) {
 __device__ __forceinline__ double key_value64(uint64_t k) {
     return __builtin_bit_cast(double, k >> 63 ? k & ~(1ull << 63) : ~k);   // NaN: all ones, a NaN
 }
+// fn(v, v of other lanes) over the wave, in all lanes: rotations in the rows of
+// 16, then exchanges of rows and halves, all in the vector unit (shuffles through
+// LDS would wait some hundred cycles each, twelve times)
+template <class Fn>
+__device__ __forceinline__ uint64_t wave_reduce64(uint64_t v, Fn fn) {
+    auto both = [](uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; };
+    v = fn(v, both(row_rotate<8>((uint32_t)v), row_rotate<8>((uint32_t)(v >> 32))));
+    v = fn(v, both(row_rotate<4>((uint32_t)v), row_rotate<4>((uint32_t)(v >> 32))));
+    v = fn(v, both(row_rotate<2>((uint32_t)v), row_rotate<2>((uint32_t)(v >> 32))));
+    v = fn(v, both(row_rotate<1>((uint32_t)v), row_rotate<1>((uint32_t)(v >> 32))));
+    // even rows on one side, odd rows on the other; then the halves
+    auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+    v = fn(both(lo[0], hi[0]), both(lo[1], hi[1]));
+    lo = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+    hi = __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+    return fn(both(lo[0], hi[0]), both(lo[1], hi[1]));
+}
 __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint64_t o = __shfl_xor((unsigned long long)v, m, 64);
-        v = o > v ? o : v;
-    }
-    return v;
+    return wave_reduce64(v, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+}
+// the same bits in all lanes: every lane adds the same pairs of pairs
+__device__ __forceinline__ double wave_sum64(double v) {
+    return __builtin_bit_cast(double, wave_reduce64(__builtin_bit_cast(uint64_t, v), [](uint64_t a, uint64_t b) {
+        return __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b));
+    }));
 }
 
 // The largest of a wave's N*64 keys (lane l's i-th is expert 64 i + l), which
@@ -370,7 +419,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const ScoreArgs& c,
     }
     double most = 0, total = 1;
     if constexpr (!SIGMOID) {
-        for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+        top = (float)key_value64(wave_max64(order_key64(top)));
         most = top == -INFINITY ? 0.0 : (double)top;
         total = 0;
 #pragma unroll
@@ -378,7 +427,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const ScoreArgs& c,
             total += exp((double)x[i] - most);
             __builtin_amdgcn_sched_barrier(0);
         }
-        for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m, 64);
+        total = wave_sum64(total);
     }
     uint64_t key[N];
 #pragma unroll
@@ -426,7 +475,7 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const ScoreArgs& c,
 // largest finite |bias|.
 template <int V, int S, bool SIGMOID>
 __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const ScoreArgs& c, const float* bias, float far,
-                                                 unsigned long long* mask, int tl) {
+                                                 unsigned long long* mask, int tl, int32_t (&mine)[S]) {
     // opaque: what depends on the lane alone would otherwise be hoisted out of
     // the loop over the block's tokens and held in registers
     int lane = threadIdx.x & 63;
@@ -448,74 +497,129 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
         if (most == -INFINITY) most = 0.f;
         total = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) total += key[i] ? expf(key_value(key[i]) - most) : 0.f;
+        for (int i = 0; i < V; ++i) total += key[i] ? __builtin_amdgcn_exp2f((key_value(key[i]) - most) * 1.44269504f) : 0.f;
         total = row_sum(total);
     }
-    // An FP32 value's error, with half steps u: a sigmoid's exponential is
-    // within 2 u of itself and two roundings follow, 2.5 u in all; a softmax
-    // score p has u |x - most| p <= 0.37 u from its exponent and at most
-    // (V + 16) u p from the exponential, the sum and the division; the bias adds
-    // a rounding, u |v|.
-    const float off = SIGMOID ? 2.5f * kUnit : (1.f + (V + 16) / total) * kUnit;
+    const float inverse = SIGMOID ? 1.f : 1.f / total;
+    // An FP32 value's error, with half steps u = 2^-24 (the hardware's
+    // exponential and reciprocal are within 2 u of themselves).  Sigmoid with
+    // e = exp(-|x|): the exponent is rounded, u |x| e <= 0.37 u, e itself 2 u e
+    // (both times at most e' = 1 / (1 + e)^2 <= 1 where e is small and 1/4 where
+    // it is 1: 0.9 u together), 1 + e u, the reciprocal 2 u, e q u / 2: 4.5 u in
+    // all.  Softmax: two roundings of the exponent, 2 u |x - most| p <= 0.74 u,
+    // and at most (V + 16) u p from the exponential, the sum and its inverse.
+    // The bias adds a rounding, u |v|.
+    const float off = SIGMOID ? 4.5f * kUnit : (1.f + (V + 16) * inverse) * kUnit;
     bool close = false;
     auto near = [&](uint32_t hi, uint32_t lo, float within) {
         const float h = key_value(hi), d = h - key_value(lo);   // infinity or NaN unless both are finite
         return fabsf(h) < INFINITY && d <= within;
     };
-    unsigned long long open = ~0ull;
-    if (c.groups > 1) {
-        // sixteen lanes take the groups in turn
-        const int size = E / c.groups;
-        uint32_t rank[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int g = 16 * q + l;
-            rank[q] = 0;
-            if (live && g < c.groups) {
-                uint32_t one = 0, two = 0;
-                for (int e = g * size; e < (g + 1) * size; ++e) {
-                    const float x = row[e], b = bias[e];
-                    const uint32_t v = order_key(score_value<SIGMOID, float>(x, b, most, total));
-                    two = max(two, min(one, v));
-                    one = max(one, v);
-                }
-                rank[q] = c.best == 2 && two != 0 && key_value(two) != -INFINITY ? order_key(key_value(one) + key_value(two)) : one;
-            }
-        }
-        const float within = (4.f * off + 8.f * kUnit * (1.f + far)) * 1.01f;
-        open = 0;
-        uint32_t last = 0;
-        for (int j = 0; j < c.top_groups; ++j) {
-            last = row_max(max(max(rank[0], rank[1]), max(rank[2], rank[3])));
-            uint32_t at = 64;
-#pragma unroll
-            for (int q = 3; q >= 0; --q) at = rank[q] == last ? (uint32_t)(16 * q + l) : at;
-            at = row_min(at);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) rank[q] = at == (uint32_t)(16 * q + l) ? 0u : rank[q];
-            open |= 1ull << (at & 63);
-        }
-        const uint32_t left = row_max(max(max(rank[0], rank[1]), max(rank[2], rank[3])));
-        close = left != 0 && near(last, left, within);
-    }
-    // e / size for e < 1024 by a multiplication
-    const uint32_t by_size = c.groups > 1 ? ((1u << 20) + E / c.groups - 1) / (E / c.groups) : 0u;
-    if (!c.by_logits) {   // in place, four experts at a time
+    if (!c.by_logits) {   // values in the logits' place, four experts at a time
 #pragma unroll
         for (int q = 0; q < V / 4; ++q) {
             const f32x4 b = *reinterpret_cast<const f32x4*>(&bias[64 * q + 4 * l]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t e = 64 * q + 4 * l + i;
-                const float x = key_value(key[4 * q + i]);
-                const uint32_t v = order_key(score_value<SIGMOID, float>(x, b[i], most, total));
-                const bool in = key[4 * q + i] != 0 && (c.groups == 1 || (open >> ((e * by_size) >> 20 & 63) & 1));
-                key[4 * q + i] = in ? v : 0u;
+                const uint32_t v = order_key(score_value32<SIGMOID>(key_value(key[4 * q + i]), b[i], most, inverse));
+                key[4 * q + i] = key[4 * q + i] != 0 ? v : 0u;
             }
             if constexpr (V > 16) __builtin_amdgcn_sched_barrier(0);   // side by side they do not fit the registers
         }
     }
-    int32_t mine[S];
+    if (c.groups > 1) {
+        const int size = E / c.groups;
+        const float within = (4.f * off + 8.f * kUnit * (1.f + far)) * 1.01f;
+        unsigned long long open = 0;
+        uint32_t last = 0, left;
+        if (size >= 4 && (size & (size - 1)) == 0) {
+            // Groups of 4, 8, .. neighbours: a lane's four keys are of one group,
+            // and so are those of size / 4 lanes, or of size / 64 runs.  A lane
+            // keeps its runs' groups' values.  (16384 tokens, 4 of 8 groups of 32:
+            // the way below 24 us more than without groups.)
+            uint32_t one[V / 4], two[V / 4];
+            const int shift = __builtin_ctz(size);
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q) {
+                one[q] = max(key[4 * q], key[4 * q + 1]);
+                two[q] = min(key[4 * q], key[4 * q + 1]);
+                merge_two(one[q], two[q], max(key[4 * q + 2], key[4 * q + 3]), min(key[4 * q + 2], key[4 * q + 3]));
+                if (size >= 8) merge_lanes<0xB1>(one[q], two[q]);     // lane l ^ 1
+                if (size >= 16) merge_lanes<0x4E>(one[q], two[q]);    // l ^ 2
+                if (size >= 32) merge_lanes<0x141>(one[q], two[q]);   // 7 - l of 8: the other quad
+                if (size >= 64) merge_lanes<0x140>(one[q], two[q]);   // 15 - l: the other eight
+            }
+#pragma unroll
+            for (int d = 1; d < V / 4; d *= 2)
+                if (64 * d < size) {
+#pragma unroll
+                    for (int q = 0; q < V / 4; ++q)
+                        if (!(q & d)) {
+                            merge_two(one[q], two[q], one[q + d], two[q + d]);
+                            one[q + d] = one[q];
+                            two[q + d] = two[q];
+                        }
+                }
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q) one[q] = group_key(one[q], two[q], c.best);
+            auto best_left = [&]() {
+                uint32_t m = one[0];
+#pragma unroll
+                for (int q = 1; q < V / 4; ++q) m = max(m, one[q]);
+                return row_max(m);
+            };
+            for (int j = 0; j < c.top_groups; ++j) {
+                last = best_left();
+                uint32_t at = 64;
+#pragma unroll
+                for (int q = V / 4 - 1; q >= 0; --q) at = one[q] == last ? (uint32_t)((64 * q + 4 * l) >> shift) : at;
+                at = row_min(at);
+#pragma unroll
+                for (int q = 0; q < V / 4; ++q) one[q] = at == (uint32_t)((64 * q + 4 * l) >> shift) ? 0u : one[q];
+                open |= 1ull << (at & 63);
+            }
+            left = best_left();
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q) {
+                const bool in = open >> (((64 * q + 4 * l) >> shift) & 63) & 1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) key[4 * q + i] = in ? key[4 * q + i] : 0u;
+            }
+        } else {
+            // the sixteen lanes take the groups in turn, their values made again
+            uint32_t rank[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int g = 16 * q + l;
+                uint32_t one = 0, two = 0;
+                if (live && g < c.groups)
+                    for (int e = g * size; e < (g + 1) * size; ++e) {
+                        const uint32_t v = order_key(score_value32<SIGMOID>(row[e], bias[e], most, inverse));
+                        merge_two(one, two, v, 0);
+                    }
+                rank[q] = group_key(one, two, c.best);
+            }
+            for (int j = 0; j < c.top_groups; ++j) {
+                last = row_max(max(max(rank[0], rank[1]), max(rank[2], rank[3])));
+                uint32_t at = 64;
+#pragma unroll
+                for (int q = 3; q >= 0; --q) at = rank[q] == last ? (uint32_t)(16 * q + l) : at;
+                at = row_min(at);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) rank[q] = at == (uint32_t)(16 * q + l) ? 0u : rank[q];
+                open |= 1ull << (at & 63);
+            }
+            left = row_max(max(max(rank[0], rank[1]), max(rank[2], rank[3])));
+            // e / size for e < 1024 by a multiplication
+            const uint32_t by_size = ((1u << 20) + size - 1) / size;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t e = 64 * (i >> 2) + 4 * l + (i & 3);
+                key[i] = open >> ((e * by_size) >> 20 & 63) & 1 ? key[i] : 0u;
+            }
+        }
+        close = left != 0 && near(last, left, within);
+    }
     // a wave without tokens does not compete with the others
     const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens + __builtin_amdgcn_readfirstlane(tl);   // the wave's first
     const int rounds = t0 < a.T ? k : 0;
@@ -604,7 +708,10 @@ __global__ __launch_bounds__(THREADS) void moe_select_scores_kernel(RouteArgs a,
     if ((tid & 63) == 0) widest[tid >> 6] = far;
     __syncthreads();
     for (int w = 0; w < THREADS / 64; ++w) far = fmaxf(far, widest[w]);
-    for (int tl = tid >> 4; tl < kRouteTokens; tl += THREADS / 16) select_by_scores<V, S, SIGMOID>(a, c, bias, far, mask, tl);
+    constexpr bool kOnce = THREADS / 16 == kRouteTokens;
+    int32_t mine[S];
+    for (int tl = tid >> 4; tl < kRouteTokens; tl += THREADS / 16)
+        select_by_scores<V, S, SIGMOID>(a, c, bias, far, mask, tl, mine);
     __syncthreads();
     const bool single = a.blocks == 1;
     if (single) {
@@ -636,8 +743,11 @@ __global__ __launch_bounds__(THREADS) void moe_select_scores_kernel(RouteArgs a,
     for (int tl = tid >> 4; tl < kRouteTokens; tl += THREADS / 16) {
         const int64_t t = (int64_t)blockIdx.x * kRouteTokens + tl;
         if (t >= a.T) break;
-        for (int j = l; j < k; j += 16) {
-            const int32_t e = a.experts[t * k + j];   // this thread's own store
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int j = 16 * s + l;
+            if (j >= k) break;
+            const int32_t e = kOnce ? mine[s] : a.experts[t * k + j];   // this thread's own store
             int32_t r = __popcll(mask[e] & ((1ull << tl) - 1));
             if (single) {
                 r += start[e];
