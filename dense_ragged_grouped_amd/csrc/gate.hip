@@ -74,26 +74,38 @@ __device__ __forceinline__ float sigmoid(float g) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
-// Codes of eight values and, for the block's 16 lanes, its scale.  127 x is
-// exact for BF16 x, so that x = m / 2 is a true tie (63.5, to 64); blocks whose
-// largest value is beyond 2^120 are scaled by 2^-8 first, so that it is finite.
+// Codes of eight values and, for the block's 16 lanes, its scale.  a = 127 x is
+// exact for BF16 x (times a power of two for blocks near FP32's limits).  The
+// quotient a / m is the product with m's approximate reciprocal and one
+// correction by the exact remainder: where it is a half exactly (x = m / 2: 63.5,
+// to 64) the correction makes it so, and elsewhere it is at least 2^-17 of itself
+// from one (a quotient of 15 and 8 bits), so that the code is that of the exact
+// quotient.  Adding 1.5 * 2^23 rounds it to an integer, ties to even, in the low
+// byte.  With correctly rounded divisions instead, 131072 rows of 2 x 768 took 201
+// us.
 __device__ __forceinline__ u32x2 keep8(u32x4 v, float* scale) {
-    uint32_t m = 0;
+    uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(bf16_at(v, i)) & 0x7FFFFFFFu);
-    m = max16(m);
-    const bool bad = m >= 0x7F800000u;
-    const float most = __uint_as_float(m);
+    for (int i = 0; i < 8; ++i) bits = max(bits, __float_as_uint(bf16_at(v, i)) & 0x7FFFFFFFu);
+    bits = max16(bits);
+    const bool bad = bits >= 0x7F800000u;
+    const float most = __uint_as_float(bits);
     *scale = bad ? __uint_as_float(0x7FC00000u) : most / 127.f;
-    const float down = most > 0x1p120f ? 0x1p-8f : 1.f;
-    const float by = bad || m == 0 ? 1.f : most * down;
-    u32x2 q = {0, 0};
+    const float by = most > 0x1p100f ? 0x1p-64f : most < 0x1p-60f ? 0x1p64f : 1.f;
+    const float m = bad || bits == 0 ? 1.f : most * by, inverse = __builtin_amdgcn_rcpf(m), by127 = 127.f * by;
+    uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int c = bad ? 0 : (int)rintf(bf16_at(v, i) * down * 127.f / by);
-        q[i >> 2] |= (uint32_t)(c & 0xFF) << (8 * (i & 3));
+        const float a = bf16_at(v, i) * by127, q = a * inverse;
+        c[i] = __float_as_uint(__builtin_fmaf(__builtin_fmaf(-q, m, a), inverse, q) + 12582912.f);
     }
-    return q;
+    u32x2 codes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        codes[h] = bad ? 0u
+                       : __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[4 * h + 3], c[4 * h + 2], 0x0c0c0400u),
+                                               __builtin_amdgcn_perm(c[4 * h + 1], c[4 * h], 0x0c0c0400u), 0x05040100u);
+    return codes;
 }
 
 __global__ __launch_bounds__(256) void moe_gate_int8_kernel(GateArgs a) {

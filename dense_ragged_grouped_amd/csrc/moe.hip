@@ -406,9 +406,11 @@ __device__ __forceinline__ uint64_t take_best64(uint64_t (&key)[N], int* expert)
     return m;
 }
 
-// Token t's choice from values in 64 bits, by one wave; chosen(j, e) for each round.
+// Token t's choice from values in 64 bits, by one wave; chosen(j, e) for each
+// round.  The groups that take part are those of `open` unless regroup.
 template <int N, bool SIGMOID, class Chosen>
-__device__ __forceinline__ void choose64(const RouteArgs& a, const ScoreArgs& c, const float* bias, int64_t t, Chosen chosen) {
+__device__ __forceinline__ void choose64(const RouteArgs& a, const ScoreArgs& c, const float* bias, int64_t t,
+                                         unsigned long long open, bool regroup, Chosen chosen) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     float x[N], top = -INFINITY;
@@ -437,8 +439,8 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const ScoreArgs& c,
         key[i] = e >= a.E ? 0 : order_key64(score_value<SIGMOID, double>(x[i], b, most, total));
         __builtin_amdgcn_sched_barrier(0);   // one at a time: sixteen exponentials side by side do not fit the registers
     }
-    if (c.groups > 1) {
-        const int size = a.E / c.groups;
+    const int size = a.E / c.groups;
+    if (regroup) {
         uint64_t rank = 0;   // lane g: the value of group g
         for (int g = 0; g < c.groups; ++g) {
             uint64_t in[N];
@@ -457,12 +459,13 @@ __device__ __forceinline__ void choose64(const RouteArgs& a, const ScoreArgs& c,
             const uint64_t v = __shfl((unsigned long long)rank, g, 64);
             ahead += v > rank || (v == rank && g < lane);
         }
-        const unsigned long long open = __ballot(lane < c.groups && ahead < c.top_groups);
+        open = __ballot(lane < c.groups && ahead < c.top_groups);
+    }
+    if (c.groups > 1) {
+        // e / size for e < 1024 by a multiplication
+        const uint32_t by_size = ((1u << 20) + size - 1) / size;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = 64 * i + lane;
-            if (e < a.E && !(open >> (e / size) & 1)) key[i] = 0;
-        }
+        for (int i = 0; i < N; ++i) key[i] = open >> (((64 * i + lane) * by_size) >> 20 & 63) & 1 ? key[i] : 0;
     }
     for (int j = 0; j < a.k; ++j) {
         int e;
@@ -527,10 +530,11 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
             if constexpr (V > 16) __builtin_amdgcn_sched_barrier(0);   // side by side they do not fit the registers
         }
     }
+    unsigned long long open = 0;   // the groups that take part
+    bool regroup = false;
     if (c.groups > 1) {
         const int size = E / c.groups;
         const float within = (4.f * off + 8.f * kUnit * (1.f + far)) * 1.01f;
-        unsigned long long open = 0;
         uint32_t last = 0, left;
         if (size >= 4 && (size & (size - 1)) == 0) {
             // Groups of 4, 8, .. neighbours: a lane's four keys are of one group,
@@ -618,7 +622,7 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
                 key[i] = open >> ((e * by_size) >> 20 & 63) & 1 ? key[i] : 0u;
             }
         }
-        close = left != 0 && near(last, left, within);
+        regroup = left != 0 && near(last, left, within);
     }
     // a wave without tokens does not compete with the others
     const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens + __builtin_amdgcn_readfirstlane(tl);   // the wave's first
@@ -636,11 +640,14 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
             if (j == 16 * s + l && j < rounds) mine[s] = (int32_t)e;
     }
     // the tokens of this wave that FP32 does not decide
-    unsigned long long undecided = __ballot(close && live);
+    unsigned long long undecided = __ballot((close || regroup) && live);
+    const unsigned long long groups_too = __ballot(regroup);
     while (undecided) {
         const int at = __ffsll((long long)undecided) - 1;   // a lane of the token's row
         undecided &= ~(0xFFFFull << (at & ~15));
-        choose64<V / 4, SIGMOID>(a, c, bias, t0 + (at >> 4), [&](int j, int e) {
+        const unsigned long long its_open = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(open >> 32), at) << 32 |
+                                            (uint32_t)__builtin_amdgcn_readlane((int)open, at);
+        choose64<V / 4, SIGMOID>(a, c, bias, t0 + (at >> 4), its_open, groups_too >> at & 1, [&](int j, int e) {
 #pragma unroll
             for (int s = 0; s < S; ++s)
                 if (lane >> 4 == at >> 4 && j == 16 * s + l) mine[s] = e;
@@ -687,9 +694,14 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
 }
 
 // The block of 64 tokens, THREADS / 16 at a time, then their pairs' ranks and the
-// counts as moe_select_kernel leaves them.  More than 256 experts take 512 or
-// 256 threads: with 1024 a lane has 128 registers, which 32 or 64 keys do not
-// fit beside the rest.
+// counts as moe_select_kernel leaves them.  More than 512 experts take 256
+// threads: with 1024 a lane has 128 registers, with 512 256, and 64 keys do not
+// fit them beside the rest.
+//
+// 16384 tokens, k = 8 of 256 experts, graph replays: 14 us without groups and
+// bias (moe_select_kernel 12), 20 with a bias, 25 with 4 of 8 groups; of the last
+// two 3 and 5 us are the 13 tokens or so of these that are chosen again in 64
+// bits, at the end of blocks that the others wait for.
 template <int V, int S, int THREADS, bool SIGMOID>
 __global__ __launch_bounds__(THREADS) void moe_select_scores_kernel(RouteArgs a, ScoreArgs c) {
     __shared__ unsigned long long mask[16 * V];
@@ -1252,7 +1264,7 @@ hipError_t launch_moe_route_scores(const float* logits, int64_t T, int32_t E, in
     timing_mark("moe_select_scores_kernel", s);
     for_experts(E, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        constexpr int kThreads = V <= 16 ? 1024 : V == 32 ? 512 : 256;
+        constexpr int kThreads = V <= 32 ? 1024 : 256;
         const dim3 grid((unsigned)a.blocks), block(kThreads);
         if (c.score == DRGG_SCORE_SIGMOID) {
             if (k <= 16) hipLaunchKernelGGL((moe_select_scores_kernel<V, 1, kThreads, true>), grid, block, 0, s, a, sc);

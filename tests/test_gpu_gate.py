@@ -346,3 +346,25 @@ def test_refusals(drgg):
                 lambda: moe.ffn(*block(4, 4, 64, 64), 2, kept="fp8")):
         with pytest.raises((TypeError, ValueError, drgg.DrggError)):
             bad()
+
+
+def test_every_quotient(drgg):
+    """Codes of every BF16 value from 2^-9 to 1 times a block's largest, for every significand of that, at scales from
+    FP32's smallest to its largest: those of the exact quotient, ties to even."""
+    x = (np.arange(128, 256)[None, :] * np.exp2(-7.0 - np.arange(10))[:, None]).reshape(-1)   # [2^-9, 2)
+    for shift in (-126.0, -70.0, 0.0, 99.0, 126.0):
+        rows = []
+        for m in np.arange(128, 256) / 128:
+            v = x[x <= m]
+            v = np.concatenate([v, np.zeros(-len(v) % 127)]).reshape(-1, 127)
+            rows.append(np.concatenate([np.full((len(v), 1), m), v * np.where(np.arange(127) % 2, -1, 1)], 1))
+        g = np.concatenate(rows) * 2.0 ** shift
+        g = np.where(np.abs(g) < 2.0 ** -133, 0, g).astype(np.float32)
+        GU = dev(np.concatenate([g, g[:, ::-1]], 1)).bfloat16()
+        R = len(g)
+        positions, weights = torch.arange(R, dtype=torch.int32, device="cuda").view(R, 1), torch.ones(R, 1, device="cuda")
+        _, codes, scale = drgg.moe_gate_int8(GU, positions, weights)
+        gu = host(GU)
+        want = [kept64(gu[:, :128]), kept64(gu[:, 128:])]
+        assert np.array_equal(host(codes), np.concatenate([w[0] for w in want], 1))
+        assert np.array_equal(scale.cpu().numpy(), np.concatenate([w[1] for w in want], 1))
