@@ -339,9 +339,9 @@ __global__ __launch_bounds__(64 * W, 2) void mx_rows_kernel(MxArgs a) {
     const int64_t NO = GATED ? a.N / 2 : a.N;
     constexpr int kCols = 16 * (GATED ? NB / 2 : NB);
     if (!find_rows_item<TOK>(a.offs, a.E, a.M, (int32_t)((NO + kCols - 1) / kCols), &it)) return;
-    const int64_t left = it.hi - it.m0;
+    const int64_t left = it.hi - it.m0;   // of the group; this block's are at most TOK
     if (left <= 16) mx_rows_block<OUT, GATED, GATHERED, NB, 1, W, 2>(a, it, sums);
-    else if (left <= 32) mx_rows_block<OUT, GATED, GATHERED, NB, 2, W, 1>(a, it, sums);
+    else if (TOK == 32 || left <= 32) mx_rows_block<OUT, GATED, GATHERED, NB, 2, W, 1>(a, it, sums);
     else if constexpr (TOK > 32) mx_rows_block<OUT, GATED, GATHERED, NB, 4, W, 1>(a, it, sums);
 }
 

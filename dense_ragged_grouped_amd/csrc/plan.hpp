@@ -572,17 +572,52 @@ inline Int8Program int8_program(int64_t E, int64_t M, int64_t N, int64_t K, bool
     return {int8_tile(E, M, K, ceil_div(cols_out, bc), ceil_div(cols_out, bc / 2), may128), 0, 0, 0};
 }
 
-// The same for a 4-bit product: its rows are K/2 bytes, and a step of 64 bytes
-// takes as long whatever the elements.  128x128 tiles have room for
-// kMx128MaxExperts groups beside the scales, two of them on a CU.  codes: the
-// result is quantised, in blocks of 32 columns of one workgroup.
+// The same for a 4-bit product (rows of K/2 bytes, s of them in steps of 64),
+// with its own bounds, from two sweeps of 560 random sizes (E 1 to 128, M 8 to
+// 40000, N 768 to 4096, K 512 to 4096, even and skewed groups).  A round of tiles
+// takes about
+//   256x256  6.4 + 0.77 s    128x256  4.4 + 0.56 s    128x128  3.15 + 0.655 s,
+// 128x128 tiles that have a CU each 2.55 + 0.286 s.  With these, margins of 5 % for
+// the smaller tiles, and 128x128 up to 128 rows a group, the tile taken is 0.4 and
+// 0.7 % slower than the best of the three in the geometric mean of either sweep
+// (int8_tile's bounds: 0.9 and 1.1 %; E = 32, 4548x2544x512 then takes 21.8 us, in
+// 128x128 15.8).  128x128 tiles have room for kMx128MaxExperts groups beside the
+// scales, two of them on a CU.
+//
+// Many experts' weights are read at memory speed by the few-row blocks up to 10
+// rows a group (E = 32, 246x4096x1056: 23.1 us, 128x128 tiles 24.2); beyond, several
+// token blocks of one expert read them again (E = 128, 2580x4096x2048: 155, 122).
+// codes: the result is quantised, in blocks of 32 columns of one workgroup.
 constexpr int kMx128MaxExperts = 992;
 inline Int8Program mxfp4_program(int64_t E, int64_t M, int64_t N, int64_t K, bool gated, bool bf16, bool codes,
                                  int forced_tile) {
-    Int8Program p = int8_program(E, M, N, K / 2, gated, bf16, forced_tile);
-    if (p.tile == kTile128x128 && E > kMx128MaxExperts) p.tile = kTile128x256;
-    if (codes && p.tile == kTileAuto && p.nb < 4) p.nb = 4;
-    return p;
+    const bool may128 = !(gated && bf16) && E <= kMx128MaxExperts;
+    const int64_t cols_out = gated ? N / 2 : N, bc = gated ? 128 : 256;
+    if (forced_tile == kTile256x256 || forced_tile == kTile128x256 || (forced_tile == kTile128x128 && may128))
+        return {forced_tile, 0, 0, 0};
+    // a launch has fewer than 2^32 threads (the tiles walk theirs)
+    const bool rows = (M / 32 + E) * ceil_div(N, 16) < int64_t(1) << 22;
+    const int64_t cols = ceil_div(N, 64), full = M < E ? M : E;
+    const int64_t blocks = cols * (M <= 48 * E ? full : ceil_div(M, 64) + E / 2);
+    if (rows && cols * E >= 2 * kRuleCUs && M <= 10 * E) return {kTileAuto, 4, 4, 32};
+    if (rows && blocks <= kRuleCUs) {
+        // one block per CU at most: the smallest blocks for which that holds
+        if (codes || 2 * blocks > kRuleCUs) return {kTileAuto, 4, 8, 64};
+        return {kTileAuto, gated || 4 * blocks > kRuleCUs ? 2 : 1, 8, 64};
+    }
+    if (rows && blocks <= 2 * kRuleCUs && M <= 48 * E) return {kTileAuto, 4, 4, 64};
+    const double s = (double)K / 128;
+    auto tiles = [&](int64_t bm, int64_t nc) {
+        const int64_t about = ceil_div(M, bm) + E / 2;
+        return (about > full ? about : full) * nc;
+    };
+    const double c256 = (double)ceil_div(tiles(256, ceil_div(cols_out, bc)), kRuleCUs) * (6.4 + 0.77 * s);
+    const double c128x256 = 1.05 * (double)ceil_div(tiles(128, ceil_div(cols_out, bc)), kRuleCUs) * (4.4 + 0.56 * s);
+    const double r = (double)tiles(128, ceil_div(cols_out, bc / 2)) / (2 * kRuleCUs);
+    const double c128 = 1.05 * (r <= 0.5 ? 2.55 + 0.286 * s : (r > 1 ? r + 0.25 : 1.0) * (3.15 + 0.655 * s));
+    const double best = c256 < c128x256 ? c256 : c128x256;
+    if (may128 && (M <= 128 * E || c128 < best)) return {kTile128x128, 0, 0, 0};
+    return {best == c256 ? kTile256x256 : kTile128x256, 0, 0, 0};
 }
 
 }  // namespace drgg
