@@ -229,11 +229,14 @@ drgg_status moe_ffn_mxfp4(const void* X, const float* logits, const uint8_t* W1q
     st = current_cu_count(&cus);
     if (st != DRGG_OK) return st;
     const int64_t R = T * k;
+    // the scored selection's launch quantises few tokens' rows too
+    const MxQuantArgs rows{X, x, xs, T, H};
+    const bool together = scoring && T * H <= kSelectMxMost;
     hipError_t e = scoring ? launch_moe_route_scores(logits, T, E, k, *scoring, experts, weights, offsets, positions, tokens,
-                                                     ws + L.table, stream)
+                                                     ws + L.table, stream, together ? &rows : nullptr)
                            : launch_moe_route(logits, T, E, k, 1, experts, weights, offsets, positions, tokens,
                                               ws + L.table, stream);
-    if (e == hipSuccess) e = launch_quantize_mxfp4(X, true, T, H, x, xs, stream);
+    if (e == hipSuccess && !together) e = launch_quantize_mxfp4(X, true, T, H, x, xs, stream);
     if (e == hipSuccess)
         e = launch_mxfp4(MxArgs{x, W1q, xs, w1_scale, offsets, hq, R, 2 * I, H, E, tokens, T, hs}, true, false, cus,
                          knob_tile(), stream);

@@ -137,10 +137,21 @@ hipError_t launch_int8(const Int8Args& a, bool gated, bool bf16, int cus, int fo
 
 // ---- selection by scores (moe.hip), 4-bit products (mxfp4.hip), kept activations (gate.hip)
 
-// the scored selection; its workspace is moe_route's
+// Arguments of the 4-bit quantisation (mxfp4.hpp): X [T,K] to codes and scales.
+struct MxQuantArgs {
+    const void* X;
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t T, K;
+};
+// the most values that the scored selection's launch quantises too
+constexpr int64_t kSelectMxMost = int64_t(1) << 21;
+
+// The scored selection; its workspace is moe_route's.  quantize: also the
+// quantisation of these BF16 rows, which needs nothing of the selection.
 hipError_t launch_moe_route_scores(const float* logits, int64_t T, int32_t E, int32_t k, const drgg_scoring& scoring,
                                    int32_t* experts, float* weights, int32_t* offsets, int32_t* positions,
-                                   int32_t* tokens, void* table, hipStream_t s);
+                                   int32_t* tokens, void* table, hipStream_t s, const MxQuantArgs* quantize = nullptr);
 hipError_t launch_moe_route_scores_grad(const float* dweights, const float* logits, const int32_t* experts,
                                         const float* weights, int64_t T, int32_t E, int32_t k,
                                         const drgg_scoring& scoring, float* dlogits, hipStream_t s);

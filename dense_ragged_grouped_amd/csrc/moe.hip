@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "internal.hpp"
+#include "mxfp4.hpp"
 #include "plan.hpp"
 #include "quantize.hpp"
 
@@ -703,7 +704,15 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
 // two 3 and 5 us are the 13 tokens or so of these that are chosen again in 64
 // bits, at the end of blocks that the others wait for.
 template <int V, int S, int THREADS, bool SIGMOID>
-__global__ __launch_bounds__(THREADS) void moe_select_scores_kernel(RouteArgs a, ScoreArgs c) {
+__global__ __launch_bounds__(THREADS) void moe_select_scores_kernel(RouteArgs a, ScoreArgs c, MxQuantArgs quant) {
+    if (blockIdx.x >= a.blocks) {   // the rows' quantisation, half a wave per row and 256 columns
+        const int64_t n = quant.T * ceil_div(quant.K, 256);
+        for (int64_t p = (int64_t)(blockIdx.x - a.blocks) * (THREADS / 32); p < n; p += (int64_t)(gridDim.x - a.blocks) * (THREADS / 32)) {
+            const int64_t u = p + (threadIdx.x >> 5);
+            quantize_mx_piece<true>(quant, u < n ? u % quant.T : quant.T, u < n ? u / quant.T : 0);
+        }
+        return;
+    }
     __shared__ unsigned long long mask[16 * V];
     __shared__ int32_t start[16 * V], tmp[THREADS / 64];
     __shared__ __attribute__((aligned(16))) float bias[16 * V];
@@ -1258,20 +1267,22 @@ hipError_t launch_moe_route(const float* logits, int64_t T, int32_t E, int32_t k
 
 hipError_t launch_moe_route_scores(const float* logits, int64_t T, int32_t E, int32_t k, const drgg_scoring& c,
                                    int32_t* experts, float* weights, int32_t* offsets, int32_t* positions,
-                                   int32_t* tokens, void* table, hipStream_t s) {
+                                   int32_t* tokens, void* table, hipStream_t s, const MxQuantArgs* quantize) {
     RouteArgs a{logits, experts, weights, offsets, positions, tokens, table, T, route_blocks(T), E, k, c.renormalize != 0};
     const ScoreArgs sc{c.bias, c.groups, c.top_groups, c.best, !c.bias && c.groups == 1, c.scale};
+    const MxQuantArgs quant = quantize ? *quantize : MxQuantArgs{};
     timing_mark("moe_select_scores_kernel", s);
     for_experts(E, [&](auto v) {
         constexpr int V = decltype(v)::value;
         constexpr int kThreads = V <= 32 ? 1024 : 256;
-        const dim3 grid((unsigned)a.blocks), block(kThreads);
+        const dim3 grid((unsigned)(a.blocks + (quantize ? ceil_div(quantize->T * ceil_div(quantize->K, 256), kThreads / 32) : 0)));
+        const dim3 block(kThreads);
         if (c.score == DRGG_SCORE_SIGMOID) {
-            if (k <= 16) hipLaunchKernelGGL((moe_select_scores_kernel<V, 1, kThreads, true>), grid, block, 0, s, a, sc);
-            else hipLaunchKernelGGL((moe_select_scores_kernel<V, 4, kThreads, true>), grid, block, 0, s, a, sc);
+            if (k <= 16) hipLaunchKernelGGL((moe_select_scores_kernel<V, 1, kThreads, true>), grid, block, 0, s, a, sc, quant);
+            else hipLaunchKernelGGL((moe_select_scores_kernel<V, 4, kThreads, true>), grid, block, 0, s, a, sc, quant);
         } else {
-            if (k <= 16) hipLaunchKernelGGL((moe_select_scores_kernel<V, 1, kThreads, false>), grid, block, 0, s, a, sc);
-            else hipLaunchKernelGGL((moe_select_scores_kernel<V, 4, kThreads, false>), grid, block, 0, s, a, sc);
+            if (k <= 16) hipLaunchKernelGGL((moe_select_scores_kernel<V, 1, kThreads, false>), grid, block, 0, s, a, sc, quant);
+            else hipLaunchKernelGGL((moe_select_scores_kernel<V, 4, kThreads, false>), grid, block, 0, s, a, sc, quant);
         }
     });
     return finish_route(a, s);

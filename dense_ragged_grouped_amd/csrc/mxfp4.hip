@@ -14,6 +14,7 @@
 
 #include "engine.hpp"
 #include "internal.hpp"
+#include "mxfp4.hpp"
 #include "plan.hpp"
 #include "products.hpp"
 
@@ -23,93 +24,17 @@ namespace {
 
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
-// ---------------------------------------------------------------------------
-// quantisation
-//
-// Half a wave per row and 256 columns: lane l has columns 8l .. 8l+7, four
-// lanes a block of 32.  The maxima are two rotations within quads; the codes
-// leave as one dword per lane, the scales of 128 columns as one dword of the
-// row of 16 lanes that holds them.
-
-// v of lane l ^ 1, l ^ 2
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
-}
-// or over the row of 16 of values that agree within each quad
-__device__ __forceinline__ uint32_t or_quads(uint32_t v) {
-    v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false);
-    return v | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false);
-}
-
-// The scale byte for a largest magnitude given as bits: its exponent field
-// less 2 (the largest code is 1.5 * 2^2), 255 for infinity and NaN.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t most) {
-    const int e = (int)(most >> 23);
-    return e == 255 ? 255u : e > 2 ? (uint32_t)(e - 2) : 0u;
-}
-// 2^(127 - b), by which the values are multiplied, for a finite block (b is at
-// most 252).  Exact; a result below FP32's normal range is far below half the
-// smallest code.
-__device__ __forceinline__ float scale_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
-// eight codes, the first in the lowest bits.  The conversion rounds to the
-// nearest code, ties to even, and limits to 6.
-__device__ __forceinline__ uint32_t codes8(const float (&y)[8]) {
-    uint32_t q = 0;
-    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, y[0], y[1], 1.f, 0);
-    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, y[2], y[3], 1.f, 1);
-    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, y[4], y[5], 1.f, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, y[6], y[7], 1.f, 3);
-}
-
-template <bool BF16>
-__device__ __forceinline__ void load8(float (&f)[8], const void* X, int64_t i) {
-    if constexpr (BF16) {
-        const u32x4 v = reinterpret_cast<const u32x4*>(X)[i];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            f[2 * r] = __uint_as_float(v[r] << 16);
-            f[2 * r + 1] = __uint_as_float(v[r] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f32x4 v = reinterpret_cast<const f32x4*>(X)[2 * i + h];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) f[4 * h + r] = v[r];
-        }
-    }
-}
-
-struct MxRowArgs {
-    const void* X;      // quantisation: values; dequantisation: codes
-    const uint8_t* in_scales;
-    void* out;          // codes; values
-    uint8_t* scales;
+struct MxRowArgs {   // dequantisation
+    const uint8_t* codes;
+    const uint8_t* scales;
+    void* X;
     int64_t T, K;
 };
 
 template <bool BF16>
-__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(MxRowArgs a) {
-    const int l = threadIdx.x & 31;
-    const int64_t kb = blockIdx.y, c = 256 * kb + 8 * l;
-    // every lane of a wave takes part in the exchanges
-    for (int64_t t0 = (int64_t)blockIdx.x * 8; t0 < a.T; t0 += (int64_t)gridDim.x * 8) {
-        const int64_t t = t0 + (threadIdx.x >> 5);
-        const bool live = t < a.T && c < a.K;
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live) load8<BF16>(f, a.X, (t * a.K + c) / 8);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-        const uint32_t b = scale_byte(quad_max(m));
-        const float by = scale_inverse(b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = b == 255 ? 0.f : f[i] * by;
-        if (live) static_cast<uint32_t*>(a.out)[(t * a.K + c) / 8] = codes8(f);
-        const uint32_t four = or_quads(live ? b << (8 * ((l >> 2) & 3)) : 0u);
-        if ((l & 15) == 0 && t < a.T) reinterpret_cast<uint32_t*>(a.scales)[(kb * a.T + t) * 2 + (l >> 4)] = four;
-    }
+__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(MxQuantArgs a) {
+    for (int64_t t0 = (int64_t)blockIdx.x * 8; t0 < a.T; t0 += (int64_t)gridDim.x * 8)
+        quantize_mx_piece<BF16>(a, t0 + (threadIdx.x >> 5), blockIdx.y);
 }
 
 // The values of eight codes: converted with scale 1 and moved by the block's
@@ -121,8 +46,8 @@ __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(MxRowArgs a) {
     const int64_t kb = blockIdx.y, c = 256 * kb + 8 * l;
     if (c >= a.K) return;
     for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * 8) {
-        const uint32_t q = static_cast<const uint32_t*>(a.X)[(t * a.K + c) / 8];
-        const int b = a.in_scales[(kb * a.T + t) * 8 + (l >> 2)];
+        const uint32_t q = reinterpret_cast<const uint32_t*>(a.codes)[(t * a.K + c) / 8];
+        const int b = a.scales[(kb * a.T + t) * 8 + (l >> 2)];
         const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0);
         const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1);
         const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2);
@@ -131,10 +56,10 @@ __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(MxRowArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = b == 255 ? __uint_as_float(0x7FC00000u) : ldexpf(f[i], b - 127);
         if constexpr (BF16) {
-            static_cast<u32x4*>(a.out)[(t * a.K + c) / 8] =
+            static_cast<u32x4*>(a.X)[(t * a.K + c) / 8] =
                 u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
         } else {
-            f32x4* out = static_cast<f32x4*>(a.out) + (t * a.K + c) / 4;
+            f32x4* out = static_cast<f32x4*>(a.X) + (t * a.K + c) / 4;
             out[0] = f32x4{f[0], f[1], f[2], f[3]};
             out[1] = f32x4{f[4], f[5], f[6], f[7]};
         }
@@ -185,26 +110,17 @@ __device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& i
     const uint8_t* w0 = a.W + ((int64_t)it.e * a.N + n0) * B;
     const auto rw = make_rsrc(w0);
     const auto rw2 = make_rsrc(GATED ? w0 + NO * B : w0);
-    // a row's byte offset, bytes it has from this lane's 16 on, and its scales' offset
-    int off[4], xoff[MB], xk[MB], wk[NC], xs[MB];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) off[b] = (16 * b + r) * B + 16 * g;
+    // a row's byte offset, and bytes it has from this lane's 16 on
+    int off[4], xk[MB], wk[NC];
+    int32_t from[MB];   // rows of X; T * B < 2^31
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
         const bool ok = it.m0 + 16 * b + r < it.hi;
-        xoff[b] = off[b];
         xk[b] = ok ? B - 16 * g : 0;
-        xs[b] = (16 * b + r) * 8;
-        if constexpr (GATHERED) {   // T * B < 2^31
-            const int32_t from = ok ? a.rows[it.m0 + 16 * b + r] : -1;
-            if ((uint32_t)from < (uint32_t)a.T) {
-                xoff[b] = from * B + 16 * g;
-                xs[b] = from * 8;
-            } else {
-                xk[b] = 0;
-            }
-        }
+        from[b] = GATHERED ? ok ? a.rows[it.m0 + 16 * b + r] : -1 : 16 * b + r;
     }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) off[b] = (16 * b + r) * B + 16 * g;
 #pragma unroll
     for (int b = 0; b < NC; ++b) wk[b] = n0 + 16 * b + r < NO ? B - 16 * g : 0;
     const int64_t xrows = GATHERED ? a.T : a.M, wrows = (int64_t)a.E * a.N;
@@ -230,13 +146,16 @@ __device__ __forceinline__ void mx_rows_block(const MxArgs& a, const RowsItem& i
                 sw[u][b] = __builtin_amdgcn_raw_buffer_load_b64(
                     b < NC ? rws : rws2, k < wk[b % NC] ? (uint32_t)(16 * (b % NC) + r) * 8 : kOOB, 0, 0);
             }
+            // the tokens' rows after the weights: where they are gathered, their
+            // indices arrive behind the first weights' loads
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
+                const int left = !GATHERED || (uint32_t)from[b] < (uint32_t)a.T ? xk[b] - k : 0;
+                const uint32_t at = (uint32_t)(from[b] * B + 16 * g + k);
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    fx[u][s][b] = __builtin_amdgcn_raw_buffer_load_b128(
-                        rx, k + 64 * s < xk[b] ? (uint32_t)(xoff[b] + k + 64 * s) : kOOB, 0, 0);
-                sx[u][b] = __builtin_amdgcn_raw_buffer_load_b64(rxs, k < xk[b] ? (uint32_t)xs[b] : kOOB, 0, 0);
+                    fx[u][s][b] = __builtin_amdgcn_raw_buffer_load_b128(rx, 64 * s < left ? at + 64 * s : kOOB, 0, 0);
+                sx[u][b] = __builtin_amdgcn_raw_buffer_load_b64(rxs, 0 < left ? (uint32_t)from[b] * 8 : kOOB, 0, 0);
             }
         }
 #pragma unroll
@@ -694,7 +613,7 @@ hipError_t launch_mx_program(const MxArgs& a, const Int8Program& p, bool bf16, h
 
 hipError_t launch_quantize_mxfp4(const void* X, bool bf16, int64_t T, int64_t K, uint8_t* codes, uint8_t* scales,
                                  hipStream_t s) {
-    const MxRowArgs a{X, nullptr, codes, scales, T, K};
+    const MxQuantArgs a{X, codes, scales, T, K};
     timing_mark("quantize_mxfp4_kernel", s);
     if (bf16) hipLaunchKernelGGL(quantize_mxfp4_kernel<true>, mx_row_grid(T, K), dim3(256), 0, s, a);
     else hipLaunchKernelGGL(quantize_mxfp4_kernel<false>, mx_row_grid(T, K), dim3(256), 0, s, a);
@@ -704,7 +623,7 @@ hipError_t launch_quantize_mxfp4(const void* X, bool bf16, int64_t T, int64_t K,
 
 hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t T, int64_t K, bool bf16,
                                    void* X, hipStream_t s) {
-    const MxRowArgs a{codes, scales, X, nullptr, T, K};
+    const MxRowArgs a{codes, scales, X, T, K};
     timing_mark("dequantize_mxfp4_kernel", s);
     if (bf16) hipLaunchKernelGGL(dequantize_mxfp4_kernel<true>, mx_row_grid(T, K), dim3(256), 0, s, a);
     else hipLaunchKernelGGL(dequantize_mxfp4_kernel<false>, mx_row_grid(T, K), dim3(256), 0, s, a);

@@ -74,8 +74,10 @@ hipError_t launch_moe_route(const float*, int64_t T, int32_t E, int32_t k, int r
 }
 hipError_t launch_moe_route_scores(const float*, int64_t T, int32_t E, int32_t k, const drgg_scoring&, int32_t* experts,
                                    float* weights, int32_t* offsets, int32_t* positions, int32_t* tokens, void* table,
-                                   hipStream_t) {
-    return route(T, E, k, experts, weights, offsets, positions, tokens, table, true);
+                                   hipStream_t, const MxQuantArgs* quantize) {
+    route(T, E, k, experts, weights, offsets, positions, tokens, table, true);
+    if (quantize) launch_quantize_mxfp4(quantize->X, true, quantize->T, quantize->K, quantize->codes, quantize->scales, nullptr);
+    return hipSuccess;
 }
 hipError_t launch_moe_route_scores_grad(const float*, const float*, const int32_t*, const float*, int64_t, int32_t, int32_t,
                                         const drgg_scoring&, float*, hipStream_t) { return hipSuccess; }
