@@ -144,7 +144,9 @@ struct MxQuantArgs {
     uint8_t* scales;
     int64_t T, K;
 };
-// the most values that the scored selection's launch quantises too
+// The most values that the scored selection's launch quantises too: the serving
+// block (E = 32, k = 8, H 2048, I 768) takes 32.1 instead of 34.2 us for 8 tokens,
+// 45.4 for 47.6 at 256 and 74 for 77 at 1024; at 2048 tokens both take 103.
 constexpr int64_t kSelectMxMost = int64_t(1) << 21;
 
 // The scored selection; its workspace is moe_route's.  quantize: also the

@@ -623,7 +623,8 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
                 key[i] = open >> ((e * by_size) >> 20 & 63) & 1 ? key[i] : 0u;
             }
         }
-        regroup = left != 0 && near(last, left, within);
+        // (sums of biases beyond 2^126 may leave FP32's range)
+        regroup = left != 0 && (near(last, left, within) || far > 0x1p126f);
     }
     // a wave without tokens does not compete with the others
     const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens + __builtin_amdgcn_readfirstlane(tl);   // the wave's first

@@ -15,7 +15,7 @@ operators raises.
 """
 import torch
 
-from . import (Routing, Scoring, grouped_gemm_dgrad, grouped_gemm_fwd, grouped_gemm_wgrad, moe_combine, moe_combine_grad,
+from . import (Routing, Scoring, grouped_gemm_dgrad, grouped_gemm_fwd, grouped_gemm_int8, grouped_gemm_wgrad, moe_combine, moe_combine_grad,
                moe_dispatch, moe_ffn_int8, moe_ffn_mxfp4, moe_gate_int8, moe_gate_int8_grad, moe_route, moe_route_grad,
                moe_route_scores, moe_route_scores_grad, quantize_int8, quantize_mxfp4)
 from .autograd import gradient, grouped_linear
@@ -29,14 +29,24 @@ def quantize_weights(W):
     return q.view(E, N, K), scale.view(E, N)
 
 
-def ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True):
+def ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=True, scoring=None):
     """The block on 8-bit weights (codes and scales as quantize_weights gives
     them): X [T, H] BF16 to [T, H] BF16.  Rows are quantised per token before
     each product; the activation between the products stays in FP32 until
     then (rounded to BF16 first, values near the border of two codes would
     take the other one, which moves the result by 0.75 % of its norm).  The
-    experts' outputs are rounded to BF16 before they are added in FP32."""
-    return moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=renormalize)
+    experts' outputs are rounded to BF16 before they are added in FP32.
+    scoring: a Scoring to select by scores (renormalize is then the Scoring's),
+    by the block's single calls instead of the one."""
+    if scoring is None:
+        return moe_ffn_int8(X, logits, W1q, w1_scale, W2q, w2_scale, k, renormalize=renormalize)
+    r = moe_route_scores(logits, k, scoring)
+    gather = X.numel() < 2 ** 31 - 4096
+    q, scale = quantize_int8(X) if gather else quantize_int8(X, r.positions)
+    h = grouped_gemm_int8(q, scale, W1q, w1_scale, r.group_offsets, gated=True, rows=r.tokens if gather else None,
+                          out_dtype=torch.float32)
+    y = grouped_gemm_int8(*quantize_int8(h), W2q, w2_scale, r.group_offsets)
+    return moe_combine(y, r.positions, r.weights)
 
 
 def quantize_weights_mxfp4(W):

@@ -689,8 +689,8 @@ drgg_status dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_
                              drgg_dtype dtype, void *X, hipStream_t stream);
 
 /*
- * Y[t,n] = sum_k x[t,k] * w[e(t),n,k], FP32 accumulation in one fixed order,
- * rounded once to out_dtype.  Xq [M, K/2] with scales x_scale, Wq [E, N, K/2]
+ * Y[t,n] = sum_k x[t,k] * w[e(t),n,k], FP32 accumulation in an order that the
+ * sizes alone decide, rounded once to out_dtype.  Xq [M, K/2] with scales x_scale, Wq [E, N, K/2]
  * with w_scale (E*N rows).  Every product of two elements is exact.  gated,
  * rows and group_offsets as for grouped_gemm_int8 (gated: silu(g) to within
  * (4 |g| + 16) 2^-24 of it); with rows, Xq [T, K/2] and T*K/2 <= 2^31 - 4097.
@@ -742,6 +742,8 @@ drgg_status moe_ffn_mxfp4_workspace_size(int64_t T, int32_t E, int32_t k, int64_
  *               h[p] = weights[t,j] * g s u                                 BF16
  *               dweights[t,j] = sum over I of dh[p] * g s u                 FP32
  *             (h again, for the gradient of the product that takes it).
+ * silu and s are as exact as grouped_gemm_int8's gate (0 below g = -87).  A row
+ * of weight 0 gets zeros in h and dGU, whatever GU, its codes and dh hold.
  * With the weights here, the rows that the following product makes are added
  * without weights (moe_combine, weights NULL) and need not be kept for the
  * weights' gradient.  A position outside [0, T*k) is skipped (its dweights are

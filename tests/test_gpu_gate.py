@@ -278,8 +278,9 @@ def test_only_some_gradients(drgg):
     full = torch.autograd.grad(moe.ffn(X, logits, W1, W2, 2, kept="int8").float().sum(), (X, logits, W1, W2))
     for i, t in enumerate((X, logits, W1, W2)):
         parts = [u if u is t else u.detach() for u in (X, logits, W1, W2)]
-        one, = torch.autograd.grad(moe.ffn(*parts, 2, kept="int8").float().sum(), t)
-        assert torch.equal(one, full[i])
+        for graph in (False, True):
+            one, = torch.autograd.grad(moe.ffn(*parts, 2, kept="int8").float().sum(), t, create_graph=graph)
+            assert torch.equal(one, full[i])
 
 
 def test_second_derivative_raises(drgg):

@@ -377,3 +377,31 @@ def test_on_another_stream(drgg):
     for a, b in zip(want, got):
         assert torch.equal(a, b)
     assert torch.equal(grad, drgg.moe_route_scores_grad(dw, x, want.experts, want.weights, sc))
+
+
+def test_large_biases(drgg):
+    """Sums of two biases beyond FP32's range are still compared as 64-bit values."""
+    x = torch.zeros(5, 16, device="cuda")
+    bias = torch.full((16,), -3e38)
+    bias[[0, 1, 8, 9]] = torch.tensor([3.1e38, 2.0e38, 3.0e38, 3.0e38])
+    r = drgg.moe_route_scores(x, 3, drgg.Scoring(bias=bias.cuda(), groups=2, top_groups=1))
+    assert host(r.experts).tolist() == [[8, 9, 10]] * 5
+
+
+def test_int8_block_by_scores(drgg):
+    """The 8-bit serving block with a Scoring that is moe_route's selection: the one call's result."""
+    from dense_ragged_grouped_amd import moe
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    X = torch.randn(70, 64, generator=g, device="cuda").bfloat16()
+    logits = torch.randn(70, 8, generator=g, device="cuda")
+    w = (*moe.quantize_weights(torch.randn(8, 96, 64, generator=g, device="cuda")),
+         *moe.quantize_weights(torch.randn(8, 64, 48, generator=g, device="cuda")))
+    assert torch.equal(drgg.moe_route(logits, 2).weights, drgg.moe_route_scores(logits, 2, drgg.Scoring("softmax")).weights)
+    assert torch.equal(moe.ffn_int8(X, logits, *w, 2), moe.ffn_int8(X, logits, *w, 2, scoring=drgg.Scoring("softmax")))
+    sc = drgg.Scoring(bias=torch.linspace(-1, 1, 8, device="cuda"), scale=2.0)
+    r = drgg.moe_route_scores(logits, 2, sc)
+    q, s = drgg.quantize_int8(X)
+    h = drgg.grouped_gemm_int8(q, s, w[0], w[1], r.group_offsets, gated=True, rows=r.tokens, out_dtype=torch.float32)
+    y = drgg.grouped_gemm_int8(*drgg.quantize_int8(h), w[2], w[3], r.group_offsets)
+    assert torch.equal(moe.ffn_int8(X, logits, *w, 2, scoring=sc), drgg.moe_combine(y, r.positions, r.weights))
