@@ -33,8 +33,8 @@ struct MxRowArgs {   // dequantisation
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_mxfp4_kernel(MxQuantArgs a) {
-    for (int64_t t0 = (int64_t)blockIdx.x * 8; t0 < a.T; t0 += (int64_t)gridDim.x * 8)
-        quantize_mx_piece<BF16>(a, t0 + (threadIdx.x >> 5), blockIdx.y);
+    for (int64_t t0 = (int64_t)blockIdx.y * 8; t0 < a.T; t0 += (int64_t)gridDim.y * 8)
+        quantize_mx_piece<BF16>(a, t0 + (threadIdx.x >> 5), blockIdx.x);
 }
 
 // The values of eight codes: converted with scale 1 and moved by the block's
@@ -43,9 +43,9 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(MxRowArgs a) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     const int l = threadIdx.x & 31;
-    const int64_t kb = blockIdx.y, c = 256 * kb + 8 * l;
+    const int64_t kb = blockIdx.x, c = 256 * kb + 8 * l;
     if (c >= a.K) return;
-    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.x * 8) {
+    for (int64_t t = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); t < a.T; t += (int64_t)gridDim.y * 8) {
         const uint32_t q = reinterpret_cast<const uint32_t*>(a.codes)[(t * a.K + c) / 8];
         const int b = a.scales[(kb * a.T + t) * 8 + (l >> 2)];
         const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0);
@@ -66,10 +66,14 @@ __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(MxRowArgs a) {
     }
 }
 
+// Workgroups of neighbouring columns follow one another, so that those running at
+// once read whole rows (rows first, 131072 BF16 rows of 2048 took 164 instead of
+// 126 us and their values 175 instead of 127).
 dim3 mx_row_grid(int64_t T, int64_t K) {
-    // a launch has fewer than 2^32 threads: blocks walk the rows beyond
+    // a launch has fewer than 2^32 threads and 65536 rows of workgroups: they walk the rows beyond
     const int64_t kb = ceil_div(K, 256), n = ceil_div(T, 8), most = (int64_t(1) << 23) / kb;
-    return dim3((unsigned)(n < most ? n : most), (unsigned)kb);
+    const int64_t y = n < most ? n : most;
+    return dim3((unsigned)kb, (unsigned)(y < 65535 ? y : 65535));
 }
 
 // ---------------------------------------------------------------------------
