@@ -108,6 +108,7 @@ __device__ __forceinline__ u32x2 keep8(u32x4 v, float* scale) {
     return codes;
 }
 
+// 131072 rows of 2 x 768 in 167 us, of 805 MB: 4.8 TB/s; a large copy reaches 5.0.
 __global__ __launch_bounds__(256) void moe_gate_int8_kernel(GateArgs a) {
     const int64_t B = (a.C + 15) / 16;   // scales of a half
     for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < a.R; r0 += (int64_t)gridDim.x * blockDim.y) {
@@ -119,8 +120,10 @@ __global__ __launch_bounds__(256) void moe_gate_int8_kernel(GateArgs a) {
             const bool in = c < a.C;
             u32x4 g = {0, 0, 0, 0}, u = g;
             if (in) {
-                g = static_cast<const u32x4*>(a.src)[p * 2 * a.C + c];
-                u = static_cast<const u32x4*>(a.src)[p * 2 * a.C + a.C + c];
+                // not read again (32768 rows of 2 x 2048: 106 us with plain loads, 90 with
+                // the hint; 131072 rows of 2 x 768: 167 either way)
+                g = __builtin_nontemporal_load(static_cast<const u32x4*>(a.src) + p * 2 * a.C + c);
+                u = __builtin_nontemporal_load(static_cast<const u32x4*>(a.src) + p * 2 * a.C + a.C + c);
             }
             float f[8];
 #pragma unroll
@@ -143,6 +146,7 @@ __global__ __launch_bounds__(256) void moe_gate_int8_kernel(GateArgs a) {
     }
 }
 
+// 131072 rows of 2 x 768 in 203 us, of 1.0 GB: 5.0 TB/s.
 __global__ __launch_bounds__(256) void moe_gate_int8_grad_kernel(GateArgs a) {
     __shared__ float part[16];   // a sum per 16 lanes
     const int64_t B = (a.C + 15) / 16;

@@ -629,20 +629,39 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
     // a wave without tokens does not compete with the others
     const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens + __builtin_amdgcn_readfirstlane(tl);   // the wave's first
     const int rounds = t0 < a.T ? k : 0;
-    uint32_t last = 0;
-    for (int j = 0; j <= rounds; ++j) {
-        if (j == rounds && (rounds == 0 || c.by_logits)) break;
-        uint32_t best, e = 0;
-        if (j < rounds) e = take_best<V>(key, l, &best);
-        else best = best_key<V>(key);
-        if (!c.by_logits && j > 0 && best != 0) close |= near(last, best, (2.f * off + 2.f * kUnit * fabsf(key_value(last))) * 1.01f);
-        last = best;
+    uint32_t kept[S];   // lane j % 16 keeps round j's value in its slot j / 16
+#pragma unroll
+    for (int s = 0; s < S; ++s) kept[s] = 0;
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t best;
+        const uint32_t e = take_best<V>(key, l, &best);
 #pragma unroll
         for (int s = 0; s < S; ++s)
-            if (j == 16 * s + l && j < rounds) mine[s] = (int32_t)e;
+            if (j == 16 * s + l) {
+                kept[s] = best;
+                mine[s] = (int32_t)e;
+            }
+    }
+    if (!c.by_logits) {
+        // each of the chosen and the best of the rest against the one before
+        const uint32_t rest = best_key<V>(key);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int j = 16 * s + l;
+            uint32_t before = row_rotate<1>(kept[s]);   // lane l - 1's
+            if (l == 0) before = 0;
+            if (s > 0) {
+                const uint32_t wrap = row_rotate<1>(kept[s > 0 ? s - 1 : 0]);   // in lane 0 the last slot's lane 15
+                if (l == 0) before = wrap;
+            }
+            const uint32_t it = j < k ? kept[s] : j == k ? rest : 0u;
+            if (before != 0 && it != 0) close |= near(before, it, (2.f * off + 2.f * kUnit * fabsf(key_value(before))) * 1.01f);
+            if (s == S - 1 && k == 16 * S && l == 15 && rest != 0)   // no lane is left for the rest
+                close |= near(kept[s], rest, (2.f * off + 2.f * kUnit * fabsf(key_value(kept[s]))) * 1.01f);
+        }
     }
     // the tokens of this wave that FP32 does not decide
-    unsigned long long undecided = __ballot((close || regroup) && live);
+    unsigned long long undecided = __ballot((close || regroup) && live);   // any lane of a row
     const unsigned long long groups_too = __ballot(regroup);
     while (undecided) {
         const int at = __ffsll((long long)undecided) - 1;   // a lane of the token's row
