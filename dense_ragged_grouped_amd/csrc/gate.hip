@@ -108,7 +108,8 @@ __device__ __forceinline__ u32x2 keep8(u32x4 v, float* scale) {
     return codes;
 }
 
-// 131072 rows of 2 x 768 in 167 us, of 805 MB: 4.8 TB/s; a large copy reaches 5.0.
+// 131072 rows of 2 x 768 in 150 to 167 us, of 812 MB: 5.4 to 4.9 TB/s; a large copy
+// reaches 5.1.
 __global__ __launch_bounds__(256) void moe_gate_int8_kernel(GateArgs a) {
     const int64_t B = (a.C + 15) / 16;   // scales of a half
     for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < a.R; r0 += (int64_t)gridDim.x * blockDim.y) {
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(256) void moe_gate_int8_kernel(GateArgs a) {
     }
 }
 
-// 131072 rows of 2 x 768 in 203 us, of 1.0 GB: 5.0 TB/s.
+// 131072 rows of 2 x 768 in 203 to 217 us, of 1.0 GB: 5.0 to 4.7 TB/s.
 __global__ __launch_bounds__(256) void moe_gate_int8_grad_kernel(GateArgs a) {
     __shared__ float part[16];   // a sum per 16 lanes
     const int64_t B = (a.C + 15) / 16;

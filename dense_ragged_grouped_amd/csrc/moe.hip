@@ -541,7 +541,7 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
             // Groups of 4, 8, .. neighbours: a lane's four keys are of one group,
             // and so are those of size / 4 lanes, or of size / 64 runs.  A lane
             // keeps its runs' groups' values.  (16384 tokens, 4 of 8 groups of 32:
-            // the way below 24 us more than without groups.)
+            // 4 us more than a bias alone; the way below took 20 more.)
             uint32_t one[V / 4], two[V / 4];
             const int shift = __builtin_ctz(size);
 #pragma unroll
@@ -719,10 +719,10 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
 // threads: with 1024 a lane has 128 registers, with 512 256, and 64 keys do not
 // fit them beside the rest.
 //
-// 16384 tokens, k = 8 of 256 experts, graph replays: 14 us without groups and
-// bias (moe_select_kernel 12), 20 with a bias, 25 with 4 of 8 groups; of the last
-// two 3 and 5 us are the 13 tokens or so of these that are chosen again in 64
-// bits, at the end of blocks that the others wait for.
+// 16384 tokens, k = 8 of 256 experts: 13 us without groups and bias
+// (moe_select_kernel 12), 18 with a bias, 22 with 4 of 8 groups; of the last two 3
+// to 5 us are the 13 tokens or so of these that are chosen again in 64 bits, at
+// the end of blocks that the others wait for.
 template <int V, int S, int THREADS, bool SIGMOID>
 __global__ __launch_bounds__(THREADS) void moe_select_scores_kernel(RouteArgs a, ScoreArgs c, MxQuantArgs quant) {
     if (blockIdx.x >= a.blocks) {   // the rows' quantisation, half a wave per row and 256 columns

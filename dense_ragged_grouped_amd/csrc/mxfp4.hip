@@ -91,6 +91,9 @@ dim3 mx_row_grid(int64_t T, int64_t K) {
 // bytes of a piece are one load; the lane's two of them are permuted into bytes
 // 0 and 1, which the two steps' MFMAs select.  Rows and columns outside the
 // operands carry an out-of-range offset and read as zero.
+//
+// One row through 4096x4096 takes 5.0 us (8.9 MB, 1.8 us at the rate of a copy):
+// latency.  32 rows on 32 experts of 1536x2048 10.5 us (about 33 MB, 6.6 us).
 
 // What a product leaves: FP32 or BF16 values, or (gated) codes and scales, those
 // of quantize_mxfp4 on the FP32 values, so that the next product's operand is made
@@ -301,8 +304,8 @@ hipError_t launch_mx_rows(const MxArgs& a, bool bf16, hipStream_t s) {
 // 4 + q.  The blocks a lane sees in a pair are then neighbours, and their four
 // scale bytes one aligned dword, which the four sub-steps' MFMAs select from by an
 // immediate: no instruction handles a scale but the LDS read.  (In the order of
-// the 8-bit product the scales of a stage had to be permuted into place, and the
-// wait for them stood among the MFMAs: 8192x8192x8192 259 to 273 us.)  The scales
+// the 8-bit product the scales of a stage had to be permuted into place: on one
+// card 299 to 309 us for 8192x8192x8192, 295 to 298 in this one.)  The scales
 // of a pair (eight bytes a row) are loaded beside its codes and land behind them
 // in its buffer.  A pair of stages lands as one, so that the upper half may read
 // ahead of the stage.
@@ -512,6 +515,16 @@ __device__ __forceinline__ void store_tile_mx(Value value, int rb, const MxArgs&
 }
 
 // The 8-bit product's walk and epilogue without scales of whole rows.
+//
+// 131072x1536x2048 in 8 groups, BF16 out: 250 to 265 us (3.3 to 3.1 PFLOP/s);
+// 8192x8192x8192 264 us (4.2; a large library product of the same operands 3.1),
+// 16384 cubed 2070 us (4.25; 3.4).  A 256x256 tile takes 0.77 to 0.92 us per step
+// of 64 bytes, more on slower cards and on codes that toggle more bits: the clock
+// is the power limit's (1.79 GHz; on zeros 8192 cubed takes 204 us), the matrix
+// pipe busy 54 % of the time.  About 6 us are a tile's epilogue and switch, 30 % at
+// K = 2048.  Measured and not taken: 4 waves of 128x128 each (295 us against 282 at
+// 8192 cubed), stores without the non-temporal hint (302 against 277 to 285), and
+// waiting for a tile's stores only inside the next tile's main loop (no change).
 template <int BM, int BN, MxOut OUT, bool GATED, bool GATHERED, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, BM == 128 && BN == 128 ? 2 : 1) void mx_tile_kernel(MxArgs a) {
     DRGG_MX_STAGES(BM, BN, stg);
