@@ -1,7 +1,7 @@
 // engine.hpp -- the tile engine of the gfx950 matrix-product kernels
-// (kernels.hip: BF16; int8.hip: 8-bit integers): ragged schedules, operand
-// staging, the MFMA main loop and the staged epilogue.  Included by kernel
-// files only.
+// (kernels.hip: BF16; int8.hip: 8-bit integers; mxfp4.hip: microscaled 4-bit
+// floating point): ragged schedules, operand staging, the MFMA main loop and the
+// staged epilogue.  Included by kernel files only.
 #pragma once
 
 #include <hip/hip_runtime.h>
