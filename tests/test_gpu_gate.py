@@ -283,6 +283,29 @@ def test_only_some_gradients(drgg):
             assert torch.equal(one, full[i])
 
 
+def test_blocks_without_tokens(drgg):
+    """No tokens: empty results and zero gradients of the weights, from every block that selects by scores."""
+    from dense_ragged_grouped_amd import moe
+    E, H, I, k = 4, 64, 32, 2
+    sc = drgg.Scoring(bias=torch.zeros(E, device="cuda"), groups=2, top_groups=1)
+    X = torch.zeros(0, H, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    logits = torch.zeros(0, E, device="cuda", requires_grad=True)
+    W1 = torch.ones(E, 2 * I, H, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    W2 = torch.ones(E, H, I, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    for kept in ("int8", None):
+        out = moe.ffn(X, logits, W1, W2, k, scoring=sc, kept=kept)
+        assert out.shape == (0, H)
+        grads = torch.autograd.grad(out.float().sum(), (X, logits, W1, W2))
+        assert [g.shape for g in grads] == [x.shape for x in (X, logits, W1, W2)]
+        assert not grads[2].any() and not grads[3].any()
+    w1, w2 = W1.detach(), W2.detach()
+    for scoring in (sc, None):
+        assert moe.ffn_int8(X.detach(), logits.detach(), *moe.quantize_weights(w1), *moe.quantize_weights(w2), k,
+                            scoring=scoring).shape == (0, H)
+        assert moe.ffn_mxfp4(X.detach(), logits.detach(), *moe.quantize_weights_mxfp4(w1), *moe.quantize_weights_mxfp4(w2), k,
+                             scoring=scoring).shape == (0, H)
+
+
 def test_second_derivative_raises(drgg):
     from dense_ragged_grouped_amd import moe
     X, logits, W1, W2 = block(10, 4, 64, 64)
