@@ -968,17 +968,42 @@ __global__ __launch_bounds__(256) void moe_route_grad_kernel(RouteGradArgs a) {
 //   sigmoid:  w_j (1 - s_j) (dw_j - r), without the r where the weights are not
 //             renormalised;  1 - s = sigmoid(-x)
 //   softmax:  as above, with r for s
+// Renormalised weights add up to the scale, so that dw_j - r stays what it is when
+// the same is taken from every dw.  With the heaviest expert's taken, r is the sum
+// over the others alone: exactly 0 where only one is chosen (dw - (scale dw) / scale
+// is not: at scale 2.5 it is off by up to 2^-23 of dw for an eighth of the tokens),
+// and where one has nearly all the weight the small difference keeps its digits.
+// Weights that a caller has changed may have another sum: for those the formula as
+// it stands.  The selection's sum is within 18 half steps of the scale (its sum of
+// scores and this one 8 each, quotient and factor one each); 64 are let pass.
 template <int V>
 __global__ __launch_bounds__(256) void moe_route_scores_grad_kernel(RouteGradArgs a, int sigmoid, float scale) {
     const int l = threadIdx.x & 15;
     const int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int E = a.E, k = a.k;
     const bool live = t < a.T;
+    float base = 0.f;   // what is taken from every dw
+    if (a.renormalize) {
+        uint32_t heaviest = 0;   // weights are not negative: their bits are ordered as they are
+        float its = 0.f, sum = 0.f;
+        if (live)
+            for (int j = l; j < k; j += 16) {
+                const float w = a.weights[t * k + j];
+                sum += w;
+                if (__float_as_uint(w) > heaviest) {
+                    heaviest = __float_as_uint(w);
+                    its = a.dweights[t * k + j];
+                }
+            }
+        const bool mine = row_min(heaviest == row_max(heaviest) ? l : 16u) == (uint32_t)l;   // the first lane that has it
+        const uint32_t bits = row_max(mine ? __float_as_uint(its) : 0u);
+        if (fabsf(row_sum(sum) - scale) <= 64 * kUnit * scale) base = __uint_as_float(bits);
+    }
     float r = 0.f;
     if (live && !(sigmoid && !a.renormalize))
         for (int j = l; j < k; j += 16) {
             const float w = a.weights[t * k + j];
-            r += w != 0.f ? w * a.dweights[t * k + j] : 0.f;
+            r += w != 0.f ? w * (a.dweights[t * k + j] - base) : 0.f;
         }
     r = row_sum(r);
     float g[V];
@@ -1024,7 +1049,7 @@ __global__ __launch_bounds__(256) void moe_route_scores_grad_kernel(RouteGradArg
             const float w = a.weights[t * k + j];
             if (e >= 0 && e < E && w != 0.f) {   // of weight 0: as if not chosen
                 const float by = sigmoid ? score<true, float>(-a.logits[t * E + e], 0.f, 1.f) : 1.f;
-                out[e] = w * by * (a.dweights[t * k + j] - r);
+                out[e] = w * by * (a.dweights[t * k + j] - base - r);
             }
         }
 }

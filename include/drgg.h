@@ -656,7 +656,8 @@ drgg_status moe_route_scores(const float *logits, int64_t T, int32_t E, int32_t 
  *   softmax, renormalize != 0:  w_j (dw_j - r)            at the chosen, else 0
  *   softmax:                    s_e (scale dw_e - scale r), dw_e = 0 but at the chosen
  * Only score, renormalize and scale of `scoring` are used.  A chosen expert of
- * weight 0 counts as not chosen, and its dweights are not used.
+ * weight 0 counts as not chosen, and its dweights are not used.  Renormalised
+ * weights of one expert do not depend on the logits: their gradient is exactly 0.
  */
 drgg_status moe_route_scores_grad(const float *dweights, const float *logits, const int32_t *experts,
                                   const float *weights, int64_t T, int32_t E, int32_t k,
