@@ -535,36 +535,54 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
     bool regroup = false;
     if (c.groups > 1) {
         const int size = E / c.groups;
+        // A margin that holds for every group: values are sums of at most two v, each
+        // below 1 + far.  Biases far from the scores (a finite mask, of experts that
+        // nobody chooses) make it too wide; what lies within it is then compared by
+        // each group's own error.  (16384 tokens, 4 of 8 groups of 32, one bias of
+        // -1e9: 28 us; by the wide margin alone all tokens were chosen again, 86.)
         const float within = (4.f * off + 8.f * kUnit * (1.f + far)) * 1.01f;
+        float kept = INFINITY, others = -INFINITY;   // the least of the kept, the most of the others, by their errors
+        auto take_error = [&](uint32_t one, uint32_t two, bool in) {
+            const float v = key_value(group_key(one, two, c.best));
+            const float a = fabsf(key_value(one)), b = c.best == 2 && two != 0 ? fabsf(key_value(two)) : 0.f;
+            // two values, each within off and a rounding, the rounding of their sum and of these
+            const float m = fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f);
+            const float error = (2.f * off + 6.f * kUnit * m) * 1.01f;
+            if (one != 0 && in) kept = fminf(kept, v - error);
+            if (one != 0 && !in) others = fmaxf(others, v + error);
+        };
         uint32_t last = 0, left;
         if (size >= 4 && (size & (size - 1)) == 0) {
             // Groups of 4, 8, .. neighbours: a lane's four keys are of one group,
             // and so are those of size / 4 lanes, or of size / 64 runs.  A lane
             // keeps its runs' groups' values.  (16384 tokens, 4 of 8 groups of 32:
             // 4 us more than a bias alone; the way below took 20 more.)
-            uint32_t one[V / 4], two[V / 4];
             const int shift = __builtin_ctz(size);
+            auto largest = [&](uint32_t (&one)[V / 4], uint32_t (&two)[V / 4]) {
 #pragma unroll
-            for (int q = 0; q < V / 4; ++q) {
-                one[q] = max(key[4 * q], key[4 * q + 1]);
-                two[q] = min(key[4 * q], key[4 * q + 1]);
-                merge_two(one[q], two[q], max(key[4 * q + 2], key[4 * q + 3]), min(key[4 * q + 2], key[4 * q + 3]));
-                if (size >= 8) merge_lanes<0xB1>(one[q], two[q]);     // lane l ^ 1
-                if (size >= 16) merge_lanes<0x4E>(one[q], two[q]);    // l ^ 2
-                if (size >= 32) merge_lanes<0x141>(one[q], two[q]);   // 7 - l of 8: the other quad
-                if (size >= 64) merge_lanes<0x140>(one[q], two[q]);   // 15 - l: the other eight
-            }
-#pragma unroll
-            for (int d = 1; d < V / 4; d *= 2)
-                if (64 * d < size) {
-#pragma unroll
-                    for (int q = 0; q < V / 4; ++q)
-                        if (!(q & d)) {
-                            merge_two(one[q], two[q], one[q + d], two[q + d]);
-                            one[q + d] = one[q];
-                            two[q + d] = two[q];
-                        }
+                for (int q = 0; q < V / 4; ++q) {
+                    one[q] = max(key[4 * q], key[4 * q + 1]);
+                    two[q] = min(key[4 * q], key[4 * q + 1]);
+                    merge_two(one[q], two[q], max(key[4 * q + 2], key[4 * q + 3]), min(key[4 * q + 2], key[4 * q + 3]));
+                    if (size >= 8) merge_lanes<0xB1>(one[q], two[q]);     // lane l ^ 1
+                    if (size >= 16) merge_lanes<0x4E>(one[q], two[q]);    // l ^ 2
+                    if (size >= 32) merge_lanes<0x141>(one[q], two[q]);   // 7 - l of 8: the other quad
+                    if (size >= 64) merge_lanes<0x140>(one[q], two[q]);   // 15 - l: the other eight
                 }
+#pragma unroll
+                for (int d = 1; d < V / 4; d *= 2)
+                    if (64 * d < size) {
+#pragma unroll
+                        for (int q = 0; q < V / 4; ++q)
+                            if (!(q & d)) {
+                                merge_two(one[q], two[q], one[q + d], two[q + d]);
+                                one[q + d] = one[q];
+                                two[q + d] = two[q];
+                            }
+                    }
+            };
+            uint32_t one[V / 4], two[V / 4];
+            largest(one, two);
 #pragma unroll
             for (int q = 0; q < V / 4; ++q) one[q] = group_key(one[q], two[q], c.best);
             auto best_left = [&]() {
@@ -584,6 +602,13 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
                 open |= 1ull << (at & 63);
             }
             left = best_left();
+            regroup = left != 0 && near(last, left, within);
+            if (regroup && far > 1.f) {
+                largest(one, two);
+#pragma unroll
+                for (int q = 0; q < V / 4; ++q) take_error(one[q], two[q], open >> (((64 * q + 4 * l) >> shift) & 63) & 1);
+                regroup = row_max(order_key(others)) >= row_min(order_key(kept));
+            }
 #pragma unroll
             for (int q = 0; q < V / 4; ++q) {
                 const bool in = open >> (((64 * q + 4 * l) >> shift) & 63) & 1;
@@ -592,17 +617,17 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
             }
         } else {
             // the sixteen lanes take the groups in turn, their values made again
-            uint32_t rank[4];
+            uint32_t one[4], two[4], rank[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int g = 16 * q + l;
-                uint32_t one = 0, two = 0;
+                one[q] = two[q] = 0;
                 if (live && g < c.groups)
                     for (int e = g * size; e < (g + 1) * size; ++e) {
                         const uint32_t v = order_key(score_value32<SIGMOID>(row[e], bias[e], most, inverse));
-                        merge_two(one, two, v, 0);
+                        merge_two(one[q], two[q], v, 0);
                     }
-                rank[q] = group_key(one, two, c.best);
+                rank[q] = group_key(one[q], two[q], c.best);
             }
             for (int j = 0; j < c.top_groups; ++j) {
                 last = row_max(max(max(rank[0], rank[1]), max(rank[2], rank[3])));
@@ -615,6 +640,12 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
                 open |= 1ull << (at & 63);
             }
             left = row_max(max(max(rank[0], rank[1]), max(rank[2], rank[3])));
+            regroup = left != 0 && near(last, left, within);
+            if (regroup && far > 1.f) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) take_error(one[q], two[q], open >> (16 * q + l) & 1);
+                regroup = row_max(order_key(others)) >= row_min(order_key(kept));
+            }
             // e / size for e < 1024 by a multiplication
             const uint32_t by_size = ((1u << 20) + size - 1) / size;
 #pragma unroll
@@ -623,8 +654,8 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
                 key[i] = open >> ((e * by_size) >> 20 & 63) & 1 ? key[i] : 0u;
             }
         }
-        // (sums of biases beyond 2^126 may leave FP32's range)
-        regroup = left != 0 && (near(last, left, within) || far > 0x1p126f);
+        // sums beyond 2^126 may have left FP32's range
+        regroup |= left != 0 && far > 0x1p126f && !(fabsf(key_value(last)) <= 0x1p126f);
     }
     // a wave without tokens does not compete with the others
     const int64_t t0 = (int64_t)blockIdx.x * kRouteTokens + __builtin_amdgcn_readfirstlane(tl);   // the wave's first
