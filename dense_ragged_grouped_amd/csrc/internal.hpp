@@ -176,7 +176,7 @@ struct MxArgs {
     int32_t E;
     const int32_t* rows = nullptr;   // row r of the product is row rows[r] of X and xs, T rows (null: row r)
     int64_t T = 0;
-    uint8_t* out_scales = nullptr;   // gated: out are codes [M,N/4], with these scales (null: values)
+    uint8_t* out_scales = nullptr;   // gated with rows: out are codes [M,N/4], with these scales (null: values)
 };
 hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s);
 

@@ -280,7 +280,7 @@ hipError_t launch_mx_rows(const MxArgs& a, bool bf16, hipStream_t s) {
     timing_mark("mx_rows_kernel", s);
     auto launch = [&](auto gathered) {
         constexpr bool G = decltype(gathered)::value;
-        if constexpr (GATED && NB == 4)
+        if constexpr (GATED && G && NB == 4)
             if (a.out_scales) {
                 hipLaunchKernelGGL((mx_rows_kernel<kOutMx, GATED, G, NB, W, TOK>), grid, block, 0, s, a);
                 return;
@@ -591,7 +591,7 @@ template <int BM, int BN, int WAVES, bool GATED, bool GATHERED>
 void launch_mx_tile_t(const MxArgs& a, bool bf16, dim3 grid, hipStream_t s) {
     const dim3 block(64 * WAVES);
     constexpr bool kBf16 = !GATED || BN >= 256;   // a gated 128x128 tile has 32 columns per wave, half a BF16 line
-    if constexpr (GATED)
+    if constexpr (GATED && GATHERED)
         if (a.out_scales) {
             hipLaunchKernelGGL((mx_tile_kernel<BM, BN, kOutMx, GATED, GATHERED, WAVES>), grid, block, 0, s, a);
             return;
@@ -649,6 +649,7 @@ hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, 
 }
 
 hipError_t launch_mxfp4(const MxArgs& a, bool gated, bool bf16, int cus, int forced_tile, hipStream_t s) {
+    if (a.out_scales && !(gated && a.rows)) return hipErrorInvalidValue;   // codes leave the block's first product alone
     const Int8Program p = mxfp4_program(a.E, a.M, a.N, a.K, gated, bf16, a.out_scales != nullptr, forced_tile);
     if (p.tile == kTileAuto)
         return gated ? launch_mx_program<true>(a, p, bf16, s) : launch_mx_program<false>(a, p, bf16, s);
