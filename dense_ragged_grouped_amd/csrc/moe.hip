@@ -1013,29 +1013,38 @@ __global__ __launch_bounds__(256) void moe_route_scores_grad_kernel(RouteGradArg
     const int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int E = a.E, k = a.k;
     const bool live = t < a.T;
-    float base = 0.f;   // what is taken from every dw
+    // lane l has the chosen l, l + 16, ..
+    float w[4], dw[4];
+    int32_t expert[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool has = live && 16 * i + l < k;
+        const int64_t at = t * k + 16 * i + l;
+        w[i] = has ? a.weights[at] : 0.f;
+        dw[i] = has ? a.dweights[at] : 0.f;
+        expert[i] = has ? a.experts[at] : -1;
+    }
     if (a.renormalize) {
         uint32_t heaviest = 0;   // weights are not negative: their bits are ordered as they are
         float its = 0.f, sum = 0.f;
-        if (live)
-            for (int j = l; j < k; j += 16) {
-                const float w = a.weights[t * k + j];
-                sum += w;
-                if (__float_as_uint(w) > heaviest) {
-                    heaviest = __float_as_uint(w);
-                    its = a.dweights[t * k + j];
-                }
-            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum += w[i];
+            its = __float_as_uint(w[i]) > heaviest ? dw[i] : its;
+            heaviest = max(heaviest, __float_as_uint(w[i]));
+        }
         const bool mine = row_min(heaviest == row_max(heaviest) ? l : 16u) == (uint32_t)l;   // the first lane that has it
-        const uint32_t bits = row_max(mine ? __float_as_uint(its) : 0u);
-        if (fabsf(row_sum(sum) - scale) <= 64 * kUnit * scale) base = __uint_as_float(bits);
+        const float base = __uint_as_float(row_max(mine ? __float_as_uint(its) : 0u));
+        if (fabsf(row_sum(sum) - scale) <= 64 * kUnit * scale) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dw[i] -= base;
+        }
     }
     float r = 0.f;
-    if (live && !(sigmoid && !a.renormalize))
-        for (int j = l; j < k; j += 16) {
-            const float w = a.weights[t * k + j];
-            r += w != 0.f ? w * (a.dweights[t * k + j] - base) : 0.f;
-        }
+    if (!(sigmoid && !a.renormalize)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r += w[i] != 0.f ? w[i] * dw[i] : 0.f;
+    }
     r = row_sum(r);
     float g[V];
     if (a.renormalize || sigmoid) {
@@ -1074,14 +1083,11 @@ __global__ __launch_bounds__(256) void moe_route_scores_grad_kernel(RouteGradArg
         }
     }
     __syncthreads();   // the row's stores are performed before the ones below
-    if (live)
-        for (int j = l; j < k; j += 16) {
-            const int32_t e = a.experts[t * k + j];
-            const float w = a.weights[t * k + j];
-            if (e >= 0 && e < E && w != 0.f) {   // of weight 0: as if not chosen
-                const float by = sigmoid ? score<true, float>(-a.logits[t * E + e], 0.f, 1.f) : 1.f;
-                out[e] = w * by * (a.dweights[t * k + j] - base - r);
-            }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (expert[i] >= 0 && expert[i] < E && w[i] != 0.f) {   // of weight 0: as if not chosen
+            const float by = sigmoid ? score<true, float>(-a.logits[t * E + expert[i]], 0.f, 1.f) : 1.f;
+            out[expert[i]] = w[i] * by * (dw[i] - r);
         }
 }
 
