@@ -80,7 +80,10 @@ drgg_status run_mxfp4(const uint8_t* Xq, const uint8_t* xs, const uint8_t* Wq, c
 
 // The parts of moe_ffn_mxfp4's workspace (byte offsets, multiples of 256).  The
 // experts' outputs y take the place of the codes of X, which are no longer
-// needed by then.
+// needed by then.  They are BF16, as in the 8-bit block: bytes bound their way to
+// memory and back (16384 tokens, k = 8, H 2048: 537 MB each way, about 210 of 570
+// us; FP32 would be twice that).  Their rounding and that of the sum make 0.24 % of
+// the result, that of the sum alone 0.17 %.
 struct MxFfnLayout {
     int64_t experts, weights, offsets, positions, tokens, table, hq, hs, x, xs, y, bytes;
 };

@@ -750,10 +750,14 @@ __device__ __forceinline__ void select_by_scores(const RouteArgs& a, const Score
 // threads: with 1024 a lane has 128 registers, with 512 256, and 64 keys do not
 // fit them beside the rest.
 //
-// 16384 tokens, k = 8 of 256 experts: 13 us without groups and bias
-// (moe_select_kernel 12), 18 with a bias, 22 with 4 of 8 groups; of the last two 3
+// 16384 tokens, k = 8 of 256 experts, normal logits: 13 us without groups and bias
+// (moe_select_kernel 12), 17 with a bias, 20 with 4 of 8 groups; of the last two 3
 // to 5 us are the 13 tokens or so of these that are chosen again in 64 bits, at
-// the end of blocks that the others wait for.
+// the end of blocks that the others wait for.  The time depends on the values: equal
+// ones count as undecided, and so do sigmoids that FP32 does not tell apart.  Logits
+// rounded to BF16 take 24 us with a bias, 37 with a bias of zeros or none (a third of
+// the tokens chosen again), logits of standard deviation 8 26 with a bias, and 82
+// without; all logits equal 82.
 template <int V, int S, int THREADS, bool SIGMOID>
 __global__ __launch_bounds__(THREADS) void moe_select_scores_kernel(RouteArgs a, ScoreArgs c, MxQuantArgs quant) {
     if (blockIdx.x >= a.blocks) {   // the rows' quantisation, half a wave per row and 256 columns

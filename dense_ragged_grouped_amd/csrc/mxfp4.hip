@@ -516,7 +516,7 @@ __device__ __forceinline__ void store_tile_mx(Value value, int rb, const MxArgs&
 
 // The 8-bit product's walk and epilogue without scales of whole rows.
 //
-// 131072x1536x2048 in 8 groups, BF16 out: 250 to 265 us (3.3 to 3.1 PFLOP/s);
+// 131072x1536x2048 in 8 groups, BF16 out: 248 to 277 us (3.3 to 3.0 PFLOP/s);
 // 8192x8192x8192 264 us (4.2; a large library product of the same operands 3.1),
 // 16384 cubed 2070 us (4.25; 3.4).  A 256x256 tile takes 0.77 to 0.92 us per step
 // of 64 bytes, more on slower cards and on codes that toggle more bits: the clock

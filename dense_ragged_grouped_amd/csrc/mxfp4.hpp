@@ -71,9 +71,10 @@ __device__ __forceinline__ void load8(float (&f)[8], const void* X, int64_t i) {
 // row of 16 lanes that holds them.  Called by whole waves; a row past the last
 // writes nothing.
 //
-// Bound by memory: 49152 FP32 rows of 2048 (456 MB, not in the last-level cache)
-// in 78 us, 131072 BF16 rows (680 MB) in 126 us: 5.8 and 5.4 TB/s, a large copy
-// reaches 5.0.
+// Bound by memory: 49152 FP32 rows of 2048 (456 MB) in 88 us where other kernels'
+// data lie between two calls (75 with the same rows again, part of them in the
+// last-level cache), 131072 BF16 rows (680 MB) in 118 to 131 us: 5.2 and 5.2 to 5.8
+// TB/s, a large copy reaches 5.0.
 template <bool BF16>
 __device__ __forceinline__ void quantize_mx_piece(const MxQuantArgs& a, int64_t t, int64_t kb) {
     const int l = threadIdx.x & 31;

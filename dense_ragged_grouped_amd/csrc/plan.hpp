@@ -574,15 +574,18 @@ inline Int8Program int8_program(int64_t E, int64_t M, int64_t N, int64_t K, bool
 
 // The same for a 4-bit product (rows of K/2 bytes, s of them in steps of 64),
 // with its own bounds, from two sweeps of 560 random sizes (E 1 to 128, M 8 to
-// 40000, N 768 to 4096, K 512 to 4096, even and skewed groups).  A round of tiles
-// takes about
+// 40000, N 768 to 4096, K 512 to 4096, even and skewed groups; BF16 results, FP32
+// ones of half the columns where gated).  A round of tiles takes about
 //   256x256  6.4 + 0.77 s    128x256  4.4 + 0.56 s    128x128  3.15 + 0.655 s,
 // 128x128 tiles that have a CU each 2.55 + 0.286 s.  With these, margins of 5 % for
 // the smaller tiles, and 128x128 up to 128 rows a group, the tile taken is 0.4 and
 // 0.7 % slower than the best of the three in the geometric mean of either sweep
 // (int8_tile's bounds: 0.9 and 1.1 %; E = 32, 4548x2544x512 then takes 21.8 us, in
-// 128x128 15.8).  128x128 tiles have room for kMx128MaxExperts groups beside the
-// scales, two of them on a CU.
+// 128x128 15.8).  Ungated FP32 results were not swept and go by the same bounds, which
+// leave out their stores: E = 32, 16411x2048x768, a round of 67 MB, takes 52 to 62 us
+// in the 256x256 tiles that are taken, 51 in 128x256 and 47 in 128x128 (BF16 36, 40
+// and 39).  128x128 tiles have room for kMx128MaxExperts groups beside the scales, two
+// of them on a CU.
 //
 // Many experts' weights are read at memory speed by the few-row blocks up to 10
 // rows a group (E = 32, 246x4096x1056: 23.1 us, 128x128 tiles 24.2); beyond, several
